@@ -74,7 +74,9 @@ typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
 typedef enum pkv_cache_kind {
     PKV_CACHE_F16 = 0,   /* K and V stored as fp16 */
     PKV_CACHE_BF16 = 1,  /* K and V stored as bf16 */
-    PKV_CACHE_K8V4 = 2   /* K int8 symmetric, V 4-bit asymmetric (see below) */
+    PKV_CACHE_K8V4 = 2,  /* K int8 symmetric, V 4-bit asymmetric (see below) */
+    PKV_CACHE_I8 = 3,    /* K and V int8, one fp32 scale per (block, kv head) */
+    PKV_CACHE_E4M3 = 4   /* K and V fp8 e4m3, one fp32 scale per (block, kv head) */
 } pkv_cache_kind;
 
 /*
@@ -94,6 +96,13 @@ typedef enum pkv_cache_kind {
  *   v_scale   fp16  [num_blocks, num_kv_heads, 16, G]          one per (token, kv head, group)
  *   v_zero    fp16  [num_blocks, num_kv_heads, 16, G]
  *   Dequantised values: k = code * k_scale;  v = code * v_scale + v_zero.
+ * PKV_CACHE_I8 / PKV_CACHE_E4M3 (this library's own formats: half the fp16
+ *   cache's bytes, and a scale that costs 8 bytes per block and kv head):
+ *   k, v            int8 in [-127, 127], or fp8 e4m3 (finite: 0x7f and 0xff are
+ *                   not numbers here)  [num_blocks, 16, num_kv_heads, head_dim]
+ *   k_scale, v_scale  fp32 [num_blocks, num_kv_heads]; v_zero, v_group unused
+ *   Dequantised values: code * scale.  Attention and gather take any finite
+ *   scale; pkv_quantize_kv_blocks writes its own grid of them.
  */
 typedef struct pkv_cache {
     int32_t kind;          /* pkv_cache_kind */
@@ -170,18 +179,47 @@ pkv_status pkv_quantize_kv(const pkv_cache *cache, const void *k_new, const void
                            uint32_t *err_flags, pkv_stream_t stream);
 
 /*
+ * Append new tokens to a PKV_CACHE_I8 or PKV_CACHE_E4M3 cache.  A block's scale
+ * covers all its tokens, so the call is by sequence and position, not by slot:
+ * the n_s new tokens of sequence s are its last ones, positions
+ * [context_lens[s] - n_s, context_lens[s]).
+ *   k_new, v_new  [num_tokens, num_kv_heads, head_dim], src_dtype PKV_F16 or PKV_BF16.
+ *   cu_new_lens   int32 [num_seqs + 1] device: sequence s's rows are cu[s] ..
+ *                 cu[s+1] - 1 (n_s may be 0; cu[num_seqs] <= num_tokens), or NULL:
+ *                 seqs->q_len rows each, and num_tokens = num_seqs * q_len.
+ * For each touched block, kv head and K or V apart (fp32, round half to even):
+ *   t = max|new| / qmax (IEEE division; qmax 127 for I8, 448 for E4M3)
+ *   need = t rounded up to three significant bits (I8) or to a power of two (E4M3)
+ *   s = need if the first new token opens the block, else max(the block's scale, need);
+ *       older rows, if the scale grew: code = round(code * (s_old / s))
+ *   new rows: code = round(x * (1 / s)); s = 0 (all zero): code 0
+ * so codes and scales are reproducible bit for bit.  Rows behind the last new
+ * token keep their bytes, and so does every block the call does not touch.  A
+ * sequence with context_lens[s] <= 0 is padding and is skipped; new rows before
+ * position 0 are skipped; positions past the block table are skipped and flag
+ * PKV_DEVERR_CAPACITY; a block id out of range flags PKV_DEVERR_OOB_BLOCK and its
+ * tokens are skipped.  Inputs must be finite, else the touched blocks' codes and
+ * scales are unspecified.  No two sequences of one call may append to the same
+ * block (shared prefix blocks are complete, so they never do): its contents
+ * would be unspecified.
+ */
+pkv_status pkv_quantize_kv_blocks(const pkv_cache *cache, const void *k_new, const void *v_new,
+                                  pkv_dtype src_dtype, int32_t num_tokens, const int32_t *cu_new_lens,
+                                  const pkv_seqs *seqs, uint32_t *err_flags, pkv_stream_t stream);
+
+/*
  * Single-pass paged decode attention [METAL: the pagedattention kernel, the GQA
  * stride trick kv_head = q_head / gqa_factor; MTPLX-2 §"Kernel Interface and
  * Memory Slicing": only the stored tokens are read].
  *   out  [num_seqs*q_len, num_heads, head_dim], out_dtype PKV_F16, PKV_BF16 or PKV_F32.
  *   q    [num_seqs*q_len, num_heads, head_dim], q_dtype PKV_F16 or PKV_BF16; for
- *        fp16/bf16 caches q_dtype must equal the cache dtype; K8V4 takes either.
+ *        fp16/bf16 caches q_dtype must equal the cache dtype; the others take either.
  *   scale  multiplies q.k before the softmax (usually 1/sqrt(head_dim)).
  * out[r, h] = sum_t softmax_t(scale * q[r,h] . K[t, h/g]) V[t, h/g] over the
  * visible tokens of row r; a row with no visible token gets zeros.
  * Each (sequence, kv head) is handled whole by one CTA, which serves all g
  * query heads of the group, so each KV block is read from HBM once per step.
- * q_len > 1 (and the K8V4 cache) requires g * q_len <= 16.
+ * q_len > 1 (and the K8V4, I8 and E4M3 caches) requires g * q_len <= 16.
  */
 pkv_status pkv_paged_attention(void *out, pkv_dtype out_dtype, const void *q, pkv_dtype q_dtype,
                                int32_t num_heads, float scale, const pkv_cache *cache,
@@ -273,6 +311,8 @@ pkv_status pkv_paged_attention_balanced(void *out, pkv_dtype out_dtype, const vo
  * written into the cache buffer in place]; the pages print no fused call.
  *   k_new, v_new   [num_tokens, num_kv_heads, head_dim] of src_dtype (the cache
  *                  dtype for fp16/bf16 caches; PKV_F16 or PKV_BF16 for K8V4).
+ *   I8 and E4M3 caches are PKV_ERR_UNSUPPORTED (a new token may change the scale
+ *   of a block that other CTAs are reading): call pkv_quantize_kv_blocks first.
  *   slot_mapping   int64 [num_tokens]; < 0 skips the token.
  *   Token s*q_len + j (j < q_len) is draft j of sequence s.  When its slot is
  *   the slot of position context_lens[s] - q_len + j, the attention takes that
@@ -426,9 +466,9 @@ pkv_status pkv_gather_kv_cache(void *k_out, void *v_out, const int32_t *cu_seq_l
                                pkv_stream_t stream);
 
 /*
- * Dequantising gather of a PKV_CACHE_K8V4 cache: every visible token of every
- * sequence to contiguous fp16 / bf16 rows, k = code * k_scale and
- * v = code * v_scale + v_zero [METAL §"The K/V asymmetry"; MTPLX-2
+ * Dequantising gather of a PKV_CACHE_K8V4, PKV_CACHE_I8 or PKV_CACHE_E4M3 cache:
+ * every visible token of every sequence to contiguous fp16 / bf16 rows,
+ * k = code * k_scale and v = code * v_scale (+ v_zero for K8V4) [METAL §"The K/V asymmetry"; MTPLX-2
  * §"Quantization-Aware Memory Layout"], with the gather of pkv_gather_kv_cache.
  *   out_dtype    PKV_F16 or PKV_BF16.
  *   cu_seq_lens  int32 [num_seqs + 1] device, as for pkv_gather_kv_cache.
@@ -436,7 +476,7 @@ pkv_status pkv_gather_kv_cache(void *k_out, void *v_out, const int32_t *cu_seq_l
  *                16-byte aligned.
  * Each value is formed in fp32 with one rounding (the K product is exact; V is
  * one fused multiply-add) and rounded to out_dtype to nearest even.  Errors as
- * for pkv_gather_kv_cache; a non-K8V4 cache is PKV_ERR_INVALID_ARG.
+ * for pkv_gather_kv_cache; an fp16 or bf16 cache is PKV_ERR_INVALID_ARG.
  */
 pkv_status pkv_gather_kv_cache_dequant(void *k_out, void *v_out, pkv_dtype out_dtype, const int32_t *cu_seq_lens,
                                        const pkv_cache *cache, const pkv_seqs *seqs, uint32_t *err_flags,

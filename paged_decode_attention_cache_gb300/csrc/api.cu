@@ -58,9 +58,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 pkv_status check_cache(const pkv_cache* c, bool need_half) {
     if (!c) return fail(PKV_ERR_INVALID_ARG, "cache is NULL");
-    if (c->kind != PKV_CACHE_F16 && c->kind != PKV_CACHE_BF16 && c->kind != PKV_CACHE_K8V4)
+    if (c->kind != PKV_CACHE_F16 && c->kind != PKV_CACHE_BF16 && c->kind != PKV_CACHE_K8V4 &&
+        !pkv::is_byte_cache(c->kind))
         return fail(PKV_ERR_INVALID_ARG, "unknown cache kind %d", c->kind);
-    if (need_half && c->kind == PKV_CACHE_K8V4)
+    if (need_half && c->kind != PKV_CACHE_F16 && c->kind != PKV_CACHE_BF16)
         return fail(PKV_ERR_INVALID_ARG, "this call needs an fp16 or bf16 cache");
     if (c->block_size != 16) return fail(PKV_ERR_UNSUPPORTED, "block_size %d (only 16)", c->block_size);
     if (c->head_dim != 64 && c->head_dim != 128)
@@ -76,6 +77,10 @@ pkv_status check_cache(const pkv_cache* c, bool need_half) {
         CHECK_PTR(c->k_scale, "cache->k_scale");
         CHECK_PTR(c->v_scale, "cache->v_scale");
         CHECK_PTR(c->v_zero, "cache->v_zero");
+    }
+    if (pkv::is_byte_cache(c->kind)) {
+        CHECK_PTR(c->k_scale, "cache->k_scale");
+        CHECK_PTR(c->v_scale, "cache->v_scale");
     }
     return PKV_OK;
 }
@@ -156,15 +161,16 @@ CUtensorMapSwizzle swizzle_for(int row_bytes) {
 // CUDA-core kernel: one box per tile (16 rows x one kv head), no swizzle.
 // Tensor-core kernel: swizzled rows of at most 128 bytes, so that the ldmatrix /
 // 128-bit reads of a tile are conflict-free (fp16/bf16: 64-dim chunks with the
-// 128B swizzle, one 3-D box; K8: the whole D-byte row; V4: the whole D/2-byte row).
+// 128B swizzle, one 3-D box; 8-bit codes: the whole D-byte row; V4: the whole D/2-byte row).
 pkv_status cache_maps(const pkv_cache* c, CUtensorMap* km, CUtensorMap* vm, bool tc) {
     const int64_t rows = int64_t(c->num_blocks) * 16;
     const int D = c->head_dim, H = c->num_kv_heads;
     pkv_status st;
-    if (c->kind == PKV_CACHE_K8V4) {
+    if (c->kind == PKV_CACHE_K8V4 || pkv::is_byte_cache(c->kind)) {
+        const int DV = c->kind == PKV_CACHE_K8V4 ? D / 2 : D;   // bytes of a V row
         st = tile_map(km, c->k, rows, int64_t(H) * D, D, swizzle_for(D));
         if (st != PKV_OK) return st;
-        return tile_map(vm, c->v, rows, int64_t(H) * D / 2, D / 2, swizzle_for(D / 2));
+        return tile_map(vm, c->v, rows, int64_t(H) * DV, DV, swizzle_for(DV));
     }
     if (tc) {
         st = chunk_map(km, c->k, rows, int64_t(H) * D * 2, D);
@@ -190,7 +196,7 @@ pkv_status attn_setup(pkv::AttnParams* p, const void* q, pkv_dtype q_dtype, int3
     if ((st = check_seqs(seqs)) != PKV_OK) return st;
     CHECK_PTR(q, "q");
     if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return fail(PKV_ERR_INVALID_ARG, "q_dtype %d", q_dtype);
-    if (cache->kind != PKV_CACHE_K8V4 && q_dtype != cache_dtype(cache))
+    if ((cache->kind == PKV_CACHE_F16 || cache->kind == PKV_CACHE_BF16) && q_dtype != cache_dtype(cache))
         return fail(PKV_ERR_INVALID_ARG, "q_dtype must match the fp16/bf16 cache dtype");
     if (num_heads < 1 || num_heads % cache->num_kv_heads != 0)
         return fail(PKV_ERR_INVALID_ARG, "num_heads %d is not a multiple of num_kv_heads %d", num_heads,
@@ -300,6 +306,45 @@ pkv_status pkv_quantize_kv(const pkv_cache* cache, const void* k_new, const void
     p.v_zero = cache->v_zero;
     p.src_dtype = src_dtype;
     return cuda_result(pkv::launch_quantize_kv(p, reinterpret_cast<cudaStream_t>(stream)), "quantize_kv launch");
+}
+
+pkv_status pkv_quantize_kv_blocks(const pkv_cache* cache, const void* k_new, const void* v_new, pkv_dtype src_dtype,
+                                  int32_t num_tokens, const int32_t* cu_new_lens, const pkv_seqs* seqs,
+                                  uint32_t* err_flags, pkv_stream_t stream) {
+    pkv_status st = check_cache(cache, false);
+    if (st != PKV_OK) return st;
+    if (!pkv::is_byte_cache(cache->kind))
+        return fail(PKV_ERR_INVALID_ARG, "quantize_kv_blocks needs an I8 or E4M3 cache");
+    if (src_dtype != PKV_F16 && src_dtype != PKV_BF16) return fail(PKV_ERR_INVALID_ARG, "src_dtype %d", src_dtype);
+    if ((st = check_seqs(seqs)) != PKV_OK) return st;
+    if (num_tokens < 0 || num_tokens > INT32_MAX / 2) return fail(PKV_ERR_INVALID_ARG, "num_tokens %d", num_tokens);
+    if (!cu_new_lens && int64_t(seqs->num_seqs) * seqs->q_len != num_tokens)
+        return fail(PKV_ERR_INVALID_ARG, "without cu_new_lens num_tokens (%d) must be num_seqs * q_len (%lld)", num_tokens,
+                    (long long)seqs->num_seqs * seqs->q_len);
+    if (num_tokens == 0 || seqs->num_seqs == 0) return ok();
+    CHECK_PTR(k_new, "k_new");
+    CHECK_PTR(v_new, "v_new");
+    pkv::BlockWriteParams p{};
+    p.k_cache = cache->k;
+    p.v_cache = cache->v;
+    p.k_scale = static_cast<float*>(cache->k_scale);
+    p.v_scale = static_cast<float*>(cache->v_scale);
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.cu_new = cu_new_lens;
+    p.block_tables = seqs->block_tables;
+    p.context_lens = seqs->context_lens;
+    p.num_seqs = seqs->num_seqs;
+    p.max_blocks = seqs->max_blocks_per_seq;
+    p.q_len = seqs->q_len;
+    p.num_tokens = num_tokens;
+    p.num_blocks = cache->num_blocks;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.head_dim = cache->head_dim;
+    p.cache_kind = cache->kind;
+    p.src_dtype = src_dtype;
+    p.err = err_flags;
+    return cuda_result(pkv::launch_append_blocks(p, reinterpret_cast<cudaStream_t>(stream)), "quantize_kv_blocks launch");
 }
 
 pkv_status pkv_paged_attention(void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, int32_t num_heads,
@@ -623,6 +668,8 @@ pkv_status pkv_decode_step_balanced(void* out, pkv_dtype out_dtype, const void* 
     pkv_status st = attn_setup(&p, q, q_dtype, num_heads, scale, cache, seqs, err_flags, &gqa);
     if (st != PKV_OK) return st;
     if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens %d", num_tokens);
+    if (pkv::is_byte_cache(cache->kind))
+        return fail(PKV_ERR_UNSUPPORTED, "no fused step for a cache with block scales: call pkv_quantize_kv_blocks, then the attention");
     if (cache->kind == PKV_CACHE_K8V4) {
         if (src_dtype != PKV_F16 && src_dtype != PKV_BF16) return fail(PKV_ERR_INVALID_ARG, "src_dtype %d", src_dtype);
     } else if (src_dtype != cache_dtype(cache)) {
@@ -851,7 +898,8 @@ pkv_status pkv_gather_kv_cache_dequant(void* k_out, void* v_out, pkv_dtype out_d
                                        pkv_stream_t stream) {
     pkv_status st = check_cache(cache, false);
     if (st != PKV_OK) return st;
-    if (cache->kind != PKV_CACHE_K8V4) return fail(PKV_ERR_INVALID_ARG, "the dequantising gather needs a K8V4 cache");
+    if (cache->kind != PKV_CACHE_K8V4 && !pkv::is_byte_cache(cache->kind))
+        return fail(PKV_ERR_INVALID_ARG, "the dequantising gather needs a quantised cache (K8V4, I8 or E4M3)");
     if (out_dtype != PKV_F16 && out_dtype != PKV_BF16) return fail(PKV_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
     if ((st = check_seqs(seqs)) != PKV_OK) return st;
     if (seqs->num_seqs == 0) return ok();
@@ -876,7 +924,9 @@ pkv_status pkv_gather_kv_cache_dequant(void* k_out, void* v_out, pkv_dtype out_d
     p.num_kv_heads = cache->num_kv_heads;
     p.head_dim = cache->head_dim;
     p.err = err_flags;
-    return cuda_result(pkv::launch_gather_dequant(p, reinterpret_cast<cudaStream_t>(stream)),
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_result(pkv::is_byte_cache(cache->kind) ? pkv::launch_gather_blocks(p, cache->kind, cs)
+                                                       : pkv::launch_gather_dequant(p, cs),
                        "dequantising gather launch");
 }
 

@@ -1,7 +1,8 @@
 // attention.cu -- host side of the attention kernels: which shapes run, the
 // attention-only instantiation of the persistent kernel (attention_impl.cuh)
 // and the balanced workspace size.  The fused decode step's instantiation is
-// in attention_fused.cu, the cascade passes' in attention_cascade.cu.
+// in attention_fused.cu, the cascade passes' in attention_cascade.cu, the 8-bit
+// caches' in attention_byte.cu.
 #include "attention_impl.cuh"
 
 namespace pkv {
@@ -19,11 +20,12 @@ bool attention_supported(int cache_kind, int head_dim, int gqa, int q_len) {
 // streams at ~42 GB/s per SM.  At group size 1 and 2 the CUDA-core math does
 // proportionally less work and is a little faster (both measured).
 bool attention_uses_tensor_cores(int cache_kind, int q_len, int gqa, bool cascade_pass) {
-    return cascade_pass || cache_kind == PKV_CACHE_K8V4 || q_len > 1 || gqa * q_len >= kTcMinRows;
+    return cascade_pass || cache_kind == PKV_CACHE_K8V4 || is_byte_cache(cache_kind) || q_len > 1 || gqa * q_len >= kTcMinRows;
 }
 
 cudaError_t launch_attention(AttnParams p, int cache_kind, int gqa, const CUtensorMap& km, const CUtensorMap& vm,
                              cudaStream_t stream) {
+    if (is_byte_cache(cache_kind)) return launch_attention_byte(p, cache_kind, km, vm, stream);
     if (is_cascade_pass(p)) return launch_attention_cascade(p, cache_kind, gqa, km, vm, stream);
     if (p.num_new > 0) return launch_attention_fused(p, cache_kind, gqa, km, vm, stream);
     return launch_attention_impl<false, false>(p, cache_kind, gqa, km, vm, stream);

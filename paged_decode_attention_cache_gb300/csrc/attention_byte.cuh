@@ -1,0 +1,316 @@
+// attention_byte.cuh -- block math of the caches held in 8 bits with one scale
+// per (16-token block, kv head): int8 (PKV_CACHE_I8) and fp8 e4m3
+// (PKV_CACHE_E4M3) codes.  Included after attention_impl.cuh.
+#pragma once
+
+#include "attention_impl.cuh"
+
+namespace pkv {
+
+namespace {
+
+// Bytes 0 and 2 (ODD false) or 1 and 3 (ODD true) of w -> fp16x2.
+// int8: the exact integers (flip the sign bit, splice the byte under the
+// exponent of 1024, subtract 1024 + 128).  e4m3: sign, 4 exponent and 3
+// mantissa bits placed in fp16's fields, which is the exact value times 2^-8
+// (the exponent biases are 7 and 15; subnormals land on subnormals).  Every
+// code gives a finite number (e4m3's NaN pattern reads as 480 x 2^-8), so a slot
+// past the context never poisons a product with P = 0.
+template <bool E4M3, bool ODD>
+__device__ __forceinline__ uint32_t byte_pair_to_f16x2(uint32_t w) {
+    if constexpr (E4M3) {
+        if constexpr (ODD) return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+        return ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+    } else {
+        const uint32_t x = __byte_perm(w ^ 0x80808080u, 0x64646464u, ODD ? 0x4341 : 0x4240);
+        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+        __half2 h;
+        memcpy(&h, &x, 4);
+        h = __hsub2(h, bias);
+        uint32_t r;
+        memcpy(&r, &h, 4);
+        return r;
+    }
+}
+
+// As TqMath, the contraction is turned around: S^T = K Q^T puts the block's 16
+// tokens on the MMA's M side and up to 8 (NT = 1) or 16 (NT = 2) query columns
+// on N, and O^T = V^T P^T puts 16 head dims on M.
+//   K: codes to exact fp16 in registers.  A thread's four k positions of a
+//      k-step are four consecutive bytes of a row, paired (0, 2) and (1, 3); the
+//      query operand uses the same dim order.  The block's one K scale
+//      multiplies the scores.
+//   Q: fp16 in the operand.  bf16 queries are first scaled by a power of two
+//      per row (largest magnitude to [256, 512)), taken off the scores again, so
+//      no bf16 query leaves fp16's range.
+//   V: codes to fp16 in the A operand (ldmatrix.trans of 16-bit words = 2 dims x
+//      2 tokens): the 16 dims of an M tile are a row's 16-byte chunk, even dims in
+//      rows 0-7, odd dims in rows 8-15.  The block's one V scale multiplies the
+//      block's product as it is added to the fp32 accumulators: folded into the
+//      fp16 P instead it would push small weights under fp16's range.
+//   P: fp16 hi + lo (two MMAs, P exact to ~2^-22): one fp16 P rounds each weight
+//      by 2^-12, as large an error as the rounding of an fp16 output.
+// 4 KB per block and kv head at D = 128: half the bf16 cache's bytes for about
+// the same instructions, so the consumers' issue rate sits nearer the HBM rate.
+template <bool E4M3, int D, int NT>
+struct TeMath {
+    static constexpr bool kTensor = true;
+    static constexpr int kD = D;
+    static constexpr int NCW = NT == 1 ? 11 : 7;
+    static constexpr int kSegCost = pkv::kSegCost;
+    static constexpr int kIssueGroup = 22;
+    static constexpr int NKS = D / 16;     // k-steps of the score contraction
+    static constexpr int NMT = D / 16;     // M tiles of O^T
+    static constexpr int KT = kBS * D;
+    static constexpr int OFF_V = align_up(KT, 1024);
+    static constexpr int OFF_S = OFF_V + KT;   // {K scale, V scale}
+    static constexpr int TX = 2 * KT;   // bytes the TMA copies deliver
+    static constexpr int STAGE = align_up(OFF_S + 16, 1024);
+    static constexpr int SCRATCH = 0;
+    static constexpr bool kQ8 = true;
+    static constexpr float kUnit = E4M3 ? 256.f : 1.f;   // what the operand's numbers are short of the codes'
+    static_assert(OFF_V % 1024 == 0 && STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
+
+    uint32_t qb[NT][NKS][2];   // Q^T operand: query column g (+8), this thread's dims
+    float o[NT][NMT][4];       // O^T: dims 16 mt + 2g, + 1 of query columns 2t, 2t + 1
+    float m_run[NT][2], l_part[NT][2];   // query columns 2t, 2t + 1 (l: this thread's tokens)
+    float kcol[NT][2];         // what turns the column's products into base-2 scores, but for the K scale
+    int lim[NT][2];
+    int lo_;       // first visible token
+    int lim_lo_;   // smallest lim over this thread's live columns (no live column: INT_MAX)
+    float scale_log2_;
+
+    static __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* vm,
+                                                 const AttnParams& p, int kvh, int pb, uint64_t* bar) {
+        const size_t meta = size_t(pb) * p.num_kv_heads + kvh;
+        cp_async_4(dst + OFF_S, static_cast<const float*>(p.k_scale) + meta);
+        cp_async_4(dst + OFF_S + 4, static_cast<const float*>(p.v_scale) + meta);
+        cp_async_mbar_arrive(bar);
+        mbar_arrive_expect_tx(bar, TX);
+        const uint64_t pol = l2_evict_first_policy();
+        tma_load_2d_hint(dst, km, kvh * D, pb * kBS, bar, pol);
+        tma_load_2d_hint(dst + OFF_V, vm, kvh * D, pb * kBS, bar, pol);
+    }
+
+    // the fused step does not take these caches (a new token may change its block's scale)
+    __device__ __forceinline__ void patch(uint8_t*, int, int, const uint8_t*, int, const AttnParams&) const {}
+
+    __device__ __forceinline__ void init(int) {}
+
+    // query column n = head (n / q_len), draft (n % q_len)
+    template <bool CASC>
+    __device__ __forceinline__ void begin(const AttnParams& p, int s, int kvh, int ctx, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const int G = p.num_heads / p.num_kv_heads, QL = p.q_len, M = G * QL;
+        lo_ = visible_lo<CASC>(p, s, ctx);
+        lim_lo_ = INT_MAX;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int n = 8 * nt + g;
+            const int h = n < M ? n / QL : 0, j = n < M ? n % QL : 0;
+            const int qr = n < M ? query_row<CASC>(p, s, j) : -1;
+            const bool valid = qr >= 0;
+            const size_t qoff = (size_t(valid ? qr : 0) * p.num_heads + kvh * G + h) * D;
+            // this thread's dims t*D/4 .. t*D/4 + D/4 - 1: D/2 contiguous bytes, as 16-byte loads
+            uint32_t qw[D / 8];
+            const uint4* qv = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + qoff + t * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 x = valid ? qv[i] : make_uint4(0u, 0u, 0u, 0u);
+                qw[4 * i] = x.x; qw[4 * i + 1] = x.y; qw[4 * i + 2] = x.z; qw[4 * i + 3] = x.w;
+            }
+            float back = 1.f;
+            if (p.q_dtype == PKV_BF16) {
+                // largest exponent field of the column: the power of two that brings it to 2^8
+                uint32_t ex = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) ex = max(ex, max((qw[i] >> 7) & 0xffu, (qw[i] >> 23) & 0xffu));
+                ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 1));
+                ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 2));
+                // 2^(135 - ex) and its inverse stay normal fp32 numbers; a row of zeros or subnormals
+                // (ex 0) and one with an infinity or NaN (ex 255) take the nearest of them
+                const uint32_t e = min(max(ex, 16u), 254u);
+                const float up = __uint_as_float((262u - e) << 23);
+                back = __uint_as_float((e - 8u) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float2 f = Half16<__nv_bfloat16>::unpack2(qw[i]);
+                    qw[i] = pack2<false>(f.x * up, f.y * up);
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < NKS; ++kk) {
+                // dims d0 .. d0 + 3 (d0 = t*D/4 + 4*kk) as (d0, d0 + 2), (d0 + 1, d0 + 3)
+                qb[nt][kk][0] = __byte_perm(qw[2 * kk], qw[2 * kk + 1], 0x5410);
+                qb[nt][kk][1] = __byte_perm(qw[2 * kk], qw[2 * kk + 1], 0x7632);
+            }
+            // column 2t + e's factor sits in the lanes of g = 2t + e
+            const float kc = scale_log2_ * kUnit * back;
+            kcol[nt][0] = __shfl_sync(0xffffffffu, kc, (2 * t) * 4);
+            kcol[nt][1] = __shfl_sync(0xffffffffu, kc, (2 * t + 1) * 4);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n2 = 8 * nt + 2 * t + e;
+                const int j2 = n2 % QL;
+                const bool ok2 = n2 < M && query_row<CASC>(p, s, j2) >= 0;
+                // a cascade row (one decode query) sees the entry's whole context; verify rows are causal
+                lim[nt][e] = ok2 ? (CASC ? ctx : max(0, ctx - QL + j2 + 1)) : 0;
+                if (lim[nt][e] > 0) lim_lo_ = min(lim_lo_, lim[nt][e]);
+                m_run[nt][e] = -INFINITY;
+                l_part[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < NMT; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int /*ntok*/, uint8_t*, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const uint32_t stg_a = smem_addr(stg);
+        // ------------------------------------------------ S^T = K Q^T (rows = tokens g, g + 8)
+        uint32_t w[2][NKS];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int c = t * (D / 64) + i;
+                const uint4 v = *reinterpret_cast<const uint4*>(stg + row * D + 16 * swz<D>(c, row));
+                w[r][4 * i] = v.x; w[r][4 * i + 1] = v.y; w[r][4 * i + 2] = v.z; w[r][4 * i + 3] = v.w;
+            }
+        }
+        const float2 ss = *reinterpret_cast<const float2*>(stg + OFF_S);
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < NKS; ++kk) {
+            uint32_t a[4];
+            a[0] = byte_pair_to_f16x2<E4M3, false>(w[0][kk]);
+            a[1] = byte_pair_to_f16x2<E4M3, false>(w[1][kk]);
+            a[2] = byte_pair_to_f16x2<E4M3, true>(w[0][kk]);
+            a[3] = byte_pair_to_f16x2<E4M3, true>(w[1][kk]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+        }
+        // block scale, base-2 softmax scale, causal / context mask
+        const int pg = pos0 + g, pg8 = pos0 + g + 8;
+        const bool all = pos0 >= lo_ && pos0 + kBS <= lim_lo_;   // whole block visible to every live column
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float k = ss.x * kcol[nt][e];
+                const bool v0 = all ? lim[nt][e] > 0 : (pg < lim[nt][e] && pg >= lo_);
+                const bool v1 = all ? lim[nt][e] > 0 : (pg8 < lim[nt][e] && pg8 >= lo_);
+                sc[nt][e] = v0 ? sc[nt][e] * k : -INFINITY;
+                sc[nt][2 + e] = v1 ? sc[nt][2 + e] * k : -INFINITY;
+            }
+        // ------------------------------------------------ online softmax per query column
+        float alpha[NT][2];
+        bool rescale = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float bm = fmaxf(sc[nt][e], sc[nt][2 + e]);
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+                const float mn = fmaxf(m_run[nt][e], bm);
+                const float mu = (mn == -INFINITY) ? 0.f : mn;
+                // nothing accumulated yet (padding columns stay so): no rescale
+                alpha[nt][e] = (m_run[nt][e] == -INFINITY) ? 1.f : exp2_ftz(m_run[nt][e] - mu);
+                const float p0 = exp2_ftz(sc[nt][e] - mu), p1 = exp2_ftz(sc[nt][2 + e] - mu);
+                sc[nt][e] = p0;
+                sc[nt][2 + e] = p1;
+                l_part[nt][e] = l_part[nt][e] * alpha[nt][e] + (p0 + p1);
+                m_run[nt][e] = mn;
+                rescale |= alpha[nt][e] != 1.f;
+            }
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < NMT; ++mt) {
+                    o[nt][mt][0] *= alpha[nt][0]; o[nt][mt][2] *= alpha[nt][0];
+                    o[nt][mt][1] *= alpha[nt][1]; o[nt][mt][3] *= alpha[nt][1];
+                }
+        }
+        // ------------------------------------------------ P^T operand (tokens 2t.., query column g), hi and lo
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float x = sc[nt][2 * r], y = sc[nt][2 * r + 1];
+                const uint32_t h = pack2<false>(x, y);
+                const float2 hf = Half16<__half>::unpack2(h);
+                ph[nt][r] = movm_trans(h);
+                pl[nt][r] = movm_trans(pack2<false>(x - hf.x, y - hf.y));
+            }
+        // ------------------------------------------------ O^T += v_scale * V^T P^T
+        const float vs = ss.y * kUnit;
+#pragma unroll
+        for (int c0 = 0; c0 < NMT; c0 += 2) {
+            // matrices (transposed 16-bit words): tokens 0-7, 8-15 of chunk c0, then of chunk c0 + 1
+            const int mi = lane >> 3, r = lane & 7;
+            const int tok = (mi & 1) * 8 + r, c = c0 + (mi >> 1);
+            uint32_t X[4];
+            ldsm_x4_t(stg_a + OFF_V + tok * D + 16 * swz<D>(c, tok), X);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a[4];
+                a[0] = byte_pair_to_f16x2<E4M3, false>(X[2 * h]);
+                a[1] = byte_pair_to_f16x2<E4M3, true>(X[2 * h]);
+                a[2] = byte_pair_to_f16x2<E4M3, false>(X[2 * h + 1]);
+                a[3] = byte_pair_to_f16x2<E4M3, true>(X[2 * h + 1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(acc, a, ph[nt][0], ph[nt][1]);
+                    mma_f16(acc, a, pl[nt][0], pl[nt][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[nt][c0 + h][i] = fmaf(acc[i], vs, o[nt][c0 + h][i]);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish(int) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = l_part[nt][e];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                l_part[nt][e] = l;
+            }
+    }
+
+    // unnormalised rows [M][D] (ob_idx order) and per-row (m, l) of this warp
+    __device__ __forceinline__ void store(float* ob, float* mw, float* lw, int M, int lane) const {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int q = 8 * nt + 2 * t + e;
+                if (q >= M) continue;
+#pragma unroll
+                for (int mt = 0; mt < NMT; ++mt)
+                    *reinterpret_cast<float2*>(ob + ob_idx(q, 16 * mt + 2 * g, D)) =
+                        make_float2(o[nt][mt][e], o[nt][mt][2 + e]);
+                if (g == 0) {
+                    mw[q] = m_run[nt][e];
+                    lw[q] = l_part[nt][e];
+                }
+            }
+    }
+};
+
+}  // namespace
+
+}  // namespace pkv

@@ -47,6 +47,8 @@
 //   TqMath  K8/V4, any q_len: the contraction turned around (S^T = K Q^T,
 //           O^T = V^T P^T) so the query columns sit on the MMA's N side; codes
 //           become exact fp16 integers in registers.
+//   TeMath  the 8-bit caches with a scale per (block, kv head), any q_len, in
+//           attention_byte.cuh: turned around like TqMath.
 // Every mbarrier wait is bounded; a wait that gives up flags
 // PKV_DEVERR_TIMEOUT and the block is skipped.
 #pragma once

@@ -1,0 +1,287 @@
+// cache_blocks.cu -- the 8-bit caches with one scale per (16-token block, kv
+// head): the append of new tokens, and the dequantising gather.
+//
+// A block's scale has to cover every token in it, so the append works on whole
+// (sequence, block) pairs instead of single slots: one warp takes the new tokens
+// of one (block, kv head), for K or for V, finds their largest magnitude, grows
+// the scale if the block's own does not cover it, rewrites the block's older
+// codes for the grown scale, and quantises the new rows.  No other warp touches
+// that (block, kv head), so there is nothing to wait for and no atomic.
+//
+// Scales sit on a coarse grid: int8 scales have three significant bits, e4m3
+// scales are powers of two.  A scale that grows does so by a quarter or more
+// (int8) or doubles (e4m3), so a block filled token by token is re-rounded a few
+// times at most where exact scales would re-round at every new maximum, and an
+// e4m3 code keeps its value exactly unless it turns subnormal.  The price is up
+// to one part in five of int8's range (a tenth on average).
+//
+// Bound: HBM for prompts (4 bytes read and 2 written per element of K + V),
+// dependent-load latency for a decode step (length -> table -> scale, row).
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kBlock = 16;
+constexpr int kThreads = 256;
+
+// The largest magnitude of two 16-bit floats in each half of a and b (packed).
+template <typename Src>
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
+    using V = typename std::conditional<std::is_same<Src, __half>::value, __half2, __nv_bfloat162>::type;
+    V x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    const V z = __hmax2(x, __habs2(y));
+    uint32_t r;
+    memcpy(&r, &z, 4);
+    return r;
+}
+
+// amax / qmax rounded up to the scale grid.  0 stays 0; nothing below 2^-126
+// (so that 1 / scale is finite).
+template <bool E4M3>
+__device__ __forceinline__ float scale_for(float amax) {
+    const float t = __fdiv_rn(amax, E4M3 ? 448.f : 127.f);
+    constexpr uint32_t drop = E4M3 ? 0x007fffffu : 0x001fffffu;
+    const float up = __uint_as_float((__float_as_uint(t) + drop) & ~drop);
+    return t > 0.f ? fmaxf(up, 1.17549435e-38f) : 0.f;
+}
+
+// Four numbers already divided by the scale -> four codes.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    if constexpr (E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    } else {
+        auto q = [](float x) { return uint32_t(int(fminf(fmaxf(rintf(x), -127.f), 127.f))) & 0xffu; };
+        return q(a) | (q(b) << 8) | (q(c) << 16) | (q(d) << 24);
+    }
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float code_value(uint32_t byte) {
+    if constexpr (E4M3)
+        return __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_fp8_storage_t(byte), __NV_E4M3)));
+    return float(int(int8_t(byte)));
+}
+
+// The sequence whose new tokens hold unit `u` of the work list, where sequence
+// s's units start at cu[s] / 16 + 2 s (at least as far apart as the blocks its
+// tokens can touch).  All 32 lanes probe the remaining range at once.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int num_tokens, int u, int lane) {
+    int lo = 0, hi = num_seqs;   // start(lo) <= u, the answer is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int s = lo + lane * step;
+        const bool le = s < hi && min(max(cu[s], 0), num_tokens) / kBlock + 2 * s <= u;
+        const uint32_t m = __ballot_sync(0xffffffffu, le) | 1u;
+        const int last = 31 - __clz(m);   // the last probe that starts at or before u
+        const int nlo = lo + last * step;
+        hi = min(hi, nlo + step);
+        lo = nlo;
+    }
+    return lo;
+}
+
+template <typename Src, bool E4M3, int D>
+__global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    constexpr int LPR = D / 8;           // lanes per row, 8 values each
+    constexpr int RPP = 32 / LPR;        // rows per pass
+    constexpr int NP = kBlock / RPP;     // passes over the block
+    const int lane = threadIdx.x & 31;
+    const int H = p.num_kv_heads;
+    const int64_t w = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (w >= int64_t(p.units) * H * 2) return;
+    const int which = int(w & 1);        // 0: K, 1: V
+    const int h = int((w >> 1) % H);
+    const int u = int((w >> 1) / H);
+
+    // ---- this unit's sequence, its new tokens and the block
+    int s, i, n, row0;
+    if (p.cu_new) {
+        s = find_seq(p.cu_new, p.num_seqs, p.num_tokens, u, lane);
+        const int c0 = min(max(p.cu_new[s], 0), p.num_tokens), c1 = min(max(p.cu_new[s + 1], 0), p.num_tokens);
+        i = u - (c0 / kBlock + 2 * s);
+        n = c1 - c0;
+        row0 = c0;
+    } else {
+        const int per = (p.q_len + 14) / kBlock + 1;
+        s = u / per;
+        i = u - s * per;
+        n = p.q_len;
+        row0 = s * p.q_len;
+    }
+    if (i < 0 || n <= 0) return;
+    const int ctx = p.context_lens[s];
+    if (ctx <= 0) return;
+    const int cap = p.max_blocks * kBlock;
+    if (ctx > cap && i == 0 && h == 0 && which == 0 && lane == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
+    const int p0 = max(ctx - n, 0), p1 = min(ctx, cap);   // positions written: [p0, p1)
+    if (p0 >= p1) return;
+    const int64_t b64 = int64_t(p0 / kBlock) + i;
+    if (b64 * kBlock >= p1) return;
+    const int b = int(b64);
+    const int a = max(p0 - b * kBlock, 0), e = min(p1 - b * kBlock, kBlock);   // new rows [a, e) of the block
+    const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
+    if (pb < 0 || pb >= p.num_blocks) {
+        if (h == 0 && which == 0 && lane == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
+        return;
+    }
+    const int64_t meta = int64_t(pb) * H + h;
+    float* scale_at = (which ? p.v_scale : p.k_scale) + meta;
+    uint8_t* codes = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache) + (int64_t(pb) * kBlock * H + h) * D;
+    const uint16_t* src = static_cast<const uint16_t*>(which ? p.v_new : p.k_new);
+    const int r0 = lane / LPR, d0 = (lane % LPR) * 8;
+
+    // ---- the new rows and their largest magnitude
+    uint4 x[NP];
+    uint32_t m2 = 0;
+    const int64_t src_row = int64_t(row0) + int64_t(b) * kBlock - (int64_t(ctx) - n);   // row of offset 0
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int r = k * RPP + r0;
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= a && r < e) x[k] = __ldg(reinterpret_cast<const uint4*>(src + ((src_row + r) * H + h) * D + d0));
+    }
+    float s_old = a > 0 ? *scale_at : 0.f;
+    if (!(s_old > 0.f) || isinf(s_old)) s_old = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        m2 = absmax2<Src>(m2, x[k].x);
+        m2 = absmax2<Src>(m2, x[k].y);
+        m2 = absmax2<Src>(m2, x[k].z);
+        m2 = absmax2<Src>(m2, x[k].w);
+    }
+    const float2 mf = Half16<Src>::unpack2(m2);
+    float amax = fmaxf(mf.x, mf.y);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s_new = fmaxf(s_old, scale_for<E4M3>(amax));
+    const float inv = s_new > 0.f ? __fdiv_rn(1.f, s_new) : 0.f;
+
+    // ---- the block's older rows, for a scale that grew
+    if (a > 0 && s_new > s_old) {
+        const float share = __fdiv_rn(s_old, s_new);
+#pragma unroll 2
+        for (int r = r0; r < a; r += RPP) {
+            uint2* at = reinterpret_cast<uint2*>(codes + int64_t(r) * H * D + d0);
+            const uint2 c = *at;
+            float f[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[q] = code_value<E4M3>(((q < 4 ? c.x : c.y) >> (8 * (q & 3))) & 0xffu) * share;
+            *at = make_uint2(codes4<E4M3>(f[0], f[1], f[2], f[3]), codes4<E4M3>(f[4], f[5], f[6], f[7]));
+        }
+    }
+    // ---- the new rows
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int r = k * RPP + r0;
+        if (r < a || r >= e) continue;
+        const float2 f0 = Half16<Src>::unpack2(x[k].x), f1 = Half16<Src>::unpack2(x[k].y);
+        const float2 f2 = Half16<Src>::unpack2(x[k].z), f3 = Half16<Src>::unpack2(x[k].w);
+        *reinterpret_cast<uint2*>(codes + int64_t(r) * H * D + d0) =
+            make_uint2(codes4<E4M3>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv),
+                       codes4<E4M3>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv));
+    }
+    __syncwarp();   // every lane has read the old scale
+    if (lane == 0) *scale_at = s_new;
+}
+
+// CTA (b, s) expands logical block b of sequence s; a thread takes 8 dims of
+// one (token, kv head): an 8-byte load and a 16-byte store each for K and V.
+template <typename OutT, bool E4M3, int D>
+__global__ void __launch_bounds__(kThreads) gather_blocks_kernel(GatherParams p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    constexpr int CPT = D / 8;
+    const int s = blockIdx.y, b = blockIdx.x;
+    int ctx = p.context_lens[s];
+    const int cap = p.max_blocks * kBlock;
+    if (ctx > cap) {
+        if (b == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
+        ctx = cap;
+    }
+    const int t0 = b * kBlock;
+    if (t0 >= ctx) return;
+    const int ntok = min(kBlock, ctx - t0);
+    const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
+    if (pb < 0 || pb >= p.num_blocks) {
+        if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
+        return;
+    }
+    const int H = p.num_kv_heads;
+    const int64_t src0 = int64_t(pb) * kBlock * H * D, dst0 = (int64_t(p.cu_seq_lens[s]) + t0) * H * D;
+    const int n = ntok * H * CPT;   // the block's first ntok token rows are contiguous on both sides
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int h = (i / CPT) % H;
+        const float scales[2] = {__ldg(static_cast<const float*>(p.k_scale) + int64_t(pb) * H + h),
+                                 __ldg(static_cast<const float*>(p.v_scale) + int64_t(pb) * H + h)};
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(which ? p.v_cache : p.k_cache) + src0) + i);
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t two = ((q < 2 ? c.x : c.y) >> (16 * (q & 1))) & 0xffffu;
+                const float x = code_value<E4M3>(two & 0xffu) * scales[which], y = code_value<E4M3>(two >> 8) * scales[which];
+                if constexpr (std::is_same<OutT, __nv_bfloat16>::value) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                    memcpy(o + q, &v, 4);
+                } else {
+                    const __half2 v = __floats2half2_rn(x, y);
+                    memcpy(o + q, &v, 4);
+                }
+            }
+            *(reinterpret_cast<uint4*>(static_cast<OutT*>(which ? p.v_out : p.k_out) + dst0) + i) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+template <typename Src, bool E4M3>
+cudaError_t append_d(const BlockWriteParams& p, dim3 grid, cudaStream_t st) {
+    return p.head_dim == 128 ? launch_kernel(append_blocks_kernel<Src, E4M3, 128>, grid, dim3(kThreads), 0, st, p)
+                             : launch_kernel(append_blocks_kernel<Src, E4M3, 64>, grid, dim3(kThreads), 0, st, p);
+}
+
+template <typename OutT, bool E4M3>
+cudaError_t gather_d(const GatherParams& p, dim3 grid, cudaStream_t st) {
+    return p.head_dim == 128 ? launch_kernel(gather_blocks_kernel<OutT, E4M3, 128>, grid, dim3(kThreads), 0, st, p)
+                             : launch_kernel(gather_blocks_kernel<OutT, E4M3, 64>, grid, dim3(kThreads), 0, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_append_blocks(BlockWriteParams p, cudaStream_t stream) {
+    const int64_t units = p.cu_new ? int64_t(p.num_tokens) / kBlock + 2 * int64_t(p.num_seqs)
+                                   : int64_t(p.num_seqs) * ((p.q_len + 14) / kBlock + 1);
+    const int64_t ctas = (units * p.num_kv_heads * 2 + kThreads / 32 - 1) / (kThreads / 32);
+    if (units > 0x7fffffff || ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    p.units = int32_t(units);
+    const dim3 grid{unsigned(ctas)};
+    const bool e4 = p.cache_kind == PKV_CACHE_E4M3;
+    if (p.src_dtype == PKV_BF16)
+        return e4 ? append_d<__nv_bfloat16, true>(p, grid, stream) : append_d<__nv_bfloat16, false>(p, grid, stream);
+    return e4 ? append_d<__half, true>(p, grid, stream) : append_d<__half, false>(p, grid, stream);
+}
+
+cudaError_t launch_gather_blocks(const GatherParams& p, int cache_kind, cudaStream_t stream) {
+    const dim3 grid(p.max_blocks, p.num_seqs);
+    const bool e4 = cache_kind == PKV_CACHE_E4M3;
+    if (p.out_dtype == PKV_BF16)
+        return e4 ? gather_d<__nv_bfloat16, true>(p, grid, stream) : gather_d<__nv_bfloat16, false>(p, grid, stream);
+    return e4 ? gather_d<__half, true>(p, grid, stream) : gather_d<__half, false>(p, grid, stream);
+}
+
+}  // namespace pkv

@@ -106,10 +106,13 @@ constexpr int kBlockSize = 16;   // token slots per cache block
 constexpr int kMinChunk = 8;
 constexpr int kSegCost = 24;
 
+// A cache held in 8 bits with one scale per (block, kv head).
+inline bool is_byte_cache(int kind) { return kind == PKV_CACHE_I8 || kind == PKV_CACHE_E4M3; }
+
 // Persistent attention kernel (attention.cu): one CTA per SM at most, the
 // (sequence, kv head, block) work list split into contiguous ranges.
 bool attention_supported(int cache_kind, int head_dim, int gqa, int q_len);
-// Tensor-core maths for K8/V4, for cascade passes and whenever a kv head serves
+// Tensor-core maths for K8/V4 and the 8-bit caches, for cascade passes and whenever a kv head serves
 // at least kTcMinRows query rows (group size x q_len); the CUDA-core math for
 // fp16/bf16 below that (group size 1 or 2 decode).
 constexpr int kTcMinRows = 4;
@@ -124,6 +127,9 @@ cudaError_t launch_attention_cascade(AttnParams p, int cache_kind, int gqa, cons
                                      const CUtensorMap& vm, cudaStream_t stream);
 cudaError_t launch_attention_fused(AttnParams p, int cache_kind, int gqa, const CUtensorMap& km, const CUtensorMap& vm,
                                    cudaStream_t stream);
+// The 8-bit caches' kernels (attention_byte.cu)
+cudaError_t launch_attention_byte(const AttnParams& p, int cache_kind, const CUtensorMap& km, const CUtensorMap& vm,
+                                  cudaStream_t stream);
 size_t balanced_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim);
 
 struct ReduceParams {
@@ -202,6 +208,25 @@ struct CacheWriteParams {
 cudaError_t launch_reshape_and_cache(const CacheWriteParams& p, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_quantize_kv(const CacheWriteParams& p, cudaStream_t stream);
 
+// Append of new tokens to an 8-bit cache (cache_blocks.cu).
+struct BlockWriteParams {
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;               // [num_blocks, num_kv_heads]
+    float* v_scale;
+    const void* k_new;            // [num_tokens, num_kv_heads, head_dim], src_dtype
+    const void* v_new;
+    const int32_t* cu_new;        // [num_seqs + 1] rows of each sequence, or null: q_len rows each
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int32_t num_seqs, max_blocks, q_len, num_tokens;
+    int32_t num_blocks, num_kv_heads, head_dim;
+    int32_t cache_kind, src_dtype;
+    int32_t units;                // (sequence, block) pairs the launch covers (set by the launcher)
+    uint32_t* err;
+};
+cudaError_t launch_append_blocks(BlockWriteParams p, cudaStream_t stream);
+
 struct GatherParams {
     void* k_out;
     void* v_out;
@@ -224,5 +249,6 @@ struct GatherParams {
 };
 cudaError_t launch_gather(const GatherParams& p, int elem_bytes, cudaStream_t stream);
 cudaError_t launch_gather_dequant(const GatherParams& p, cudaStream_t stream);
+cudaError_t launch_gather_blocks(const GatherParams& p, int cache_kind, cudaStream_t stream);
 
 }  // namespace pkv

@@ -19,11 +19,14 @@ from . import build as _build
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA = 0, 1, 2, 3
 PKV_F16, PKV_BF16, PKV_F32 = 0, 1, 2
-PKV_CACHE_F16, PKV_CACHE_BF16, PKV_CACHE_K8V4 = 0, 1, 2
+PKV_CACHE_F16, PKV_CACHE_BF16, PKV_CACHE_K8V4, PKV_CACHE_I8, PKV_CACHE_E4M3 = 0, 1, 2, 3, 4
 DEVERR_OOB_BLOCK, DEVERR_OOB_SLOT, DEVERR_CAPACITY, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
 _DT = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
-_CACHE_KIND = {"f16": PKV_CACHE_F16, "bf16": PKV_CACHE_BF16, "k8v4": PKV_CACHE_K8V4}
+_CACHE_KIND = {"f16": PKV_CACHE_F16, "bf16": PKV_CACHE_BF16, "k8v4": PKV_CACHE_K8V4, "i8": PKV_CACHE_I8,
+               "e4m3": PKV_CACHE_E4M3}
+# 8-bit caches with one scale per (block, kv head): the code tensors' dtypes
+_BYTE_CODES = {"i8": (torch.int8,), "e4m3": (torch.float8_e4m3fn, torch.uint8)}
 
 
 class PkvError(RuntimeError):
@@ -79,6 +82,8 @@ def lib():
         L.pkv_reshape_and_cache.argtypes = [_P, _P, _P, _P, _I32, _P, _P]
         L.pkv_quantize_kv.restype = st
         L.pkv_quantize_kv.argtypes = [_P, _P, _P, ctypes.c_int, _P, _I32, _P, _P]
+        L.pkv_quantize_kv_blocks.restype = st
+        L.pkv_quantize_kv_blocks.argtypes = [_P, _P, _P, ctypes.c_int, _I32, _P, _P, _P, _P]
         L.pkv_paged_attention.restype = st
         L.pkv_paged_attention.argtypes = [_P, ctypes.c_int, _P, ctypes.c_int, _I32, ctypes.c_float, _P, _P, _P, _P]
         L.pkv_split_workspace_bytes.restype = ctypes.c_size_t
@@ -149,11 +154,11 @@ def _stream(stream: Optional[torch.cuda.Stream]):
 @dataclass
 class Cache:
     """One layer's paged cache (caller-owned device tensors)."""
-    kind: str                 # "f16" | "bf16" | "k8v4"
-    k: torch.Tensor           # [NB, 16, Hkv, D] (k8v4: int8)
-    v: torch.Tensor           # [NB, 16, Hkv, D] (k8v4: uint8 [NB, 16, Hkv, D/2])
-    k_scale: Optional[torch.Tensor] = None   # k8v4: fp16 [NB, Hkv, 16]
-    v_scale: Optional[torch.Tensor] = None   # k8v4: fp16 [NB, Hkv, 16, D/32]
+    kind: str                 # "f16" | "bf16" | "k8v4" | "i8" | "e4m3"
+    k: torch.Tensor           # [NB, 16, Hkv, D] (k8v4, i8: int8; e4m3: float8_e4m3fn)
+    v: torch.Tensor           # [NB, 16, Hkv, D] (k8v4: uint8 [NB, 16, Hkv, D/2]; i8, e4m3: as k)
+    k_scale: Optional[torch.Tensor] = None   # k8v4: fp16 [NB, Hkv, 16]; i8, e4m3: fp32 [NB, Hkv]
+    v_scale: Optional[torch.Tensor] = None   # k8v4: fp16 [NB, Hkv, 16, D/32]; i8, e4m3: fp32 [NB, Hkv]
     v_zero: Optional[torch.Tensor] = None
     v_group: int = 32
 
@@ -169,7 +174,18 @@ class Cache:
     def head_dim(self):
         return int(self.k.shape[3])
 
+    def _check_byte(self):
+        shape, scales = self.k.shape, (self.num_blocks, self.num_kv_heads)
+        if self.k.dtype not in _BYTE_CODES[self.kind] or self.v.dtype not in _BYTE_CODES[self.kind]:
+            raise ValueError(f"a {self.kind} cache holds {_BYTE_CODES[self.kind][0]} codes")
+        if self.v.shape != shape or self.k_scale is None or self.v_scale is None or \
+                self.k_scale.shape != scales or self.v_scale.shape != scales or \
+                self.k_scale.dtype != torch.float32 or self.v_scale.dtype != torch.float32:
+            raise ValueError(f"a {self.kind} cache has k and v of one shape and float32 scales [num_blocks, num_kv_heads]")
+
     def c_struct(self) -> _Cache:
+        if self.kind in _BYTE_CODES:
+            self._check_byte()
         return _Cache(_CACHE_KIND[self.kind], self.num_blocks, int(self.k.shape[1]), self.num_kv_heads,
                       self.head_dim, self.v_group, _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
                       _ptr(self.v_scale), _ptr(self.v_zero))
@@ -183,6 +199,10 @@ class Cache:
                          torch.zeros((NB, H, 16), dtype=torch.float16, device=device),
                          torch.zeros((NB, H, 16, D // 32), dtype=torch.float16, device=device),
                          torch.zeros((NB, H, 16, D // 32), dtype=torch.float16, device=device))
+        if kind in _BYTE_CODES:
+            code = _BYTE_CODES[kind][0]
+            return Cache(kind, *(torch.zeros((NB, 16, H, D), dtype=torch.uint8, device=device).view(code) for _ in "kv"),
+                         *(torch.zeros((NB, H), dtype=torch.float32, device=device) for _ in "kv"))
         dt = torch.float16 if kind == "f16" else torch.bfloat16
         return Cache(kind, torch.zeros((NB, 16, H, D), dtype=dt, device=device),
                      torch.zeros((NB, 16, H, D), dtype=dt, device=device))
@@ -226,6 +246,35 @@ def pkv_quantize_kv(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, slot
     c = cache.c_struct()
     _check(lib().pkv_quantize_kv(ctypes.byref(c), _ptr(k_new), _ptr(v_new), _DT[k_new.dtype], _ptr(slot_mapping),
                                  int(slot_mapping.numel()), _err_ptr(err_flags), _stream(stream)))
+
+
+def _one_device(*tensors) -> None:
+    """The tensors of a call share a device, and it is the current one (its stream runs the kernels)."""
+    device = torch.device("cuda", torch.cuda.current_device())
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"pkv tensors must live on the current CUDA device ({device}), not {t.device}")
+
+
+def pkv_quantize_kv_blocks(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, seqs: Seqs,
+                           cu_new_lens: Optional[torch.Tensor] = None, err_flags: Optional[torch.Tensor] = None,
+                           stream=None) -> None:
+    """Append each sequence's new tokens (its last ones: rows cu_new_lens[s] ..
+    cu_new_lens[s + 1] of k_new / v_new, or q_len rows each) to an "i8" or
+    "e4m3" cache; a block's scale grows when they need it."""
+    if k_new.dtype not in (torch.float16, torch.bfloat16) or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new / v_new must both be float16 or both bfloat16")
+    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (cache.num_kv_heads, cache.head_dim) or v_new.shape != k_new.shape:
+        raise ValueError("k_new / v_new must be [num_tokens, num_kv_heads, head_dim]")
+    if cu_new_lens is not None and (cu_new_lens.dtype != torch.int32 or
+                                    cu_new_lens.numel() != seqs.block_tables.shape[0] + 1):
+        raise ValueError("cu_new_lens must be int32 [num_seqs + 1]")
+    _one_device(cache.k, cache.v, cache.k_scale, cache.v_scale, k_new, v_new, seqs.block_tables, seqs.context_lens,
+                cu_new_lens, err_flags)
+    c, s = cache.c_struct(), seqs.c_struct()
+    _check(lib().pkv_quantize_kv_blocks(ctypes.byref(c), _ptr(k_new), _ptr(v_new), _DT[k_new.dtype],
+                                        int(k_new.shape[0]), _ptr(cu_new_lens), ctypes.byref(s), _err_ptr(err_flags),
+                                        _stream(stream)))
 
 
 def pkv_paged_attention(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
@@ -424,7 +473,7 @@ def pkv_gather_kv_cache(k_out: torch.Tensor, v_out: torch.Tensor, cu_seq_lens: t
 
 def pkv_gather_kv_cache_dequant(k_out: torch.Tensor, v_out: torch.Tensor, cu_seq_lens: torch.Tensor, cache: Cache,
                                 seqs: Seqs, err_flags=None, stream=None) -> None:
-    """K8/V4 cache -> contiguous fp16/bf16 (the dtype of k_out) K and V rows."""
+    """K8/V4, int8 or e4m3 cache -> contiguous fp16/bf16 (the dtype of k_out) K and V rows."""
     if cu_seq_lens.dtype != torch.int32:
         raise ValueError("cu_seq_lens must be int32")
     if k_out.dtype != v_out.dtype or k_out.dtype not in (torch.float16, torch.bfloat16):
