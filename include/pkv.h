@@ -208,6 +208,68 @@ pkv_status pkv_quantize_kv_blocks(const pkv_cache *cache, const void *k_new, con
                                   const pkv_seqs *seqs, uint32_t *err_flags, pkv_stream_t stream);
 
 /*
+ * Rotary positions.  A head's first rotary_dim dims are turned pair by pair by
+ * the angle position * frequency: pair i is dims (i, i + rotary_dim/2) in the
+ * half layout, (2i, 2i + 1) in the interleaved one; the other dims are kept.
+ *   (a, b) -> (a c - b s, b c + a s),  c = mscale cos, s = mscale sin
+ */
+typedef enum pkv_rope_layout { PKV_ROPE_HALF = 0, PKV_ROPE_INTERLEAVED = 1 } pkv_rope_layout;
+
+typedef struct pkv_rope {
+    const uint64_t *freq;  /* device [rotary_dim/2]: turns per position, times 2^64 (pkv_rope_frequencies) */
+    int32_t rotary_dim;    /* even, 2 .. head_dim */
+    int32_t layout;        /* pkv_rope_layout */
+    float mscale;          /* multiplies the cosines and sines (1: none) */
+} pkv_rope;
+
+typedef enum pkv_rope_scale {
+    PKV_ROPE_SCALE_NONE = 0,     /* theta_i = base^(-2i / rotary_dim) radians per position */
+    PKV_ROPE_SCALE_LINEAR = 1,   /* theta_i / factor */
+    PKV_ROPE_SCALE_NTK = 2,      /* base * factor^(rotary_dim / (rotary_dim - 2)) in base's place */
+    PKV_ROPE_SCALE_BY_PARTS = 3  /* by the turns r a pair makes in original_context positions: theta_i where
+                                    r >= high_rotations, theta_i / factor where r <= low_rotations, and
+                                    between them the two mixed in proportion to r */
+} pkv_rope_scale;
+
+typedef struct pkv_rope_scaling {
+    int32_t kind;          /* pkv_rope_scale */
+    double factor;
+    double low_rotations, high_rotations, original_context;   /* by parts only */
+} pkv_rope_scaling;
+
+/*
+ * The frequencies of a rotary table, on the HOST: freq [rotary_dim/2] as 64-bit
+ * fractions of a turn, to be copied to the device once.  scaling may be NULL.
+ */
+pkv_status pkv_rope_frequencies(uint64_t *freq, int32_t rotary_dim, double base, const pkv_rope_scaling *scaling);
+
+/*
+ * Rotate q and k of num_tokens tokens, and write the rotated keys and the values
+ * into their cache slots, in one launch.
+ *   q, q_out   rows of [num_heads, head_dim], consecutive rows q_stride /
+ *              q_out_stride ELEMENTS apart (a packed q/k/v projection has its full
+ *              width here); dtype PKV_F16 or PKV_BF16.
+ *   k, v       rows of [num_kv_heads, head_dim], likewise.
+ *   k_out      the rotated keys as rows, or NULL.
+ *   Strides are multiples of 8 and at least a row.  q_out may be q and k_out may
+ *   be k (same address and stride); outputs overlap no input otherwise.
+ *   cache      an fp16 / bf16 cache of `dtype`, or NULL for no write (then v and
+ *              slot_mapping are ignored and k_out is needed).  For a quantised cache
+ *              take k_out and call its own write.
+ *   positions  int64 [num_tokens], any value (negative too): the angle is exact to
+ *              2^-25 of a half-turn at every position.
+ *   slot_mapping  as for pkv_reshape_and_cache.  A token without a slot is rotated
+ *              all the same.
+ * Sums and products are fp32, rounded once.  num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_rope_and_cache(const pkv_cache *cache, const pkv_rope *rope, void *q_out, int64_t q_out_stride,
+                              const void *q, int64_t q_stride, int32_t num_heads, void *k_out,
+                              int64_t k_out_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, int32_t num_kv_heads, int32_t head_dim, pkv_dtype dtype,
+                              const int64_t *positions, const int64_t *slot_mapping, int32_t num_tokens,
+                              uint32_t *err_flags, pkv_stream_t stream);
+
+/*
  * Single-pass paged decode attention [METAL: the pagedattention kernel, the GQA
  * stride trick kv_head = q_head / gqa_factor; MTPLX-2 §"Kernel Interface and
  * Memory Slicing": only the stored tokens are read].

@@ -3,6 +3,7 @@
 // allocates device memory and nothing is cached between calls.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -345,6 +346,112 @@ pkv_status pkv_quantize_kv_blocks(const pkv_cache* cache, const void* k_new, con
     p.src_dtype = src_dtype;
     p.err = err_flags;
     return cuda_result(pkv::launch_append_blocks(p, reinterpret_cast<cudaStream_t>(stream)), "quantize_kv_blocks launch");
+}
+
+pkv_status pkv_rope_frequencies(uint64_t* freq, int32_t rotary_dim, double base, const pkv_rope_scaling* scaling) {
+    if (!freq) return fail(PKV_ERR_INVALID_ARG, "freq is NULL");
+    if (rotary_dim < 2 || rotary_dim % 2 != 0) return fail(PKV_ERR_INVALID_ARG, "rotary_dim %d (even, 2 or more)", rotary_dim);
+    if (!(base > 0.0) || !std::isfinite(base)) return fail(PKV_ERR_INVALID_ARG, "base %g", base);
+    const int32_t kind = scaling ? scaling->kind : PKV_ROPE_SCALE_NONE;
+    double factor = 1.0;
+    if (kind != PKV_ROPE_SCALE_NONE) {
+        if (kind != PKV_ROPE_SCALE_LINEAR && kind != PKV_ROPE_SCALE_NTK && kind != PKV_ROPE_SCALE_BY_PARTS)
+            return fail(PKV_ERR_INVALID_ARG, "unknown scaling kind %d", kind);
+        factor = scaling->factor;
+        if (!(factor > 0.0) || !std::isfinite(factor)) return fail(PKV_ERR_INVALID_ARG, "scaling factor %g", factor);
+    }
+    if (kind == PKV_ROPE_SCALE_BY_PARTS &&
+        !(scaling->high_rotations > scaling->low_rotations && scaling->original_context > 0.0))
+        return fail(PKV_ERR_INVALID_ARG, "by-parts scaling wants low_rotations < high_rotations and an original_context");
+    if (kind == PKV_ROPE_SCALE_NTK && rotary_dim > 2) base *= std::pow(factor, double(rotary_dim) / (rotary_dim - 2));
+    constexpr double kTwoPi = 6.283185307179586;
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double theta = std::pow(base, -2.0 * i / rotary_dim);   // radians a position
+        if (kind == PKV_ROPE_SCALE_LINEAR) theta /= factor;
+        if (kind == PKV_ROPE_SCALE_BY_PARTS) {
+            const double rotations = scaling->original_context * theta / kTwoPi;
+            double keep = (rotations - scaling->low_rotations) / (scaling->high_rotations - scaling->low_rotations);
+            keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+            theta = theta / factor * (1.0 - keep) + theta * keep;
+        }
+        const double turns = theta / kTwoPi;
+        if (!std::isfinite(turns)) return fail(PKV_ERR_INVALID_ARG, "frequency %d is not finite", i);
+        freq[i] = uint64_t(std::ldexp(turns - std::floor(turns), 64));   // below 2^64: the fraction is at most 1 - 2^-53
+    }
+    return ok();
+}
+
+pkv_status pkv_rope_and_cache(const pkv_cache* cache, const pkv_rope* rope, void* q_out, int64_t q_out_stride,
+                              const void* q, int64_t q_stride, int32_t num_heads, void* k_out, int64_t k_out_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t num_kv_heads,
+                              int32_t head_dim, pkv_dtype dtype, const int64_t* positions, const int64_t* slot_mapping,
+                              int32_t num_tokens, uint32_t* err_flags, pkv_stream_t stream) {
+    pkv_status st;
+    if (cache) {
+        if ((st = check_cache(cache, true)) != PKV_OK) return st;
+        if (cache->num_kv_heads != num_kv_heads || cache->head_dim != head_dim || cache_dtype(cache) != int(dtype))
+            return fail(PKV_ERR_INVALID_ARG, "num_kv_heads, head_dim and dtype must be the cache's");
+    }
+    if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope is NULL");
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return fail(PKV_ERR_INVALID_ARG, "dtype %d", dtype);
+    if (head_dim != 64 && head_dim != 128) return fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", head_dim);
+    if (num_heads < 1 || num_heads > 65535) return fail(PKV_ERR_INVALID_ARG, "num_heads %d", num_heads);
+    if (num_kv_heads < 1 || num_kv_heads > 65535) return fail(PKV_ERR_INVALID_ARG, "num_kv_heads %d", num_kv_heads);
+    if (rope->rotary_dim < 2 || rope->rotary_dim % 2 != 0 || rope->rotary_dim > head_dim)
+        return fail(PKV_ERR_INVALID_ARG, "rotary_dim %d (even, 2 .. head_dim)", rope->rotary_dim);
+    if (rope->layout != PKV_ROPE_HALF && rope->layout != PKV_ROPE_INTERLEAVED)
+        return fail(PKV_ERR_INVALID_ARG, "layout %d", rope->layout);
+    if (!(rope->mscale == rope->mscale)) return fail(PKV_ERR_INVALID_ARG, "mscale is NaN");
+    if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens %d", num_tokens);
+    const int64_t wq = int64_t(num_heads) * head_dim, wk = int64_t(num_kv_heads) * head_dim;
+    const struct { const char* name; int64_t stride, width; bool used; } rows[] = {
+        {"q_stride", q_stride, wq, true}, {"q_out_stride", q_out_stride, wq, true}, {"k_stride", k_stride, wk, true},
+        {"k_out_stride", k_out_stride, wk, k_out != nullptr}, {"v_stride", v_stride, wk, cache != nullptr}};
+    for (const auto& r : rows)
+        if (r.used && (r.stride < r.width || r.stride % 8 != 0))
+            return fail(PKV_ERR_INVALID_ARG, "%s %lld: at least a row (%lld) and a multiple of 8", r.name,
+                        (long long)r.stride, (long long)r.width);
+    if (num_tokens == 0) return ok();
+    CHECK_PTR(q, "q");
+    CHECK_PTR(q_out, "q_out");
+    CHECK_PTR(k, "k");
+    if (k_out) CHECK_PTR(k_out, "k_out");
+    if (!k_out && !cache) return fail(PKV_ERR_INVALID_ARG, "neither k_out nor a cache takes the keys");
+    if (cache) {
+        CHECK_PTR(v, "v");
+        if (!slot_mapping) return fail(PKV_ERR_INVALID_ARG, "slot_mapping is NULL");
+    }
+    if (!positions) return fail(PKV_ERR_INVALID_ARG, "positions is NULL");
+    if (!rope->freq) return fail(PKV_ERR_INVALID_ARG, "rope->freq is NULL");
+    pkv::RopeParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    if (cache) {
+        p.k_cache = cache->k;
+        p.v_cache = cache->v;
+        p.slot_mapping = slot_mapping;
+        p.num_blocks = cache->num_blocks;
+    }
+    p.positions = positions;
+    p.freq = rope->freq;
+    p.mscale = rope->mscale;
+    p.rotary_dim = rope->rotary_dim;
+    p.layout = rope->layout;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.dtype = dtype;
+    p.err = err_flags;
+    return cuda_result(pkv::launch_rope(p, reinterpret_cast<cudaStream_t>(stream)), "rope launch");
 }
 
 pkv_status pkv_paged_attention(void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, int32_t num_heads,

@@ -227,6 +227,28 @@ struct BlockWriteParams {
 };
 cudaError_t launch_append_blocks(BlockWriteParams p, cudaStream_t stream);
 
+// Rotary positions (rope.cu): q -> q_out, k -> k_out and / or its cache slot, v -> its cache slot.
+struct RopeParams {
+    const void* q;                // rows of [num_heads, head_dim], q_stride elements apart
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_out;                  // null: none
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    void* k_cache;
+    void* v_cache;
+    const int64_t* slot_mapping;  // null: no cache write
+    const int64_t* positions;
+    const uint64_t* freq;         // [rotary_dim / 2] turns per position, times 2^64
+    float mscale;
+    int32_t rotary_dim, layout;
+    int32_t num_tokens, num_heads, num_kv_heads, head_dim, num_blocks;
+    int32_t dtype;
+    int32_t tokens_per_cta;       // set by the launcher
+    uint32_t* err;
+};
+cudaError_t launch_rope(RopeParams p, cudaStream_t stream);
+
 struct GatherParams {
     void* k_out;
     void* v_out;

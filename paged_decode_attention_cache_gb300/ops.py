@@ -42,6 +42,16 @@ class _Cache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("v_zero", ctypes.c_void_p)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("low_rotations", ctypes.c_double),
+                ("high_rotations", ctypes.c_double), ("original_context", ctypes.c_double)]
+
+
 class _Seqs(ctypes.Structure):
     _fields_ = [("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
                 ("num_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("q_len", ctypes.c_int32),
@@ -51,6 +61,7 @@ class _Seqs(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 
 _lib_path: Optional[str] = None   # None: libpkv.so (build.LIB)
@@ -84,6 +95,11 @@ def lib():
         L.pkv_quantize_kv.argtypes = [_P, _P, _P, ctypes.c_int, _P, _I32, _P, _P]
         L.pkv_quantize_kv_blocks.restype = st
         L.pkv_quantize_kv_blocks.argtypes = [_P, _P, _P, ctypes.c_int, _I32, _P, _P, _P, _P]
+        L.pkv_rope_frequencies.restype = st
+        L.pkv_rope_frequencies.argtypes = [_P, _I32, ctypes.c_double, _P]
+        L.pkv_rope_and_cache.restype = st
+        L.pkv_rope_and_cache.argtypes = [_P, _P, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I64, _I32, _I32,
+                                         ctypes.c_int, _P, _P, _I32, _P, _P]
         L.pkv_paged_attention.restype = st
         L.pkv_paged_attention.argtypes = [_P, ctypes.c_int, _P, ctypes.c_int, _I32, ctypes.c_float, _P, _P, _P, _P]
         L.pkv_split_workspace_bytes.restype = ctypes.c_size_t
@@ -275,6 +291,85 @@ def pkv_quantize_kv_blocks(cache: Cache, k_new: torch.Tensor, v_new: torch.Tenso
     _check(lib().pkv_quantize_kv_blocks(ctypes.byref(c), _ptr(k_new), _ptr(v_new), _DT[k_new.dtype],
                                         int(k_new.shape[0]), _ptr(cu_new_lens), ctypes.byref(s), _err_ptr(err_flags),
                                         _stream(stream)))
+
+
+_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_ROPE_SCALE = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+@dataclass
+class Rope:
+    """Rotary positions of a model: its frequencies (pkv_rope_frequencies, on the device) and layout."""
+    freq: torch.Tensor        # int64 [rotary_dim / 2]: turns per position, times 2^64
+    rotary_dim: int
+    layout: str = "half"      # "half": pairs (i, i + rotary_dim/2); "interleaved": pairs (2i, 2i + 1)
+    mscale: float = 1.0
+
+    def c_struct(self) -> _Rope:
+        if self.freq.dtype != torch.int64 or self.freq.numel() * 2 != self.rotary_dim:
+            raise ValueError("freq must be int64 [rotary_dim / 2]")
+        if self.layout not in _ROPE_LAYOUT:
+            raise ValueError(f"layout {self.layout!r}: 'half' or 'interleaved'")
+        return _Rope(_ptr(self.freq), int(self.rotary_dim), _ROPE_LAYOUT[self.layout], float(self.mscale))
+
+
+def pkv_rope_frequencies(rotary_dim: int, base: float, scaling: str = "none", factor: float = 1.0,
+                         low_rotations: float = 1.0, high_rotations: float = 32.0,
+                         original_context: float = 0.0) -> torch.Tensor:
+    """The frequencies of a rotary table (host int64 [rotary_dim / 2]; copy it to
+    the device once), plain or scaled for longer contexts: "linear", "ntk" or
+    "by_parts"."""
+    if scaling not in _ROPE_SCALE:
+        raise ValueError(f"scaling {scaling!r}: one of {sorted(_ROPE_SCALE)}")
+    freq = torch.zeros(max(int(rotary_dim), 0) // 2, dtype=torch.int64)
+    sc = _RopeScaling(_ROPE_SCALE[scaling], float(factor), float(low_rotations), float(high_rotations),
+                      float(original_context))
+    _check(lib().pkv_rope_frequencies(ctypes.c_void_p(freq.data_ptr()), int(rotary_dim), float(base), ctypes.byref(sc)))
+    return freq
+
+
+def _rows(t: torch.Tensor, name: str, heads: int, head_dim: int, tokens: int, dtype: torch.dtype):
+    """Address and row stride of a [tokens, heads, head_dim] view whose rows are contiguous."""
+    if t.dtype != dtype or tuple(t.shape) != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must be {dtype} [{tokens}, {heads}, {head_dim}]")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != head_dim and heads > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    # one row (or none): any stride will do
+    return ctypes.c_void_p(t.data_ptr()), s[0] if tokens > 1 else heads * head_dim
+
+
+def pkv_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], rope: Rope,
+                       positions: torch.Tensor, cache: Optional[Cache] = None,
+                       slot_mapping: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                       err_flags: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotate q into q_out and k into its cache slot and / or k_out, and write v
+    into its slot, in one launch.  q, k, v may be views of one packed projection
+    (any row stride that is a multiple of 8); q_out may be q and k_out may be k."""
+    T, H, D = (int(x) for x in q.shape)
+    Hkv = int(k.shape[1])
+    if positions.dtype != torch.int64 or positions.numel() != T:
+        raise ValueError("positions must be int64 [num_tokens]")
+    if cache is not None and (v is None or slot_mapping is None):
+        raise ValueError("a cache write needs v and slot_mapping")
+    if slot_mapping is not None and (slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T):
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    _one_device(q_out, q, k, v, rope.freq, positions, slot_mapping, k_out, err_flags,
+                *((cache.k, cache.v) if cache is not None else ()))
+    dt = q.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16")
+    qp, qs = _rows(q, "q", H, D, T, dt)
+    qop, qos = _rows(q_out, "q_out", H, D, T, dt)
+    kp, ks = _rows(k, "k", Hkv, D, T, dt)
+    vp, vs = _rows(v, "v", Hkv, D, T, dt) if cache is not None else (None, 0)
+    kop, kos = _rows(k_out, "k_out", Hkv, D, T, dt) if k_out is not None else (None, 0)
+    r = rope.c_struct()
+    _check(lib().pkv_rope_and_cache(ctypes.byref(cache.c_struct()) if cache is not None else None, ctypes.byref(r), qop,
+                                    qos, qp, qs, H, kop, kos, kp, ks, vp, vs, Hkv, D, _DT[dt], _ptr(positions),
+                                    _ptr(slot_mapping) if cache is not None else None, T, _err_ptr(err_flags),
+                                    _stream(stream)))
+    return q_out
 
 
 def pkv_paged_attention(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
