@@ -365,6 +365,44 @@ pkv_status pkv_paged_attention_balanced(void *out, pkv_dtype out_dtype, const vo
                                         uint32_t *err_flags, pkv_stream_t stream);
 
 /*
+ * What pkv_paged_attention_scored does between scale * q.k and the softmax.  Any
+ * part may be off; the order is cap, bias, mask.
+ *   softcap          c > 0: x -> c tanh(x / c); 0: none.
+ *   distance_slopes  fp32 [num_heads] device, or NULL.  x += slope[h] * (pos - qpos),
+ *                    where row j of sequence s sits at qpos = context_lens[s] - q_len + j.
+ *   doc_starts       int32 [num_seqs] device, or NULL: only tokens at or after
+ *                    doc_starts[s] are visible (the sequence holds several documents
+ *                    and this is where the current one begins).  One at or past
+ *                    context_lens[s] leaves the sequence's rows empty: zeros.
+ *   prefix_lens      int32 [num_seqs] device, or NULL: tokens [0, prefix_lens[s])
+ *                    stay visible whatever the window and the document leave out.
+ * Row j sees token t if t <= qpos and (t < prefix_lens[s] or t is at or after
+ * doc_starts[s] and in the sliding window).  Blocks without a visible token are
+ * not read.  Negative starts and prefixes count as 0.
+ */
+typedef struct pkv_scores {
+    float softcap;
+    const float *distance_slopes;
+    const int32_t *doc_starts;
+    const int32_t *prefix_lens;
+} pkv_scores;
+
+/*
+ * pkv_paged_attention_balanced with the scores of `scores`, over every cache
+ * kind, for decode and verify blocks; arguments, workspace (of the same size) and
+ * result otherwise the same.  A non-finite K or V of a token that the context,
+ * the window, the document and the prefix leave out reaches no output; one of a
+ * draft reaches the rows of that draft and of the drafts before it in its block.
+ * distance_slopes, doc_starts and prefix_lens are read before the previous
+ * kernel of this library on `stream` has ended (like context_lens): no call of
+ * this library writes them.
+ */
+pkv_status pkv_paged_attention_scored(void *out, pkv_dtype out_dtype, const void *q, pkv_dtype q_dtype,
+                                      int32_t num_heads, float scale, const pkv_cache *cache,
+                                      const pkv_seqs *seqs, const pkv_scores *scores, void *workspace,
+                                      size_t workspace_bytes, uint32_t *err_flags, pkv_stream_t stream);
+
+/*
  * One decode step in one launch: the cache write of the step's new tokens
  * (pkv_reshape_and_cache, or pkv_quantize_kv for a K8V4 cache) and the balanced
  * attention of pkv_paged_attention_balanced, with the same results as those two

@@ -234,7 +234,7 @@ pkv_status attn_setup(pkv::AttnParams* p, const void* q, pkv_dtype q_dtype, int3
 }
 
 pkv_status attn_launch(pkv::AttnParams p, const pkv_cache* cache, int gqa, pkv_stream_t stream) {
-    const bool tc = pkv::attention_uses_tensor_cores(cache->kind, p.q_len, gqa, pkv::is_cascade_pass(p));
+    const bool tc = pkv::attention_uses_tensor_cores(cache->kind, p.q_len, gqa, pkv::is_cascade_pass(p) || p.scored != 0);
     CUtensorMap km, vm;
     pkv_status st = cache_maps(cache, &km, &vm, tc);
     if (st != PKV_OK) return st;
@@ -564,6 +564,27 @@ pkv_status pkv_paged_attention_balanced(void* out, pkv_dtype out_dtype, const vo
     if (st != PKV_OK) return st;
     if ((st = balanced_setup(p, out, out_dtype, cache, seqs, workspace, workspace_bytes)) != PKV_OK) return st;
     if (seqs->num_seqs == 0) return ok();
+    return attn_launch(p, cache, gqa, stream);
+}
+
+pkv_status pkv_paged_attention_scored(void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype,
+                                      int32_t num_heads, float scale, const pkv_cache* cache, const pkv_seqs* seqs,
+                                      const pkv_scores* scores, void* workspace, size_t workspace_bytes,
+                                      uint32_t* err_flags, pkv_stream_t stream) {
+    pkv::AttnParams p;
+    int gqa = 0;
+    pkv_status st = attn_setup(&p, q, q_dtype, num_heads, scale, cache, seqs, err_flags, &gqa);
+    if (st != PKV_OK) return st;
+    if (!scores) return fail(PKV_ERR_INVALID_ARG, "scores is NULL");
+    if (!(scores->softcap >= 0.f) || !std::isfinite(scores->softcap) || (scores->softcap > 0.f && scores->softcap < 1e-30f))
+        return fail(PKV_ERR_INVALID_ARG, "softcap %g (0, or 1e-30 and more)", double(scores->softcap));
+    if ((st = balanced_setup(p, out, out_dtype, cache, seqs, workspace, workspace_bytes)) != PKV_OK) return st;
+    if (seqs->num_seqs == 0) return ok();
+    p.scored = 1;
+    p.softcap = scores->softcap;
+    p.slopes = scores->distance_slopes;
+    p.doc_starts = scores->doc_starts;
+    p.prefix_lens = scores->prefix_lens;
     return attn_launch(p, cache, gqa, stream);
 }
 

@@ -78,6 +78,7 @@ struct TeMath {
     int lim[NT][2];
     int lo_;       // first visible token
     int lim_lo_;   // smallest lim over this thread's live columns (no live column: INT_MAX)
+    ScoreMod<2 * NT> mod_;   // query columns 8 nt + 2t, + 1
     float scale_log2_;
 
     static __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* vm,
@@ -98,17 +99,18 @@ struct TeMath {
     __device__ __forceinline__ void init(int) {}
 
     // query column n = head (n / q_len), draft (n % q_len)
-    template <bool CASC>
+    template <int VAR>
     __device__ __forceinline__ void begin(const AttnParams& p, int s, int kvh, int ctx, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int G = p.num_heads / p.num_kv_heads, QL = p.q_len, M = G * QL;
-        lo_ = visible_lo<CASC>(p, s, ctx);
+        lo_ = visible_lo<VAR>(p, s, ctx);
+        if constexpr (VAR == kScored) mod_.begin(p, s, ctx);
         lim_lo_ = INT_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int n = 8 * nt + g;
             const int h = n < M ? n / QL : 0, j = n < M ? n % QL : 0;
-            const int qr = n < M ? query_row<CASC>(p, s, j) : -1;
+            const int qr = n < M ? query_row<VAR>(p, s, j) : -1;
             const bool valid = qr >= 0;
             const size_t qoff = (size_t(valid ? qr : 0) * p.num_heads + kvh * G + h) * D;
             // this thread's dims t*D/4 .. t*D/4 + D/4 - 1: D/2 contiguous bytes, as 16-byte loads
@@ -152,9 +154,10 @@ struct TeMath {
             for (int e = 0; e < 2; ++e) {
                 const int n2 = 8 * nt + 2 * t + e;
                 const int j2 = n2 % QL;
-                const bool ok2 = n2 < M && query_row<CASC>(p, s, j2) >= 0;
+                if constexpr (VAR == kScored) mod_.column(p, 2 * nt + e, kvh * G + (n2 < M ? n2 / QL : 0), j2, ctx);
+                const bool ok2 = n2 < M && query_row<VAR>(p, s, j2) >= 0;
                 // a cascade row (one decode query) sees the entry's whole context; verify rows are causal
-                lim[nt][e] = ok2 ? (CASC ? ctx : max(0, ctx - QL + j2 + 1)) : 0;
+                lim[nt][e] = ok2 ? (VAR == kCascade ? ctx : max(0, ctx - QL + j2 + 1)) : 0;
                 if (lim[nt][e] > 0) lim_lo_ = min(lim_lo_, lim[nt][e]);
                 m_run[nt][e] = -INFINITY;
                 l_part[nt][e] = 0.f;
@@ -164,6 +167,7 @@ struct TeMath {
         }
     }
 
+    template <int VAR>
     __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int /*ntok*/, uint8_t*, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const uint32_t stg_a = smem_addr(stg);
@@ -201,10 +205,17 @@ struct TeMath {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float k = ss.x * kcol[nt][e];
-                const bool v0 = all ? lim[nt][e] > 0 : (pg < lim[nt][e] && pg >= lo_);
-                const bool v1 = all ? lim[nt][e] > 0 : (pg8 < lim[nt][e] && pg8 >= lo_);
-                sc[nt][e] = v0 ? sc[nt][e] * k : -INFINITY;
-                sc[nt][2 + e] = v1 ? sc[nt][2 + e] * k : -INFINITY;
+                if constexpr (VAR == kScored) {
+                    const bool v0 = pg < lim[nt][e] && (pg >= lo_ || pg < mod_.pre);
+                    const bool v1 = pg8 < lim[nt][e] && (pg8 >= lo_ || pg8 < mod_.pre);
+                    sc[nt][e] = v0 ? mod_(sc[nt][e] * k, pg, 2 * nt + e) : -INFINITY;
+                    sc[nt][2 + e] = v1 ? mod_(sc[nt][2 + e] * k, pg8, 2 * nt + e) : -INFINITY;
+                } else {
+                    const bool v0 = all ? lim[nt][e] > 0 : (pg < lim[nt][e] && pg >= lo_);
+                    const bool v1 = all ? lim[nt][e] > 0 : (pg8 < lim[nt][e] && pg8 >= lo_);
+                    sc[nt][e] = v0 ? sc[nt][e] * k : -INFINITY;
+                    sc[nt][2 + e] = v1 ? sc[nt][2 + e] * k : -INFINITY;
+                }
             }
         // ------------------------------------------------ online softmax per query column
         float alpha[NT][2];
@@ -310,6 +321,16 @@ struct TeMath {
             }
     }
 };
+
+template <bool E4M3, int VAR>
+cudaError_t dispatch_byte(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+    const bool narrow = (p.num_heads / p.num_kv_heads) * p.q_len <= 8;
+    if (p.head_dim == 128)
+        return narrow ? launch_math<TeMath<E4M3, 128, 1>, false, VAR>(p, km, vm, st)
+                      : launch_math<TeMath<E4M3, 128, 2>, false, VAR>(p, km, vm, st);
+    return narrow ? launch_math<TeMath<E4M3, 64, 1>, false, VAR>(p, km, vm, st)
+                  : launch_math<TeMath<E4M3, 64, 2>, false, VAR>(p, km, vm, st);
+}
 
 }  // namespace
 

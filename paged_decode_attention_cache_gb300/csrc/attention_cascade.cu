@@ -11,7 +11,7 @@ namespace pkv {
 
 cudaError_t launch_attention_cascade(AttnParams p, int cache_kind, int gqa, const CUtensorMap& km,
                                      const CUtensorMap& vm, cudaStream_t stream) {
-    return launch_attention_impl<false, true>(p, cache_kind, gqa, km, vm, stream);
+    return launch_attention_impl<false, kCascade>(p, cache_kind, gqa, km, vm, stream);
 }
 
 }  // namespace pkv

@@ -79,24 +79,94 @@ __host__ __device__ constexpr int ob_idx(int m, int d, int D) { return m * D + (
 
 // ---------------------------------------------------------------- small device helpers
 
-// CASC: the kernel runs cascade attention's pass over its list (the items'
-// shared prefixes, then every sequence from its seq_start on), where entry s
-// reads the table of item_seq[s] for the query rows row_map[s * q_len + j];
-// the other kernels compile without those reads.
+// 2^x by the hardware's approximate exponential with subnormal results
+// flushed to zero (a weight below 2^-126 of the row maximum)
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// VAR, what the kernel is compiled for:
+//   kPlain    every sequence's stored tokens, or the last `window` of them;
+//   kCascade  cascade attention's pass over its list (the items' shared prefixes,
+//             then every sequence from its seq_start on), where entry s reads the
+//             table of item_seq[s] for the query rows row_map[s * q_len + j];
+//   kScored   scores capped and biased by distance, tokens masked by document
+//             and prefix (ScoreMod).
+// Each compiles without the others' reads.
+constexpr int kPlain = 0, kCascade = 1, kScored = 2;
 
 // First visible token of list entry s: a sliding window keeps the last `window`
 // stored tokens [MTPLX-2 §"Sliding-Window Memory Control"]; a cascade entry
 // starts at its seq_start (past its item's shared prefix).
-template <bool CASC>
+template <int VAR>
 __device__ __forceinline__ int visible_lo(const AttnParams& p, int s, int ctx) {
-    if constexpr (CASC) return min(max(p.seq_start[s], 0), ctx);
-    return (p.window > 0 && ctx > p.window) ? ctx - p.window : 0;
+    if constexpr (VAR == kCascade) return min(max(p.seq_start[s], 0), ctx);
+    const int lo = (p.window > 0 && ctx > p.window) ? ctx - p.window : 0;
+    if constexpr (VAR == kScored)
+        if (p.doc_starts) return max(lo, min(p.doc_starts[s], ctx));   // its document begins there
+    return lo;
 }
 
+// Scored: the first tokens of sequence s that stay visible whatever its window and document leave out.
+__device__ __forceinline__ int prefix_tokens(const AttnParams& p, int s, int ctx) {
+    return p.prefix_lens ? min(max(p.prefix_lens[s], 0), ctx) : 0;
+}
+
+// The blocks of a sequence that hold a visible token: [0, npre), then from npre + hole on.
+struct Span {
+    int npre, hole;
+};
+template <int VAR>
+__device__ __forceinline__ Span visible_blocks(const AttnParams& p, int s, int ctx) {
+    const int lo = visible_lo<VAR>(p, s, ctx);
+    const int first = lo >= ctx ? (ctx + kBS - 1) / kBS : lo / kBS;
+    const int npre = min((prefix_tokens(p, s, ctx) + kBS - 1) / kBS, first);
+    return {npre, first - npre};
+}
+
+// What a scored pass does to a base-2 score x = log2e * scale * q.k of one of
+// this thread's N query columns (or rows):
+//   cap   x -> c tanh(x / c), c = cap * log2e.  With e = 2^(2x / cap) that is
+//         c - 2c / (1 + e), whose error is about 2^-23 of c; below |x| = c / 4,
+//         where it would cancel, the odd series of tanh to the seventh order
+//         (next term under 4e-7 of x).  Two MUFU operations and a dozen others
+//         per score, 4 to 8 scores per thread and block.
+//   bias  x += slope * log2e * (position - the query's position).
+template <int N>
+struct ScoreMod {
+    float cap2, two_over_cap, inv_cap2;   // cap2 0: no cap
+    float slope2[N];
+    int qpos[N];
+    int pre;   // prefix tokens
+
+    __device__ __forceinline__ void begin(const AttnParams& p, int s, int ctx) {
+        cap2 = p.softcap * kLog2e;
+        two_over_cap = p.softcap > 0.f ? 2.f / p.softcap : 0.f;
+        inv_cap2 = p.softcap > 0.f ? 1.f / cap2 : 0.f;
+        pre = prefix_tokens(p, s, ctx);
+    }
+    // column i is head `head`, draft j
+    __device__ __forceinline__ void column(const AttnParams& p, int i, int head, int j, int ctx) {
+        slope2[i] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
+        qpos[i] = ctx - p.q_len + j;
+    }
+    __device__ __forceinline__ float operator()(float x, int pos, int i) const {
+        if (cap2 > 0.f) {
+            const float u = x * inv_cap2, u2 = u * u;
+            const float series = x * fmaf(u2, fmaf(u2, fmaf(u2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+            const float whole = cap2 - __fdividef(2.f * cap2, 1.f + exp2_ftz(x * two_over_cap));
+            x = fabsf(u) < 0.25f ? series : whole;
+        }
+        return slope2[i] != 0.f ? fmaf(slope2[i], float(pos - qpos[i]), x) : x;
+    }
+};
+
 // q / output row of row j of list entry s; < 0: no row
-template <bool CASC>
+template <int VAR>
 __device__ __forceinline__ int query_row(const AttnParams& p, int s, int j) {
-    if constexpr (CASC) return p.row_map[s * p.q_len + j];
+    if constexpr (VAR == kCascade) return p.row_map[s * p.q_len + j];
     return s * p.q_len + j;
 }
 
@@ -174,14 +244,6 @@ __device__ __forceinline__ void s8x4_to_f16x4_biased(uint32_t w, uint32_t& lo, u
     const uint32_t x = w ^ 0x80808080u;
     lo = __byte_perm(x, 0x64646464u, 0x5140);
     hi = __byte_perm(x, 0x64646464u, 0x7362);
-}
-
-// 2^x by the hardware's approximate exponential with subnormal results
-// flushed to zero (a weight below 2^-126 of the row maximum)
-__device__ __forceinline__ float exp2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // Nibble i of both 16-bit halves of w -> fp16x2 of the exact integers 0..15.
@@ -282,10 +344,10 @@ struct CcMath {
         writer = (jl & (LPT / G - 1)) == 0;
     }
 
-    template <bool CASC>
+    template <int VAR>
     __device__ __forceinline__ void begin(const AttnParams& p, int s, int kvh, int ctx, int lane) {
         const int jl = lane % LPT;
-        lo_ = visible_lo<CASC>(p, s, ctx);
+        lo_ = visible_lo<VAR>(p, s, ctx);
         const T* qrow = reinterpret_cast<const T*>(p.q) + (size_t(s) * p.num_heads + kvh * G) * D;
 #pragma unroll
         for (int h = 0; h < G; ++h)
@@ -307,7 +369,9 @@ struct CcMath {
             for (int e = 0; e < DPL / 2; ++e) acc[h][e] = make_float2(0.f, 0.f);
     }
 
+    template <int VAR>
     __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int ntok, uint8_t* scratch, int lane) {
+        static_assert(VAR == kPlain, "the scored and cascade passes take the tensor-core maths");
         float* sc = reinterpret_cast<float*>(scratch);
         float2* pc = reinterpret_cast<float2*>(scratch + kBS * G * 4);
         float* alph = reinterpret_cast<float*>(scratch + kBS * G * 12);
@@ -436,6 +500,22 @@ struct CcMath {
 
 // ---------------------------------------------------------------- tensor-core block math
 
+// Operand masks that zero the tokens t2, t2 + 1 (m01) and 8 + t2, 9 + t2 (m23) of
+// a block where they lie past the context or, in a scored pass, are masked for
+// every row; true if the block needs none.
+template <int VAR, int N>
+__device__ __forceinline__ bool token_masks(const ScoreMod<N>& mod, int lo, int pos0, int ntok, int t2, uint32_t& m01,
+                                            uint32_t& m23) {
+    auto in = [&](int t) {
+        if constexpr (VAR == kScored) return t < ntok && (pos0 + t >= lo || pos0 + t < mod.pre);
+        return t < ntok;
+    };
+    m01 = (in(t2) ? 0x0000ffffu : 0u) | (in(t2 + 1) ? 0xffff0000u : 0u);
+    m23 = (in(8 + t2) ? 0x0000ffffu : 0u) | (in(9 + t2) ? 0xffff0000u : 0u);
+    if constexpr (VAR == kScored) return ntok == kBS && pos0 >= lo;
+    return ntok == kBS;
+}
+
 // Multi-token verify blocks on fp16 / bf16 caches: the 16-row query tile (g
 // heads x q_len drafts) against a 16-token block.
 template <int KIND, int D>
@@ -467,6 +547,7 @@ struct TcMath {
     float m_run[2], l_run[2];
     int lim[2];
     int lo_;   // first visible token (sliding window)
+    ScoreMod<2> mod_;   // rows g, g + 8
 
     static __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* vm,
                                                  const AttnParams&, int kvh, int pb, uint64_t* bar) {
@@ -493,21 +574,23 @@ struct TcMath {
     __device__ __forceinline__ void init(int) {}
 
     // rows g and g+8 of the 16-row tile: row m = head (m / q_len), draft (m % q_len)
-    template <bool CASC>
+    template <int VAR>
     __device__ __forceinline__ void begin(const AttnParams& p, int s, int kvh, int ctx, int lane) {
         const int g = lane >> 2, tid = lane & 3;
         const int G = p.num_heads / p.num_kv_heads, QL = p.q_len, M = G * QL;
+        if constexpr (VAR == kScored) mod_.begin(p, s, ctx);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int m = g + 8 * r;
             const int h = m < M ? m / QL : 0, j = m < M ? m % QL : 0;
-            const int qr = m < M ? query_row<CASC>(p, s, j) : -1;
+            if constexpr (VAR == kScored) mod_.column(p, r, kvh * G + h, j, ctx);
+            const int qr = m < M ? query_row<VAR>(p, s, j) : -1;
             const bool valid = qr >= 0;
             // a cascade row (one decode query) sees the entry's whole context; verify rows are causal
-            lim[r] = valid ? (CASC ? ctx : max(0, ctx - QL + j + 1)) : 0;
+            lim[r] = valid ? (VAR == kCascade ? ctx : max(0, ctx - QL + j + 1)) : 0;
             const size_t qoff = (size_t(valid ? qr : 0) * p.num_heads + kvh * G + h) * D;
             const uint32_t* qw = reinterpret_cast<const uint32_t*>(p.q);
-            lo_ = visible_lo<CASC>(p, s, ctx);
+            lo_ = visible_lo<VAR>(p, s, ctx);
 #pragma unroll
             for (int kk = 0; kk < NKS; ++kk) {
                 qa[kk][r] = valid ? qw[(qoff + 16 * kk + 2 * tid) / 2] : 0u;
@@ -520,6 +603,7 @@ struct TcMath {
         l_run[0] = l_run[1] = 0.f;
     }
 
+    template <int VAR>
     __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int ntok, uint8_t*, int lane) {
         const int tid = lane & 3;
         const uint32_t stg_a = smem_addr(stg);
@@ -546,7 +630,11 @@ struct TcMath {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int pos = pos0 + nt * 8 + 2 * tid + (e & 1);
-                sc[nt][e] = (pos < lim[e >> 1] && pos >= lo_) ? sc[nt][e] * scale_log2_ : -INFINITY;
+                if constexpr (VAR == kScored)
+                    sc[nt][e] = (pos < lim[e >> 1] && (pos >= lo_ || pos < mod_.pre))
+                                    ? mod_(sc[nt][e] * scale_log2_, pos, e >> 1) : -INFINITY;
+                else
+                    sc[nt][e] = (pos < lim[e >> 1] && pos >= lo_) ? sc[nt][e] * scale_log2_ : -INFINITY;
             }
         float alpha[2];
 #pragma unroll
@@ -582,6 +670,9 @@ struct TcMath {
         // ------------------------------------------------ O += P V
         // P as the A operand: bf16 keeps 8 significant bits, so P = hi + lo
         // (two MMAs, P exact to ~2^-17); fp16's 11 bits are kept as one operand.
+        // A scored pass splits fp16's P too (exact to ~2^-22): one operand's
+        // rounding would be as large as an fp16 output's own.
+        constexpr bool SPLIT = BF || VAR == kScored;
         uint32_t a[4], alo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -590,11 +681,14 @@ struct TcMath {
             if constexpr (BF) {
                 const float hx = __uint_as_float(a[i] << 16), hy = __uint_as_float(a[i] & 0xffff0000u);
                 alo[i] = pack2<BF>(x - hx, y - hy);
+            } else if constexpr (SPLIT) {
+                const float2 hf = Half16<__half>::unpack2(a[i]);
+                alo[i] = pack2<BF>(x - hf.x, y - hf.y);
             }
         }
         // V rows past the context may hold anything (NaN): zero them in the operand
-        const uint32_t m01 = (2 * tid < ntok ? 0x0000ffffu : 0u) | (2 * tid + 1 < ntok ? 0xffff0000u : 0u);
-        const uint32_t m23 = (8 + 2 * tid < ntok ? 0x0000ffffu : 0u) | (9 + 2 * tid < ntok ? 0xffff0000u : 0u);
+        uint32_t m01, m23;
+        const bool whole = token_masks<VAR>(mod_, lo_, pos0, ntok, 2 * tid, m01, m23);
 #pragma unroll
         for (int np = 0; np < NNT / 2; ++np) {
             const int mi = lane >> 3, r = lane & 7;
@@ -602,12 +696,12 @@ struct TcMath {
             const uint32_t addr = stg_a + OFF_V + (c >> 3) * 2048 + t * 128 + 16 * swz<128>(c & 7, t);
             uint32_t R[4];
             ldsm_x4_t(addr, R);
-            if (ntok < kBS) {
+            if (!whole) {
                 R[0] &= m01; R[1] &= m23; R[2] &= m01; R[3] &= m23;
             }
             mma16816<BF>(o[2 * np], a, R[0], R[1]);
             mma16816<BF>(o[2 * np + 1], a, R[2], R[3]);
-            if constexpr (BF) {
+            if constexpr (SPLIT) {
                 mma16816<BF>(o[2 * np], alo, R[0], R[1]);
                 mma16816<BF>(o[2 * np + 1], alo, R[2], R[3]);
             }
@@ -698,6 +792,7 @@ struct TtMath {
     float m_run[2], l_part[2];   // query columns 2t, 2t + 1 (l: this thread's tokens)
     int lim[2];
     int lo_;   // first visible token (sliding window)
+    ScoreMod<2> mod_;   // query columns 2t, 2t + 1
     float scale_log2_;
 
     static __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* vm,
@@ -719,15 +814,16 @@ struct TtMath {
     __device__ __forceinline__ void init(int) {}
 
     // query column n = row m of the pair (head m / q_len, draft m % q_len)
-    template <bool CASC>
+    template <int VAR>
     __device__ __forceinline__ void begin(const AttnParams& p, int s, int kvh, int ctx, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int G = p.num_heads / p.num_kv_heads, QL = p.q_len, M = G * QL;
-        lo_ = visible_lo<CASC>(p, s, ctx);
+        lo_ = visible_lo<VAR>(p, s, ctx);
+        if constexpr (VAR == kScored) mod_.begin(p, s, ctx);
         {
             // this thread's B fragments: column g
             const int h = g < M ? g / QL : 0, j = g < M ? g % QL : 0;
-            const int qr = g < M ? query_row<CASC>(p, s, j) : -1;
+            const int qr = g < M ? query_row<VAR>(p, s, j) : -1;
             const bool valid = qr >= 0;
             const size_t qoff = (size_t(valid ? qr : 0) * p.num_heads + kvh * G + h) * D;
             const uint32_t* qw = reinterpret_cast<const uint32_t*>(p.q);
@@ -742,9 +838,10 @@ struct TtMath {
             // this thread's accumulator columns 2t + e
             const int n = 2 * t + e;
             const int j = n < M ? n % QL : 0;
-            const bool ok = n < M && query_row<CASC>(p, s, j) >= 0;
+            if constexpr (VAR == kScored) mod_.column(p, e, kvh * G + (n < M ? n / QL : 0), j, ctx);
+            const bool ok = n < M && query_row<VAR>(p, s, j) >= 0;
             // a cascade row (one decode query) sees the entry's whole context; verify rows are causal
-            lim[e] = ok ? (CASC ? ctx : max(0, ctx - QL + j + 1)) : 0;
+            lim[e] = ok ? (VAR == kCascade ? ctx : max(0, ctx - QL + j + 1)) : 0;
             m_run[e] = -INFINITY;
             l_part[e] = 0.f;
         }
@@ -752,6 +849,7 @@ struct TtMath {
         for (int mt = 0; mt < NMT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
     }
 
+    template <int VAR>
     __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int ntok, uint8_t*, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int mi = lane >> 3, r = lane & 7;
@@ -770,8 +868,14 @@ struct TtMath {
         const int pg = pos0 + g, pg8 = pos0 + g + 8;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            sc[e] = (pg < lim[e] && pg >= lo_) ? sc[e] * scale_log2_ : -INFINITY;
-            sc[2 + e] = (pg8 < lim[e] && pg8 >= lo_) ? sc[2 + e] * scale_log2_ : -INFINITY;
+            if constexpr (VAR == kScored) {
+                sc[e] = (pg < lim[e] && (pg >= lo_ || pg < mod_.pre)) ? mod_(sc[e] * scale_log2_, pg, e) : -INFINITY;
+                sc[2 + e] =
+                    (pg8 < lim[e] && (pg8 >= lo_ || pg8 < mod_.pre)) ? mod_(sc[2 + e] * scale_log2_, pg8, e) : -INFINITY;
+            } else {
+                sc[e] = (pg < lim[e] && pg >= lo_) ? sc[e] * scale_log2_ : -INFINITY;
+                sc[2 + e] = (pg8 < lim[e] && pg8 >= lo_) ? sc[2 + e] * scale_log2_ : -INFINITY;
+            }
         }
         // ------------------------------------------------ online softmax per query column
         float alpha[2];
@@ -807,10 +911,15 @@ struct TtMath {
             const uint32_t l23 = pack2<BF>(sc[2] - __uint_as_float(p23 << 16), sc[3] - __uint_as_float(p23 & 0xffff0000u));
             c0 = movm_trans(l01);
             c1 = movm_trans(l23);
+        } else if constexpr (VAR == kScored) {
+            // fp16's P split too: one operand's rounding would be as large as an fp16 output's own
+            const float2 h01 = Half16<__half>::unpack2(p01), h23 = Half16<__half>::unpack2(p23);
+            c0 = movm_trans(pack2<BF>(sc[0] - h01.x, sc[1] - h01.y));
+            c1 = movm_trans(pack2<BF>(sc[2] - h23.x, sc[3] - h23.y));
         }
         // V rows past the context may hold anything (NaN): zero them in the operand
-        const uint32_t m01 = (2 * t < ntok ? 0x0000ffffu : 0u) | (2 * t + 1 < ntok ? 0xffff0000u : 0u);
-        const uint32_t m23 = (8 + 2 * t < ntok ? 0x0000ffffu : 0u) | (9 + 2 * t < ntok ? 0xffff0000u : 0u);
+        uint32_t m01, m23;
+        const bool whole = token_masks<VAR>(mod_, lo_, pos0, ntok, 2 * t, m01, m23);
         // ------------------------------------------------ O^T += V^T P^T
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt) {
@@ -818,11 +927,11 @@ struct TtMath {
             const int tk = (mi >> 1) * 8 + r, c = 2 * mt + (mi & 1);
             uint32_t a[4];
             ldsm_x4_t(stg_a + OFF_V + (c >> 3) * 2048 + tk * 128 + 16 * swz<128>(c & 7, tk), a);
-            if (ntok < kBS) {
+            if (!whole) {
                 a[0] &= m01; a[1] &= m01; a[2] &= m23; a[3] &= m23;
             }
             mma16816<BF>(o[mt], a, b0, b1);
-            if constexpr (BF) mma16816<BF>(o[mt], a, c0, c1);
+            if constexpr (BF || VAR == kScored) mma16816<BF>(o[mt], a, c0, c1);
         }
     }
 
@@ -910,6 +1019,7 @@ struct TqMath {
     float kbias[NT][2];   // 1152 * sum of q over the head dims, query columns 2t, 2t+1
     int lo_;       // first visible token (sliding window)
     int lim_lo_;   // smallest lim over this thread's live columns (no live column: INT_MAX)
+    ScoreMod<2 * NT> mod_;   // query columns 8 nt + 2t, + 1
     float scale_log2_;
 
     static __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* vm,
@@ -965,16 +1075,17 @@ struct TqMath {
     __device__ __forceinline__ void init(int) {}
 
     // query column n = head (n / q_len), draft (n % q_len)
-    template <bool CASC>
+    template <int VAR>
     __device__ __forceinline__ void begin(const AttnParams& p, int s, int kvh, int ctx, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const int G = p.num_heads / p.num_kv_heads, QL = p.q_len, M = G * QL;
-        lo_ = visible_lo<CASC>(p, s, ctx);
+        lo_ = visible_lo<VAR>(p, s, ctx);
+        if constexpr (VAR == kScored) mod_.begin(p, s, ctx);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int n = 8 * nt + g;
             const int h = n < M ? n / QL : 0, j = n < M ? n % QL : 0;
-            const int qr = n < M ? query_row<CASC>(p, s, j) : -1;
+            const int qr = n < M ? query_row<VAR>(p, s, j) : -1;
             const bool valid = qr >= 0;
             const size_t qoff = (size_t(valid ? qr : 0) * p.num_heads + kvh * G + h) * D;
             // this thread's dims t*D/4 .. t*D/4 + D/4 - 1: D/2 contiguous bytes, as 16-byte loads
@@ -1009,8 +1120,9 @@ struct TqMath {
             for (int e = 0; e < 2; ++e) {
                 const int n2 = 8 * nt + 2 * t + e;
                 const int j2 = n2 % QL;
-                const bool ok2 = n2 < M && query_row<CASC>(p, s, j2) >= 0;
-                lim[nt][e] = ok2 ? (CASC ? ctx : max(0, ctx - QL + j2 + 1)) : 0;
+                if constexpr (VAR == kScored) mod_.column(p, 2 * nt + e, kvh * G + (n2 < M ? n2 / QL : 0), j2, ctx);
+                const bool ok2 = n2 < M && query_row<VAR>(p, s, j2) >= 0;
+                lim[nt][e] = ok2 ? (VAR == kCascade ? ctx : max(0, ctx - QL + j2 + 1)) : 0;
                 m_run[nt][e] = -INFINITY;
                 l_part[nt][e] = 0.f;
             }
@@ -1026,6 +1138,7 @@ struct TqMath {
                 if (lim[nt][e] > 0) lim_lo_ = min(lim_lo_, lim[nt][e]);
     }
 
+    template <int VAR>
     __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int ntok, uint8_t*, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const uint32_t stg_a = smem_addr(stg);
@@ -1064,7 +1177,16 @@ struct TqMath {
         const __half* ksh = reinterpret_cast<const __half*>(stg + OFF_KS);
         const float k0 = __half2float(ksh[g]) * scale_log2_, k1 = __half2float(ksh[g + 8]) * scale_log2_;
         const int pg = pos0 + g, pg8 = pos0 + g + 8;
-        if (pos0 >= lo_ && pos0 + kBS <= lim_lo_) {
+        if constexpr (VAR == kScored) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = i & 1, pos = i < 2 ? pg : pg8;
+                    sc[nt][i] = (pos < lim[nt][e] && (pos >= lo_ || pos < mod_.pre))
+                                    ? mod_(sc[nt][i] * (i < 2 ? k0 : k1), pos, 2 * nt + e) : -INFINITY;
+                }
+        } else if (pos0 >= lo_ && pos0 + kBS <= lim_lo_) {
             // the whole block is visible to every live column of this thread;
             // columns with nothing visible (padding) stay masked
 #pragma unroll
@@ -1151,11 +1273,11 @@ struct TqMath {
                 }
             }
         }
-        if (ntok < kBS) {
+        if (ntok < kBS || (VAR == kScored && pos0 < lo_)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tk = 2 * t + (i & 1) + 8 * (i >> 1);
-                if (tk >= ntok) {
+                if (tk >= ntok || (VAR == kScored && pos0 + tk < lo_ && pos0 + tk >= mod_.pre)) {
 #pragma unroll
                     for (int q = 0; q < RW; ++q) sr[i][q] = zr[i][q] = 0u;
                 }
@@ -1263,16 +1385,18 @@ __device__ __forceinline__ int seq_ctx(const AttnParams& p, int s) {
 
 // First unit of a sequence (blocks / partitions wholly before its first visible
 // token are skipped) and its number of units: balanced = blocks; split = partitions.
-template <bool CASC>
+template <int VAR>
 __device__ __forceinline__ int seq_first_unit(const AttnParams& p, int s, int ctx) {
-    const int b = visible_lo<CASC>(p, s, ctx) / kBS;
+    if constexpr (VAR == kScored) return 0;   // units are the visible blocks, counted (visible_blocks)
+    const int b = visible_lo<VAR>(p, s, ctx) / kBS;
     return p.mode == kModeBalanced ? b : b / p.partition_blocks;
 }
-template <bool CASC>
+template <int VAR>
 __device__ __forceinline__ long long seq_units(const AttnParams& p, int s, int ctx) {
     const int nb = (ctx + kBS - 1) / kBS;
+    if constexpr (VAR == kScored) return nb - visible_blocks<VAR>(p, s, ctx).hole;
     const int all = p.mode == kModeBalanced ? nb : (nb + p.partition_blocks - 1) / p.partition_blocks;
-    return all - seq_first_unit<CASC>(p, s, ctx);
+    return all - seq_first_unit<VAR>(p, s, ctx);
 }
 
 struct Seg {
@@ -1281,11 +1405,19 @@ struct Seg {
     long long pair_start;   // balanced: the sequence's first unit (block) in the lane's list
     long long cost_base;    // balanced: unit u of this pair sits at cost position u + cost_base
     bool whole;             // the segment is the whole pair
+    Span span;              // scored: which blocks the units are
 };
+
+// The logical block of unit u of a segment (balanced; the block itself but in a scored pass).
+template <int VAR>
+__device__ __forceinline__ int unit_block(const Seg& g, int u) {
+    if constexpr (VAR == kScored) return u < g.span.npre ? u : u + g.span.hole;
+    return u;
+}
 
 // Iterates this CTA's segments in order.  Every warp runs its own copy; all
 // lanes of a warp hold the same state.
-template <bool CASC>
+template <int VAR>
 struct SegIter {
     long long u, u1;
     int kvh;             // split / balanced: the kv head of this CTA's lane
@@ -1295,6 +1427,7 @@ struct SegIter {
     int nb, ctx;
     int u_first;         // first unit (block or partition) of s
     int r;               // non-empty sequences before s in the lane's list
+    Span span;           // scored: the sequence's visible blocks
 
     __device__ __forceinline__ void load_seq(const AttnParams& p, int s_, long long start_, int known_ctx = -1) {
         s = s_;
@@ -1302,8 +1435,9 @@ struct SegIter {
         if (s < p.num_seqs) {
             ctx = known_ctx >= 0 ? known_ctx : seq_ctx(p, s);
             nb = (ctx + kBS - 1) / kBS;
-            u_first = seq_first_unit<CASC>(p, s, ctx);
-            n = seq_units<CASC>(p, s, ctx);
+            u_first = seq_first_unit<VAR>(p, s, ctx);
+            n = seq_units<VAR>(p, s, ctx);
+            if constexpr (VAR == kScored) span = visible_blocks<VAR>(p, s, ctx);
         } else {
             ctx = nb = u_first = 0;
             n = 0;
@@ -1318,7 +1452,7 @@ struct SegIter {
             g.kvh = int(u % Hkv);
             g.ctx = seq_ctx(p, g.s);
             g.nb = (g.ctx + kBS - 1) / kBS;
-            g.b0 = visible_lo<CASC>(p, g.s, g.ctx) / kBS;
+            g.b0 = visible_lo<VAR>(p, g.s, g.ctx) / kBS;
             g.b1 = g.nb;
             g.nu = 1;
             g.part = 0;
@@ -1342,6 +1476,7 @@ struct SegIter {
         g.nb = nb;
         g.ctx = ctx;
         g.nu = n;
+        if constexpr (VAR == kScored) g.span = span;
         if (p.mode == kModeBalanced) {
             const long long k1 = (n < k + (u1 - u)) ? n : k + (u1 - u);
             g.b0 = u_first + int(k);
@@ -1353,7 +1488,7 @@ struct SegIter {
             u += k1 - k;
         } else {
             g.part = u_first + int(k);
-            g.b0 = max(g.part * p.partition_blocks, visible_lo<CASC>(p, s, ctx) / kBS);
+            g.b0 = max(g.part * p.partition_blocks, visible_lo<VAR>(p, s, ctx) / kBS);
             g.b1 = min(nb, (g.part + 1) * p.partition_blocks);
             g.pair_start = 0;
             g.cost_base = 0;
@@ -1415,14 +1550,14 @@ struct SeqPos {
 
 // One round of nthr sequences from r0: a block-wide scan of (cost << 32 | units)
 // gives this thread's sequence its first unit and cost position.
-template <bool CASC>
+template <int VAR>
 __device__ __forceinline__ SeqPos plan_round(const AttnParams& p, int r0, long long* red,
                                              unsigned long long& base) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     SeqPos sp;
     sp.s = r0 + threadIdx.x;
     sp.ctx = sp.s < p.num_seqs ? seq_ctx(p, sp.s) : 0;
-    sp.u = sp.s < p.num_seqs ? seq_units<CASC>(p, sp.s, sp.ctx) : 0;
+    sp.u = sp.s < p.num_seqs ? seq_units<VAR>(p, sp.s, sp.ctx) : 0;
     const unsigned long long v =
         sp.u > 0 ? ((unsigned long long)(sp.u + p.seg_cost) << 32) | (unsigned long long)sp.u : 0ull;
     unsigned long long incl = v;
@@ -1461,12 +1596,12 @@ __device__ __forceinline__ void plan_resolve(const AttnParams& p, const SeqPos& 
     if (sp.C <= X1 && X1 < c_end) red[kRedU1] = sp.U + max(0ll, X1 - sp.C - sc);
 }
 
-template <bool CASC>
+template <int VAR>
 __device__ void cta_plan(const AttnParams& p, int lane_idx, int nlanes, long long* red, int* flag, Plan& pl) {
     const int B = p.num_seqs, nthr = blockDim.x;
     unsigned long long base = 0;
     SeqPos mine{};
-    for (int r0 = 0; r0 < B; r0 += nthr) mine = plan_round<CASC>(p, r0, red, base);
+    for (int r0 = 0; r0 < B; r0 += nthr) mine = plan_round<VAR>(p, r0, red, base);
     const long long total_u = (long long)(base & 0xffffffffull), total_c = (long long)(base >> 32);
     // split mode charges nothing (seg_cost 0)
     const long long span = total_c > p.seg_cost ? total_c - p.seg_cost : 0;
@@ -1487,7 +1622,7 @@ __device__ void cta_plan(const AttnParams& p, int lane_idx, int nlanes, long lon
         plan_resolve(p, mine, X0, X1, red, flag);
     } else {
         base = 0;
-        for (int r0 = 0; r0 < B; r0 += nthr) plan_resolve(p, plan_round<CASC>(p, r0, red, base), X0, X1, red, flag);
+        for (int r0 = 0; r0 < B; r0 += nthr) plan_resolve(p, plan_round<VAR>(p, r0, red, base), X0, X1, red, flag);
     }
     __syncthreads();
     pl.chunk = chunk;
@@ -1582,7 +1717,7 @@ __device__ void fused_write(const AttnParams& p, int warp, int nwarps, int tid) 
 
 // ---------------------------------------------------------------- the kernel
 
-template <class Math, bool FUSED, bool CASC>
+template <class Math, bool FUSED, int VAR>
 __global__ void __launch_bounds__((Math::NCW + 1) * 32, 1)
 attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                  const AttnParams p) {
@@ -1637,7 +1772,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     // so CTAs c .. c+Hkv-1 stream the same blocks' head slices side by side and
     // every 2*Hkv*D-byte token row of a block is read from DRAM at one time.
     const int lane_kvh = blockIdx.x % Hkv, lane_idx = blockIdx.x / Hkv, nlanes = gridDim.x / Hkv;
-    if (CASC || p.wait_first) grid_dep_wait();   // the plan reads what the previous kernel wrote
+    if (VAR == kCascade || p.wait_first) grid_dep_wait();   // the plan reads what the previous kernel wrote
     Plan pl;
     if (p.mode == kModeSingle) {
         const long long total = (long long)p.num_seqs * Hkv;
@@ -1650,7 +1785,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         pl.start0 = 0;
         __syncthreads();
     } else {
-        cta_plan<CASC>(p, lane_idx, nlanes, red, flag, pl);
+        cta_plan<VAR>(p, lane_idx, nlanes, red, flag, pl);
     }
     const long long chunk = pl.chunk;
     // Except in a cascade pass or with wait_first, everything above read only the
@@ -1663,7 +1798,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
 #endif
     if (tid == 0) grid_dep_launch();
 
-    SegIter<CASC> it;
+    SegIter<VAR> it;
     it.u = pl.u0;
     it.u1 = pl.u0 < pl.u1 ? pl.u1 : pl.u0;
     it.kvh = lane_kvh;
@@ -1686,12 +1821,12 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         bool waited = false;
         Seg sg;
         while (it.next(p, sg)) {
-            const int bt_seq = CASC ? p.item_seq[sg.s] : sg.s;   // cascade: an item reads its lending member's table
+            const int bt_seq = VAR == kCascade ? p.item_seq[sg.s] : sg.s;   // cascade: an item reads its lending member's table
             const int32_t* bt = p.block_tables + size_t(bt_seq) * p.max_blocks;
             const int n = sg.b1 - sg.b0;
             for (int i0 = 0; i0 < n; i0 += grp) {
                 if (lane < grp && i0 + lane < n) {
-                    int pb = bt[sg.b0 + i0 + lane];   // block tables: an input, read before the wait
+                    int pb = bt[unit_block<VAR>(sg, sg.b0 + i0 + lane)];   // block tables: an input, read before the wait
                     if (!waited) {
                         grid_dep_wait();
                         waited = true;
@@ -1733,17 +1868,17 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     // balanced mode: sequences with nothing visible still get their zero rows
     // (cascade: an empty partial in the sequence's own slot)
     if (p.mode == kModeBalanced) {
-        if constexpr (CASC) {
+        if constexpr (VAR == kCascade) {
             for (int s = p.num_items + blockIdx.x; s < p.num_seqs; s += gridDim.x)
-                if (seq_units<CASC>(p, s, seq_ctx(p, s)) == 0)
+                if (seq_units<VAR>(p, s, seq_ctx(p, s)) == 0)
                     for (int h = tid; h < H; h += CT) {
-                        const size_t pi = (size_t(query_row<CASC>(p, s, 0)) * H + h) * p.max_partitions;
+                        const size_t pi = (size_t(query_row<VAR>(p, s, 0)) * H + h) * p.max_partitions;
                         p.max_logits[pi] = -INFINITY;
                         p.exp_sums[pi] = 0.f;
                     }
         } else {
             for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
-                if (seq_ctx(p, s) == 0)
+                if (VAR == kScored ? seq_units<VAR>(p, s, seq_ctx(p, s)) == 0 : seq_ctx(p, s) == 0)
                     for (int i = tid; i < QL * H * D; i += CT)
                         store_out(p.out, p.out_dtype, size_t(s) * QL * H * D + i, 0.f);
         }
@@ -1760,7 +1895,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
 #ifdef PKV_TIMELINE
         if (tid == 0 && tl_seg < kTlSegs) PKV_TL(4 + 4 * tl_seg);
 #endif
-        mth.template begin<CASC>(p, sg.s, sg.kvh, sg.ctx, lane);
+        mth.template begin<VAR>(p, sg.s, sg.kvh, sg.ctx, lane);
         // Fused step: the warp that will consume a block holding new positions
         // [ctx - q_len, ctx) prefetches those rows from k_new / v_new into its
         // merge buffer (free until the merge) with cp.async, and their slot
@@ -1812,7 +1947,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             tl_first = false;
 #endif
             if (!ok && lane == 0) flag_error(p.err, PKV_DEVERR_TIMEOUT);
-            const int b = sg.b0 + i;
+            const int b = unit_block<VAR>(sg, sg.b0 + i);
             int ntok = (b == sg.nb - 1) ? sg.ctx - b * kBS : kBS;
             if (!ok || poison[st]) ntok = 0;
             bool patched = false;
@@ -1822,7 +1957,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 const int pos_l = new0 + lane;
                 const int64_t my_slot = lane < QL ? st_slot[lane] : -1;
                 const int my_pb = lane < QL ? st_pb[lane] : -1;
-                const bool in_place = lane < QL && my_slot >= 0 && pos_l >= 0 && pos_l >= visible_lo<CASC>(p, sg.s, sg.ctx) &&
+                const bool in_place = lane < QL && my_slot >= 0 && pos_l >= 0 && pos_l >= visible_lo<VAR>(p, sg.s, sg.ctx) &&
                                       my_pb >= 0 && my_pb < p.num_blocks &&
                                       my_slot == int64_t(my_pb) * kBS + pos_l % kBS;
                 const uint32_t mask = __ballot_sync(0xffffffffu, in_place);
@@ -1835,7 +1970,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
                 __syncwarp();
             }
-            if (ntok > 0) mth.block(smem + size_t(st) * Math::STAGE, b * kBS, ntok, my_scratch, lane);
+            if (ntok > 0) mth.template block<VAR>(smem + size_t(st) * Math::STAGE, b * kBS, ntok, my_scratch, lane);
             // generic writes into a stage the TMA refills: order them before the refill
             if (FUSED && patched) fence_proxy_async_smem();
             __syncwarp();
@@ -1902,8 +2037,8 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             const int m = (i4 << 2) / D, d = (i4 << 2) - m * D;
             const float L = resL[k], Mx = resM[k];
             const int h = m / QL, jq = m - (m / QL) * QL;
-            const int qrow = query_row<CASC>(p, sg.s, jq);
-            if (CASC && qrow < 0) continue;   // a cascade item's padding column
+            const int qrow = query_row<VAR>(p, sg.s, jq);
+            if (VAR == kCascade && qrow < 0) continue;   // a cascade item's padding column
             const size_t row = size_t(qrow);
             const int hg = sg.kvh * G + h;
             if (piece) {
@@ -1917,9 +2052,9 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 const float inv = live ? 1.f / L : 0.f;
                 const float4 o = live ? make_float4(res[k].x * inv, res[k].y * inv, res[k].z * inv, res[k].w * inv)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (CASC || p.mode == kModeSplit) {
+                if (VAR == kCascade || p.mode == kModeSplit) {
                     // cascade: an item's partial goes to its members' slot part_offset
-                    const int slot_p = sg.part + ((CASC && sg.s < p.num_items) ? p.part_offset : 0);
+                    const int slot_p = sg.part + ((VAR == kCascade && sg.s < p.num_items) ? p.part_offset : 0);
                     const size_t pi = (row * H + hg) * p.max_partitions + slot_p;
                     reinterpret_cast<float4*>(p.tmp_out + pi * D)[d >> 2] = o;
                     if (d == 0) {
@@ -2010,9 +2145,9 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                     const int h = m / QL, jq = m - (m / QL) * QL;
                     const float4 o = live ? make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv)
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-                    if constexpr (CASC) {
+                    if constexpr (VAR == kCascade) {
                         // the pair's combined partial into its slot (items: part_offset)
-                        const int qrow = query_row<CASC>(p, sg.s, jq);
+                        const int qrow = query_row<VAR>(p, sg.s, jq);
                         if (qrow < 0) continue;
                         const size_t pi = (size_t(qrow) * H + sg.kvh * G + h) * p.max_partitions +
                                           (sg.s < p.num_items ? p.part_offset : 0);
@@ -2050,7 +2185,7 @@ int smem_bytes(int stages, int M, int QL, int D) {
            (FUSED && !checks_fit(M, QL, D) ? NCW * kCheckBytes : 0) + NCW * M * D * 4 + NCW * Math::SCRATCH + 1024 + 64;
 }
 
-template <class Math, bool FUSED, bool CASC>
+template <class Math, bool FUSED, int VAR>
 cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
     static int num_sms = 0;
     if (num_sms == 0) {
@@ -2070,7 +2205,7 @@ cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& 
     const int smem = smem_bytes<Math, FUSED>(stages, M, p.q_len, p.head_dim);
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(attention_kernel<Math, FUSED, CASC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(attention_kernel<Math, FUSED, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemLimit);
         if (e != cudaSuccess) return e;
         attr_set = true;
@@ -2088,7 +2223,7 @@ cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& 
         if (lane_units < L) L = int(lane_units < 1 ? 1 : lane_units);
         grid = L * p.num_kv_heads;
     }
-    return launch_kernel(attention_kernel<Math, FUSED, CASC>, dim3(grid), dim3((Math::NCW + 1) * 32), size_t(smem),
+    return launch_kernel(attention_kernel<Math, FUSED, VAR>, dim3(grid), dim3((Math::NCW + 1) * 32), size_t(smem),
                          stream, km, vm, p);
 }
 
@@ -2096,8 +2231,8 @@ template <typename T, int D, bool FUSED>
 cudaError_t dispatch_cc(const AttnParams& p, int gqa, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
     // group sizes 1 and 2 (larger groups run the tensor-core math)
     switch (gqa) {
-        case 1: return launch_math<CcMath<T, D, 1>, FUSED, false>(p, km, vm, st);
-        case 2: return launch_math<CcMath<T, D, 2>, FUSED, false>(p, km, vm, st);
+        case 1: return launch_math<CcMath<T, D, 1>, FUSED, kPlain>(p, km, vm, st);
+        case 2: return launch_math<CcMath<T, D, 2>, FUSED, kPlain>(p, km, vm, st);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -2108,34 +2243,34 @@ cudaError_t dispatch_cc(const AttnParams& p, int gqa, const CUtensorMap& km, con
 // attention_uses_tensor_cores(), the predicate the host also builds the tensor
 // maps from: the tensor-core maths issue 3-D tile copies (fp16/bf16) or
 // swizzled row copies (K8/V4) that only their own maps describe.
-template <bool FUSED, bool CASC>
+template <bool FUSED, int VAR>
 cudaError_t launch_attention_impl(const AttnParams& p, int cache_kind, int gqa, const CUtensorMap& km,
                                   const CUtensorMap& vm, cudaStream_t stream) {
-    if (attention_uses_tensor_cores(cache_kind, p.q_len, gqa, CASC)) {
+    if (attention_uses_tensor_cores(cache_kind, p.q_len, gqa, VAR != kPlain)) {
         switch (cache_kind) {
             case PKV_CACHE_K8V4: {
                 const bool narrow = (p.num_heads / p.num_kv_heads) * p.q_len <= 8;
                 if (p.head_dim == 128)
-                    return narrow ? launch_math<TqMath<128, 1>, FUSED, CASC>(p, km, vm, stream)
-                                  : launch_math<TqMath<128, 2>, FUSED, CASC>(p, km, vm, stream);
-                return narrow ? launch_math<TqMath<64, 1>, FUSED, CASC>(p, km, vm, stream)
-                              : launch_math<TqMath<64, 2>, FUSED, CASC>(p, km, vm, stream);
+                    return narrow ? launch_math<TqMath<128, 1>, FUSED, VAR>(p, km, vm, stream)
+                                  : launch_math<TqMath<128, 2>, FUSED, VAR>(p, km, vm, stream);
+                return narrow ? launch_math<TqMath<64, 1>, FUSED, VAR>(p, km, vm, stream)
+                              : launch_math<TqMath<64, 2>, FUSED, VAR>(p, km, vm, stream);
             }
             case PKV_CACHE_BF16:
                 if ((p.num_heads / p.num_kv_heads) * p.q_len <= 8)
-                    return p.head_dim == 128 ? launch_math<TtMath<PKV_CACHE_BF16, 128>, FUSED, CASC>(p, km, vm, stream)
-                                             : launch_math<TtMath<PKV_CACHE_BF16, 64>, FUSED, CASC>(p, km, vm, stream);
-                return p.head_dim == 128 ? launch_math<TcMath<PKV_CACHE_BF16, 128>, FUSED, CASC>(p, km, vm, stream)
-                                         : launch_math<TcMath<PKV_CACHE_BF16, 64>, FUSED, CASC>(p, km, vm, stream);
+                    return p.head_dim == 128 ? launch_math<TtMath<PKV_CACHE_BF16, 128>, FUSED, VAR>(p, km, vm, stream)
+                                             : launch_math<TtMath<PKV_CACHE_BF16, 64>, FUSED, VAR>(p, km, vm, stream);
+                return p.head_dim == 128 ? launch_math<TcMath<PKV_CACHE_BF16, 128>, FUSED, VAR>(p, km, vm, stream)
+                                         : launch_math<TcMath<PKV_CACHE_BF16, 64>, FUSED, VAR>(p, km, vm, stream);
             default:
                 if ((p.num_heads / p.num_kv_heads) * p.q_len <= 8)
-                    return p.head_dim == 128 ? launch_math<TtMath<PKV_CACHE_F16, 128>, FUSED, CASC>(p, km, vm, stream)
-                                             : launch_math<TtMath<PKV_CACHE_F16, 64>, FUSED, CASC>(p, km, vm, stream);
-                return p.head_dim == 128 ? launch_math<TcMath<PKV_CACHE_F16, 128>, FUSED, CASC>(p, km, vm, stream)
-                                         : launch_math<TcMath<PKV_CACHE_F16, 64>, FUSED, CASC>(p, km, vm, stream);
+                    return p.head_dim == 128 ? launch_math<TtMath<PKV_CACHE_F16, 128>, FUSED, VAR>(p, km, vm, stream)
+                                             : launch_math<TtMath<PKV_CACHE_F16, 64>, FUSED, VAR>(p, km, vm, stream);
+                return p.head_dim == 128 ? launch_math<TcMath<PKV_CACHE_F16, 128>, FUSED, VAR>(p, km, vm, stream)
+                                         : launch_math<TcMath<PKV_CACHE_F16, 64>, FUSED, VAR>(p, km, vm, stream);
         }
     }
-    if constexpr (!CASC) {
+    if constexpr (VAR == kPlain) {
         if (cache_kind == PKV_CACHE_BF16)
             return p.head_dim == 128 ? dispatch_cc<__nv_bfloat16, 128, FUSED>(p, gqa, km, vm, stream)
                                      : dispatch_cc<__nv_bfloat16, 64, FUSED>(p, gqa, km, vm, stream);

@@ -87,6 +87,12 @@ struct AttnParams {
     // 1: block_tables / context_lens come from the previous kernel (the sparse
     // set-up), so the kernel waits for it before planning
     int32_t wait_first;
+    // scored pass (attention_scored.cu): what happens to the scores and which tokens are masked
+    int32_t scored;
+    float softcap;               // 0: none
+    const float* slopes;         // [num_heads] or null
+    const int32_t* doc_starts;   // [num_seqs] or null
+    const int32_t* prefix_lens;  // [num_seqs] or null
     // timeline build only (PKV_TIMELINE): per-CTA %globaltimer stamps, see
     // attention_impl.cuh; null otherwise
     unsigned long long* timeline;
@@ -112,11 +118,12 @@ inline bool is_byte_cache(int kind) { return kind == PKV_CACHE_I8 || kind == PKV
 // Persistent attention kernel (attention.cu): one CTA per SM at most, the
 // (sequence, kv head, block) work list split into contiguous ranges.
 bool attention_supported(int cache_kind, int head_dim, int gqa, int q_len);
-// Tensor-core maths for K8/V4 and the 8-bit caches, for cascade passes and whenever a kv head serves
+// Tensor-core maths for K8/V4 and the 8-bit caches, for cascade and scored passes and whenever a kv head serves
 // at least kTcMinRows query rows (group size x q_len); the CUDA-core math for
 // fp16/bf16 below that (group size 1 or 2 decode).
 constexpr int kTcMinRows = 4;
-bool attention_uses_tensor_cores(int cache_kind, int q_len, int gqa, bool cascade_pass = false);
+// own_pass: a cascade or scored pass (is_cascade_pass(p) || p.scored).
+bool attention_uses_tensor_cores(int cache_kind, int q_len, int gqa, bool own_pass = false);
 // A pass of cascade attention: its own kernel instantiation (attention_cascade.cu)
 inline bool is_cascade_pass(const AttnParams& p) { return p.seq_start != nullptr || p.row_map != nullptr; }
 cudaError_t launch_attention(AttnParams p, int cache_kind, int gqa, const CUtensorMap& k_map,
@@ -130,6 +137,9 @@ cudaError_t launch_attention_fused(AttnParams p, int cache_kind, int gqa, const 
 // The 8-bit caches' kernels (attention_byte.cu)
 cudaError_t launch_attention_byte(const AttnParams& p, int cache_kind, const CUtensorMap& km, const CUtensorMap& vm,
                                   cudaStream_t stream);
+// Scored passes over any cache (attention_scored.cu); balanced schedule only.
+cudaError_t launch_attention_scored(const AttnParams& p, int cache_kind, int gqa, const CUtensorMap& km,
+                                    const CUtensorMap& vm, cudaStream_t stream);
 size_t balanced_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim);
 
 struct ReduceParams {

@@ -52,6 +52,11 @@ class _RopeScaling(ctypes.Structure):
                 ("high_rotations", ctypes.c_double), ("original_context", ctypes.c_double)]
 
 
+class _Scores(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("distance_slopes", ctypes.c_void_p), ("doc_starts", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
 class _Seqs(ctypes.Structure):
     _fields_ = [("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
                 ("num_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("q_len", ctypes.c_int32),
@@ -114,6 +119,9 @@ def lib():
         L.pkv_paged_attention_balanced.restype = st
         L.pkv_paged_attention_balanced.argtypes = [_P, ctypes.c_int, _P, ctypes.c_int, _I32, ctypes.c_float, _P, _P,
                                                    _P, ctypes.c_size_t, _P, _P]
+        L.pkv_paged_attention_scored.restype = st
+        L.pkv_paged_attention_scored.argtypes = [_P, ctypes.c_int, _P, ctypes.c_int, _I32, ctypes.c_float, _P, _P, _P,
+                                                 _P, ctypes.c_size_t, _P, _P]
         L.pkv_decode_step_balanced.restype = st
         L.pkv_decode_step_balanced.argtypes = [_P, ctypes.c_int, _P, ctypes.c_int, _I32, ctypes.c_float, _P, _P,
                                                _P, _P, ctypes.c_int, _P, _I32, _P, ctypes.c_size_t, _P, _P]
@@ -429,6 +437,42 @@ def pkv_paged_attention_balanced(out: torch.Tensor, q: torch.Tensor, scale: floa
                                               float(scale), ctypes.byref(c), ctypes.byref(s), _ptr(workspace),
                                               int(workspace.numel() * workspace.element_size()),
                                               _err_ptr(err_flags), _stream(stream)))
+    return out
+
+
+@dataclass
+class Scores:
+    """What happens to the scores before the softmax (cap, then bias, then mask), and which tokens are masked."""
+    softcap: float = 0.0                              # c > 0: x -> c tanh(x / c)
+    distance_slopes: Optional[torch.Tensor] = None    # float32 [H]: x += slope[h] * (token position - query position)
+    doc_starts: Optional[torch.Tensor] = None         # int32 [B]: tokens before it are masked
+    prefix_lens: Optional[torch.Tensor] = None        # int32 [B]: the first tokens, visible whatever else is masked
+
+    def c_struct(self, num_seqs: int, num_heads: int) -> _Scores:
+        for name, t, dt, n in (("distance_slopes", self.distance_slopes, torch.float32, num_heads),
+                               ("doc_starts", self.doc_starts, torch.int32, num_seqs),
+                               ("prefix_lens", self.prefix_lens, torch.int32, num_seqs)):
+            if t is not None and (t.dtype != dt or t.numel() != n):
+                raise ValueError(f"{name} must be {dt} [{n}]")
+        return _Scores(float(self.softcap), _ptr(self.distance_slopes), _ptr(self.doc_starts), _ptr(self.prefix_lens))
+
+
+def pkv_paged_attention_scored(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
+                               scores: Scores, workspace: torch.Tensor, err_flags: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
+    """The balanced attention with capped and / or distance-biased scores and document / prefix masks."""
+    B, H, D = int(seqs.block_tables.shape[0]), int(q.shape[1]), cache.head_dim
+    if tuple(q.shape) != (B * seqs.q_len, H, D) or out.shape != q.shape or seqs.context_lens.numel() != B:
+        raise ValueError("q and out must be [num_seqs * q_len, num_heads, head_dim], context_lens [num_seqs]")
+    if q.dtype not in (torch.float16, torch.bfloat16) or out.dtype not in _DT:
+        raise ValueError("q must be float16 or bfloat16, out one of them or float32")
+    _one_device(out, q, cache.k, cache.v, seqs.block_tables, seqs.context_lens, scores.distance_slopes,
+                scores.doc_starts, scores.prefix_lens, workspace, err_flags)
+    c, s, x = cache.c_struct(), seqs.c_struct(), scores.c_struct(B, H)
+    _check(lib().pkv_paged_attention_scored(_ptr(out), _DT[out.dtype], _ptr(q), _DT[q.dtype], H, float(scale),
+                                            ctypes.byref(c), ctypes.byref(s), ctypes.byref(x), _ptr(workspace),
+                                            int(workspace.numel() * workspace.element_size()), _err_ptr(err_flags),
+                                            _stream(stream)))
     return out
 
 

@@ -82,7 +82,8 @@ def stored(codes, scale, tables, s, c):
 
 
 def attention(q, k, v, ctx, q_len, scale, window=0, cap=0.0, slopes=None, starts=None, prefix=None):
-    """q float64 [B * q_len, H, D]; k, v lists of float64 [ctx, Hkv, D].  Returns (out, the largest sum |q||k| scale)."""
+    """q float64 [B * q_len, H, D]; k, v lists of float64 [ctx, Hkv, D].  Returns (out, the largest magnitude that
+    goes into a score that counts: sum |q||k| scale, and the bias)."""
     out = np.zeros_like(q)
     biggest = 0.0
     for s, c in enumerate(ctx):
@@ -103,12 +104,14 @@ def attention(q, k, v, ctx, q_len, scale, window=0, cap=0.0, slopes=None, starts
             for h in range(q.shape[1]):
                 K, V, row = k[s][see, h // g], v[s][see, h // g], q[s * q_len + j, h]
                 x = K @ row * scale
-                biggest = max(biggest, float((np.abs(K) @ np.abs(row)).max() * abs(scale)))
+                size = np.abs(K) @ np.abs(row) * abs(scale)
                 if cap:
                     x = cap * np.tanh(x / cap)
                 if slopes is not None:
                     x = x + float(slopes[h]) * (at[see] - me)
+                    size = size + np.abs(float(slopes[h]) * (at[see] - me))
                 w = np.exp(x - x.max())
+                biggest = max(biggest, float(size[w > 2.0 ** -40].max()))   # the others weigh nothing
                 out[s * q_len + j, h] = w @ V / w.sum()
     return out, biggest
 
