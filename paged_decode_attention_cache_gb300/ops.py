@@ -22,7 +22,9 @@ PKV_F16, PKV_BF16, PKV_F32 = 0, 1, 2
 PKV_CACHE_F16, PKV_CACHE_BF16, PKV_CACHE_K8V4, PKV_CACHE_I8, PKV_CACHE_E4M3 = 0, 1, 2, 3, 4
 DEVERR_OOB_BLOCK, DEVERR_OOB_SLOT, DEVERR_CAPACITY, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
-_DT = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
+_HALF = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
+_DT = {**_HALF, torch.float32: PKV_F32}
+_ref = ctypes.byref
 _CACHE_KIND = {"f16": PKV_CACHE_F16, "bf16": PKV_CACHE_BF16, "k8v4": PKV_CACHE_K8V4, "i8": PKV_CACHE_I8,
                "e4m3": PKV_CACHE_E4M3}
 # 8-bit caches with one scale per (block, kv head): the code tensors' dtypes
@@ -160,19 +162,29 @@ def _check(status: int):
         raise PkvError(status, msg or lib().pkv_status_string(status).decode())
 
 
-def _ptr(t: Optional[torch.Tensor]):
+def _ptr(t: Optional[torch.Tensor], device: Optional[int] = None):
+    """A tensor's address; with `device` (_current_device()), it has to live there."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("pkv tensors must live on a CUDA device")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"pkv tensors must live on the current CUDA device ({device}), not {t.device}")
     if not t.is_contiguous():
         raise ValueError("pkv tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+# A decode step's calls are short: the index of the current device and its
+# current stream as integers, without the objects torch.cuda makes for them
+# (current_stream() alone takes 2.9 us of a 19 us call).
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _stream(stream: Optional[torch.cuda.Stream], device: Optional[int] = None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(_current_device() if device is None else device)
 
 
 @dataclass
@@ -198,21 +210,19 @@ class Cache:
     def head_dim(self):
         return int(self.k.shape[3])
 
-    def _check_byte(self):
-        shape, scales = self.k.shape, (self.num_blocks, self.num_kv_heads)
-        if self.k.dtype not in _BYTE_CODES[self.kind] or self.v.dtype not in _BYTE_CODES[self.kind]:
-            raise ValueError(f"a {self.kind} cache holds {_BYTE_CODES[self.kind][0]} codes")
-        if self.v.shape != shape or self.k_scale is None or self.v_scale is None or \
-                self.k_scale.shape != scales or self.v_scale.shape != scales or \
-                self.k_scale.dtype != torch.float32 or self.v_scale.dtype != torch.float32:
-            raise ValueError(f"a {self.kind} cache has k and v of one shape and float32 scales [num_blocks, num_kv_heads]")
-
-    def c_struct(self) -> _Cache:
-        if self.kind in _BYTE_CODES:
-            self._check_byte()
-        return _Cache(_CACHE_KIND[self.kind], self.num_blocks, int(self.k.shape[1]), self.num_kv_heads,
-                      self.head_dim, self.v_group, _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
-                      _ptr(self.v_scale), _ptr(self.v_zero))
+    def c_struct(self, device: Optional[int] = None) -> _Cache:
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        nb, bs, hkv, d = shape = k.shape
+        codes = _BYTE_CODES.get(self.kind)
+        if codes is not None:
+            if k.dtype not in codes or v.dtype not in codes:
+                raise ValueError(f"a {self.kind} cache holds {codes[0]} codes")
+            if v.shape != shape or ks is None or vs is None or ks.shape != (nb, hkv) or vs.shape != (nb, hkv) or \
+                    ks.dtype != torch.float32 or vs.dtype != torch.float32:
+                raise ValueError(f"a {self.kind} cache has k and v of one shape and float32 scales "
+                                 f"[num_blocks, num_kv_heads]")
+        return _Cache(_CACHE_KIND[self.kind], nb, bs, hkv, d, self.v_group, _ptr(k, device), _ptr(v, device),
+                      _ptr(ks, device), _ptr(vs, device), _ptr(self.v_zero, device))
 
     @staticmethod
     def empty(kind: str, num_blocks: int, num_kv_heads: int, head_dim: int, device="cuda") -> "Cache":
@@ -239,19 +249,20 @@ class Seqs:
     q_len: int = 1
     sliding_window: int = 0      # 0: none; W: only the last W stored tokens are visible
 
-    def c_struct(self) -> _Seqs:
-        if self.block_tables.dtype != torch.int32 or self.context_lens.dtype != torch.int32:
+    def c_struct(self, device: Optional[int] = None) -> _Seqs:
+        bt, cl = self.block_tables, self.context_lens
+        if bt.dtype != torch.int32 or cl.dtype != torch.int32:
             raise ValueError("block_tables and context_lens must be int32")
-        return _Seqs(_ptr(self.block_tables), _ptr(self.context_lens), int(self.block_tables.shape[0]),
-                     int(self.block_tables.shape[1]), int(self.q_len), int(self.sliding_window))
+        n, mb = bt.shape
+        return _Seqs(_ptr(bt, device), _ptr(cl, device), n, mb, int(self.q_len), int(self.sliding_window))
 
 
-def _err_ptr(err: Optional[torch.Tensor]):
+def _err_ptr(err: Optional[torch.Tensor], device: Optional[int] = None):
     if err is None:
         return None
     if err.dtype not in (torch.int32, torch.uint32) or err.numel() < 1:
         raise ValueError("err_flags must be a device int32/uint32 tensor")
-    return _ptr(err)
+    return _ptr(err, device)
 
 
 def pkv_reshape_and_cache(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
@@ -272,33 +283,27 @@ def pkv_quantize_kv(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, slot
                                  int(slot_mapping.numel()), _err_ptr(err_flags), _stream(stream)))
 
 
-def _one_device(*tensors) -> None:
-    """The tensors of a call share a device, and it is the current one (its stream runs the kernels)."""
-    device = torch.device("cuda", torch.cuda.current_device())
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"pkv tensors must live on the current CUDA device ({device}), not {t.device}")
-
-
 def pkv_quantize_kv_blocks(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, seqs: Seqs,
                            cu_new_lens: Optional[torch.Tensor] = None, err_flags: Optional[torch.Tensor] = None,
                            stream=None) -> None:
     """Append each sequence's new tokens (its last ones: rows cu_new_lens[s] ..
     cu_new_lens[s + 1] of k_new / v_new, or q_len rows each) to an "i8" or
     "e4m3" cache; a block's scale grows when they need it."""
-    if k_new.dtype not in (torch.float16, torch.bfloat16) or v_new.dtype != k_new.dtype:
+    dt = _HALF.get(k_new.dtype)
+    if dt is None or v_new.dtype != k_new.dtype:
         raise ValueError("k_new / v_new must both be float16 or both bfloat16")
-    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (cache.num_kv_heads, cache.head_dim) or v_new.shape != k_new.shape:
+    dev = _current_device()
+    c, s = cache.c_struct(dev), seqs.c_struct(dev)
+    shape = k_new.shape
+    if shape[1:] != (c.num_kv_heads, c.head_dim) or v_new.shape != shape:
         raise ValueError("k_new / v_new must be [num_tokens, num_kv_heads, head_dim]")
-    if cu_new_lens is not None and (cu_new_lens.dtype != torch.int32 or
-                                    cu_new_lens.numel() != seqs.block_tables.shape[0] + 1):
+    if seqs.context_lens.numel() != s.num_seqs:
+        raise ValueError("context_lens must be [num_seqs]")
+    if cu_new_lens is not None and (cu_new_lens.dtype != torch.int32 or cu_new_lens.numel() != s.num_seqs + 1):
         raise ValueError("cu_new_lens must be int32 [num_seqs + 1]")
-    _one_device(cache.k, cache.v, cache.k_scale, cache.v_scale, k_new, v_new, seqs.block_tables, seqs.context_lens,
-                cu_new_lens, err_flags)
-    c, s = cache.c_struct(), seqs.c_struct()
-    _check(lib().pkv_quantize_kv_blocks(ctypes.byref(c), _ptr(k_new), _ptr(v_new), _DT[k_new.dtype],
-                                        int(k_new.shape[0]), _ptr(cu_new_lens), ctypes.byref(s), _err_ptr(err_flags),
-                                        _stream(stream)))
+    _check((_lib or lib()).pkv_quantize_kv_blocks(_ref(c), _ptr(k_new, dev), _ptr(v_new, dev), dt, shape[0],
+                                                  _ptr(cu_new_lens, dev), _ref(s), _err_ptr(err_flags, dev),
+                                                  _stream(stream, dev)))
 
 
 _ROPE_LAYOUT = {"half": 0, "interleaved": 1}
@@ -313,12 +318,13 @@ class Rope:
     layout: str = "half"      # "half": pairs (i, i + rotary_dim/2); "interleaved": pairs (2i, 2i + 1)
     mscale: float = 1.0
 
-    def c_struct(self) -> _Rope:
+    def c_struct(self, device: Optional[int] = None) -> _Rope:
         if self.freq.dtype != torch.int64 or self.freq.numel() * 2 != self.rotary_dim:
             raise ValueError("freq must be int64 [rotary_dim / 2]")
-        if self.layout not in _ROPE_LAYOUT:
+        layout = _ROPE_LAYOUT.get(self.layout)
+        if layout is None:
             raise ValueError(f"layout {self.layout!r}: 'half' or 'interleaved'")
-        return _Rope(_ptr(self.freq), int(self.rotary_dim), _ROPE_LAYOUT[self.layout], float(self.mscale))
+        return _Rope(_ptr(self.freq, device), self.rotary_dim, layout, self.mscale)
 
 
 def pkv_rope_frequencies(rotary_dim: int, base: float, scaling: str = "none", factor: float = 1.0,
@@ -336,15 +342,18 @@ def pkv_rope_frequencies(rotary_dim: int, base: float, scaling: str = "none", fa
     return freq
 
 
-def _rows(t: torch.Tensor, name: str, heads: int, head_dim: int, tokens: int, dtype: torch.dtype):
+def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: int):
     """Address and row stride of a [tokens, heads, head_dim] view whose rows are contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != (tokens, heads, head_dim):
-        raise ValueError(f"{name} must be {dtype} [{tokens}, {heads}, {head_dim}]")
-    s = t.stride()
-    if s[2] != 1 or (s[1] != head_dim and heads > 1):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"pkv tensors must live on the current CUDA device ({device}), not {t.device}")
+    tokens, heads, head_dim = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != head_dim and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     # one row (or none): any stride will do
-    return ctypes.c_void_p(t.data_ptr()), s[0] if tokens > 1 else heads * head_dim
+    return t.data_ptr(), s0 if tokens > 1 else heads * head_dim
 
 
 def pkv_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], rope: Rope,
@@ -354,29 +363,30 @@ def pkv_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     """Rotate q into q_out and k into its cache slot and / or k_out, and write v
     into its slot, in one launch.  q, k, v may be views of one packed projection
     (any row stride that is a multiple of 8); q_out may be q and k_out may be k."""
-    T, H, D = (int(x) for x in q.shape)
-    Hkv = int(k.shape[1])
+    dt, shape = q.dtype, q.shape
+    T, H, D = shape
+    kv = (T, k.shape[1], D)
+    if dt not in _HALF:
+        raise ValueError("q must be float16 or bfloat16")
     if positions.dtype != torch.int64 or positions.numel() != T:
         raise ValueError("positions must be int64 [num_tokens]")
-    if cache is not None and (v is None or slot_mapping is None):
-        raise ValueError("a cache write needs v and slot_mapping")
-    if slot_mapping is not None and (slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T):
-        raise ValueError("slot_mapping must be int64 [num_tokens]")
-    _one_device(q_out, q, k, v, rope.freq, positions, slot_mapping, k_out, err_flags,
-                *((cache.k, cache.v) if cache is not None else ()))
-    dt = q.dtype
-    if dt not in (torch.float16, torch.bfloat16):
-        raise ValueError("q must be float16 or bfloat16")
-    qp, qs = _rows(q, "q", H, D, T, dt)
-    qop, qos = _rows(q_out, "q_out", H, D, T, dt)
-    kp, ks = _rows(k, "k", Hkv, D, T, dt)
-    vp, vs = _rows(v, "v", Hkv, D, T, dt) if cache is not None else (None, 0)
-    kop, kos = _rows(k_out, "k_out", Hkv, D, T, dt) if k_out is not None else (None, 0)
-    r = rope.c_struct()
-    _check(lib().pkv_rope_and_cache(ctypes.byref(cache.c_struct()) if cache is not None else None, ctypes.byref(r), qop,
-                                    qos, qp, qs, H, kop, kos, kp, ks, vp, vs, Hkv, D, _DT[dt], _ptr(positions),
-                                    _ptr(slot_mapping) if cache is not None else None, T, _err_ptr(err_flags),
-                                    _stream(stream)))
+    dev = _current_device()
+    qp, qs = _rows(q, "q", shape, dt, dev)
+    qop, qos = (qp, qs) if q_out is q else _rows(q_out, "q_out", shape, dt, dev)
+    kp, ks = _rows(k, "k", kv, dt, dev)
+    kop, kos = _rows(k_out, "k_out", kv, dt, dev) if k_out is not None else (None, 0)
+    c = slots = vp = None
+    vs = 0
+    if cache is not None:
+        if v is None or slot_mapping is None:
+            raise ValueError("a cache write needs v and slot_mapping")
+        if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+            raise ValueError("slot_mapping must be int64 [num_tokens]")
+        c, slots = _ref(cache.c_struct(dev)), _ptr(slot_mapping, dev)
+        vp, vs = _rows(v, "v", kv, dt, dev)
+    _check((_lib or lib()).pkv_rope_and_cache(c, _ref(rope.c_struct(dev)), qop, qos, qp, qs, H, kop, kos, kp, ks, vp, vs,
+                                              kv[1], D, _HALF[dt], _ptr(positions, dev), slots, T,
+                                              _err_ptr(err_flags, dev), _stream(stream, dev)))
     return q_out
 
 
@@ -433,10 +443,9 @@ def pkv_paged_attention_balanced(out: torch.Tensor, q: torch.Tensor, scale: floa
                                  workspace: torch.Tensor, err_flags: Optional[torch.Tensor] = None,
                                  stream=None) -> torch.Tensor:
     c, s = cache.c_struct(), seqs.c_struct()
-    _check(lib().pkv_paged_attention_balanced(_ptr(out), _DT[out.dtype], _ptr(q), _DT[q.dtype], int(q.shape[1]),
-                                              float(scale), ctypes.byref(c), ctypes.byref(s), _ptr(workspace),
-                                              int(workspace.numel() * workspace.element_size()),
-                                              _err_ptr(err_flags), _stream(stream)))
+    _check((_lib or lib()).pkv_paged_attention_balanced(_ptr(out), _DT[out.dtype], _ptr(q), _DT[q.dtype], q.shape[1],
+                                                        float(scale), _ref(c), _ref(s), _ptr(workspace), workspace.nbytes,
+                                                        _err_ptr(err_flags), _stream(stream)))
     return out
 
 
@@ -448,31 +457,31 @@ class Scores:
     doc_starts: Optional[torch.Tensor] = None         # int32 [B]: tokens before it are masked
     prefix_lens: Optional[torch.Tensor] = None        # int32 [B]: the first tokens, visible whatever else is masked
 
-    def c_struct(self, num_seqs: int, num_heads: int) -> _Scores:
-        for name, t, dt, n in (("distance_slopes", self.distance_slopes, torch.float32, num_heads),
-                               ("doc_starts", self.doc_starts, torch.int32, num_seqs),
-                               ("prefix_lens", self.prefix_lens, torch.int32, num_seqs)):
-            if t is not None and (t.dtype != dt or t.numel() != n):
-                raise ValueError(f"{name} must be {dt} [{n}]")
-        return _Scores(float(self.softcap), _ptr(self.distance_slopes), _ptr(self.doc_starts), _ptr(self.prefix_lens))
+    def c_struct(self, num_seqs: int, num_heads: int, device: Optional[int] = None) -> _Scores:
+        slopes, starts, prefix = self.distance_slopes, self.doc_starts, self.prefix_lens
+        if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != num_heads):
+            raise ValueError(f"distance_slopes must be float32 [{num_heads}]")
+        for name, t in (("doc_starts", starts), ("prefix_lens", prefix)):
+            if t is not None and (t.dtype != torch.int32 or t.numel() != num_seqs):
+                raise ValueError(f"{name} must be int32 [{num_seqs}]")
+        return _Scores(self.softcap, _ptr(slopes, device), _ptr(starts, device), _ptr(prefix, device))
 
 
 def pkv_paged_attention_scored(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
                                scores: Scores, workspace: torch.Tensor, err_flags: Optional[torch.Tensor] = None,
                                stream=None) -> torch.Tensor:
     """The balanced attention with capped and / or distance-biased scores and document / prefix masks."""
-    B, H, D = int(seqs.block_tables.shape[0]), int(q.shape[1]), cache.head_dim
-    if tuple(q.shape) != (B * seqs.q_len, H, D) or out.shape != q.shape or seqs.context_lens.numel() != B:
+    dev = _current_device()
+    c, s = cache.c_struct(dev), seqs.c_struct(dev)
+    B, H, shape = s.num_seqs, q.shape[1], q.shape
+    if shape != (B * s.q_len, H, c.head_dim) or out.shape != shape or seqs.context_lens.numel() != B:
         raise ValueError("q and out must be [num_seqs * q_len, num_heads, head_dim], context_lens [num_seqs]")
-    if q.dtype not in (torch.float16, torch.bfloat16) or out.dtype not in _DT:
+    qt, ot = _HALF.get(q.dtype), _DT.get(out.dtype)
+    if qt is None or ot is None:
         raise ValueError("q must be float16 or bfloat16, out one of them or float32")
-    _one_device(out, q, cache.k, cache.v, seqs.block_tables, seqs.context_lens, scores.distance_slopes,
-                scores.doc_starts, scores.prefix_lens, workspace, err_flags)
-    c, s, x = cache.c_struct(), seqs.c_struct(), scores.c_struct(B, H)
-    _check(lib().pkv_paged_attention_scored(_ptr(out), _DT[out.dtype], _ptr(q), _DT[q.dtype], H, float(scale),
-                                            ctypes.byref(c), ctypes.byref(s), ctypes.byref(x), _ptr(workspace),
-                                            int(workspace.numel() * workspace.element_size()), _err_ptr(err_flags),
-                                            _stream(stream)))
+    _check((_lib or lib()).pkv_paged_attention_scored(_ptr(out, dev), ot, _ptr(q, dev), qt, H, scale, _ref(c), _ref(s),
+                                                      _ref(scores.c_struct(B, H, dev)), _ptr(workspace, dev),
+                                                      workspace.nbytes, _err_ptr(err_flags, dev), _stream(stream, dev)))
     return out
 
 
