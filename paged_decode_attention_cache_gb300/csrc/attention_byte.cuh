@@ -9,27 +9,32 @@ namespace pkv {
 
 namespace {
 
-// Bytes 0 and 2 (ODD false) or 1 and 3 (ODD true) of w -> fp16x2.
-// int8: the exact integers (flip the sign bit, splice the byte under the
-// exponent of 1024, subtract 1024 + 128).  e4m3: sign, 4 exponent and 3
-// mantissa bits placed in fp16's fields, which is the exact value times 2^-8
-// (the exponent biases are 7 and 15; subnormals land on subnormals).  Every
-// code gives a finite number (e4m3's NaN pattern reads as 480 x 2^-8), so a slot
-// past the context never poisons a product with P = 0.
-template <bool E4M3, bool ODD>
-__device__ __forceinline__ uint32_t byte_pair_to_f16x2(uint32_t w) {
+__device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
+    __half2 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    const __half2 z = __hsub2(x, y);
+    uint32_t r;
+    memcpy(&r, &z, 4);
+    return r;
+}
+
+// Four codes (code i in byte i) -> fp16x2 of codes (0, 2) and (1, 3), exact.
+// int8: the byte goes under the exponent of 1024 with its sign bit flipped, which
+// is 1152 + code; subtract 1152.
+// e4m3: the conversion instruction, on bytes put in that order.  Its NaN codes
+// (0x7f, 0xff) come out NaN.
+template <bool E4M3>
+__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
     if constexpr (E4M3) {
-        if constexpr (ODD) return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
-        return ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+        const uint32_t x = __byte_perm(w, 0u, 0x3120);
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(even), "=r"(odd)
+            : "r"(x));
     } else {
-        const uint32_t x = __byte_perm(w ^ 0x80808080u, 0x64646464u, ODD ? 0x4341 : 0x4240);
-        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
-        __half2 h;
-        memcpy(&h, &x, 4);
-        h = __hsub2(h, bias);
-        uint32_t r;
-        memcpy(&r, &h, 4);
-        return r;
+        even = hsub2_u32((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
+        odd = hsub2_u32(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
     }
 }
 
@@ -45,9 +50,13 @@ __device__ __forceinline__ uint32_t byte_pair_to_f16x2(uint32_t w) {
 //      no bf16 query leaves fp16's range.
 //   V: codes to fp16 in the A operand (ldmatrix.trans of 16-bit words = 2 dims x
 //      2 tokens): the 16 dims of an M tile are a row's 16-byte chunk, even dims in
-//      rows 0-7, odd dims in rows 8-15.  The block's one V scale multiplies the
-//      block's product as it is added to the fp32 accumulators: folded into the
-//      fp16 P instead it would push small weights under fp16's range.
+//      rows 0-7, odd dims in rows 8-15.  The block's one V scale goes into P,
+//      relative to the largest scale seen so far (vref, a power of two; the
+//      accumulators are rescaled when it grows, as for the running maximum) and
+//      times 2^14, so that the operand P * scale / vref * 2^14 keeps its bits
+//      down to 2^-28 of the largest; the accumulators stay in the MMA.  (A
+//      multiply-add of each block's product onto the accumulators took 32 more
+//      instructions and as many registers.)
 //   P: fp16 hi + lo (two MMAs, P exact to ~2^-22): one fp16 P rounds each weight
 //      by 2^-12, as large an error as the rounding of an fp16 output.
 // 4 KB per block and kv head at D = 128: half the bf16 cache's bytes for about
@@ -63,17 +72,21 @@ struct TeMath {
     static constexpr int NMT = D / 16;     // M tiles of O^T
     static constexpr int KT = kBS * D;
     static constexpr int OFF_V = align_up(KT, 1024);
-    static constexpr int OFF_S = OFF_V + KT;   // {K scale, V scale}
     static constexpr int TX = 2 * KT;   // bytes the TMA copies deliver
-    static constexpr int STAGE = align_up(OFF_S + 16, 1024);
+    static constexpr int STAGE = 2 * KT;
+    // {K scale, V scale} of each stage, in an array of their own: behind the tiles
+    // they cost a stage 1 KB of padding, and the ring a quarter of its depth
+    // (copies alone, 8 x 65536 tokens: 135 us against 111 us)
+    static constexpr int kSide = 8;
     static constexpr int SCRATCH = 0;
     static constexpr bool kQ8 = true;
-    static constexpr float kUnit = E4M3 ? 256.f : 1.f;   // what the operand's numbers are short of the codes'
+    static constexpr float kPUnit = 16384.f;   // 2^14, see V
     static_assert(OFF_V % 1024 == 0 && STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
 
     uint32_t qb[NT][NKS][2];   // Q^T operand: query column g (+8), this thread's dims
     float o[NT][NMT][4];       // O^T: dims 16 mt + 2g, + 1 of query columns 2t, 2t + 1
     float m_run[NT][2], l_part[NT][2];   // query columns 2t, 2t + 1 (l: this thread's tokens)
+    float vref;                // o holds sum P V / (vref 2^-14)
     float kcol[NT][2];         // what turns the column's products into base-2 scores, but for the K scale
     int lim[NT][2];
     int lo_;       // first visible token
@@ -81,11 +94,12 @@ struct TeMath {
     ScoreMod<2 * NT> mod_;   // query columns 8 nt + 2t, + 1
     float scale_log2_;
 
-    static __device__ __forceinline__ void issue(uint8_t* dst, const CUtensorMap* km, const CUtensorMap* vm,
-                                                 const AttnParams& p, int kvh, int pb, uint64_t* bar) {
+    static __device__ __forceinline__ void issue(uint8_t* dst, uint8_t* side, const CUtensorMap* km,
+                                                 const CUtensorMap* vm, const AttnParams& p, int kvh, int pb,
+                                                 uint64_t* bar) {
         const size_t meta = size_t(pb) * p.num_kv_heads + kvh;
-        cp_async_4(dst + OFF_S, static_cast<const float*>(p.k_scale) + meta);
-        cp_async_4(dst + OFF_S + 4, static_cast<const float*>(p.v_scale) + meta);
+        cp_async_4(side, static_cast<const float*>(p.k_scale) + meta);
+        cp_async_4(side + 4, static_cast<const float*>(p.v_scale) + meta);
         cp_async_mbar_arrive(bar);
         mbar_arrive_expect_tx(bar, TX);
         const uint64_t pol = l2_evict_first_policy();
@@ -106,6 +120,7 @@ struct TeMath {
         lo_ = visible_lo<VAR>(p, s, ctx);
         if constexpr (VAR == kScored) mod_.begin(p, s, ctx);
         lim_lo_ = INT_MAX;
+        vref = 1.17549435e-38f;   // 2^-126
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int n = 8 * nt + g;
@@ -147,7 +162,7 @@ struct TeMath {
                 qb[nt][kk][1] = __byte_perm(qw[2 * kk], qw[2 * kk + 1], 0x7632);
             }
             // column 2t + e's factor sits in the lanes of g = 2t + e
-            const float kc = scale_log2_ * kUnit * back;
+            const float kc = scale_log2_ * back;
             kcol[nt][0] = __shfl_sync(0xffffffffu, kc, (2 * t) * 4);
             kcol[nt][1] = __shfl_sync(0xffffffffu, kc, (2 * t + 1) * 4);
 #pragma unroll
@@ -168,7 +183,7 @@ struct TeMath {
     }
 
     template <int VAR>
-    __device__ __forceinline__ void block(const uint8_t* stg, int pos0, int /*ntok*/, uint8_t*, int lane) {
+    __device__ __forceinline__ void block(const uint8_t* stg, const uint8_t* side, int pos0, int ntok, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const uint32_t stg_a = smem_addr(stg);
         // ------------------------------------------------ S^T = K Q^T (rows = tokens g, g + 8)
@@ -183,17 +198,15 @@ struct TeMath {
                 w[r][4 * i] = v.x; w[r][4 * i + 1] = v.y; w[r][4 * i + 2] = v.z; w[r][4 * i + 3] = v.w;
             }
         }
-        const float2 ss = *reinterpret_cast<const float2*>(stg + OFF_S);
+        const float2 ss = *reinterpret_cast<const float2*>(side);
         float sc[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < NKS; ++kk) {
             uint32_t a[4];
-            a[0] = byte_pair_to_f16x2<E4M3, false>(w[0][kk]);
-            a[1] = byte_pair_to_f16x2<E4M3, false>(w[1][kk]);
-            a[2] = byte_pair_to_f16x2<E4M3, true>(w[0][kk]);
-            a[3] = byte_pair_to_f16x2<E4M3, true>(w[1][kk]);
+            bytes_to_f16<E4M3>(w[0][kk], a[0], a[2]);
+            bytes_to_f16<E4M3>(w[1][kk], a[1], a[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], a, qb[nt][kk][0], qb[nt][kk][1]);
         }
@@ -239,29 +252,43 @@ struct TeMath {
                 m_run[nt][e] = mn;
                 rescale |= alpha[nt][e] != 1.f;
             }
+        float grow = 1.f;
+        if (fabsf(ss.y) > vref) {   // the same in every lane
+            const uint32_t up = min((__float_as_uint(fabsf(ss.y)) + 0x007fffffu) & 0xff800000u, 253u << 23);
+            const float ref = __uint_as_float(up);
+            grow = vref * __uint_as_float((254u << 23) - up);
+            vref = ref;
+            rescale = true;
+        }
         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f0 = alpha[nt][0] * grow, f1 = alpha[nt][1] * grow;
 #pragma unroll
                 for (int mt = 0; mt < NMT; ++mt) {
-                    o[nt][mt][0] *= alpha[nt][0]; o[nt][mt][2] *= alpha[nt][0];
-                    o[nt][mt][1] *= alpha[nt][1]; o[nt][mt][3] *= alpha[nt][1];
+                    o[nt][mt][0] *= f0; o[nt][mt][2] *= f0;
+                    o[nt][mt][1] *= f1; o[nt][mt][3] *= f1;
                 }
+            }
         }
         // ------------------------------------------------ P^T operand (tokens 2t.., query column g), hi and lo
         uint32_t ph[NT][2], pl[NT][2];
+        // scale / vref is exact but for a subnormal product: 1 / vref is a power of two
+        const float ratio = ss.y * __uint_as_float((254u << 23) - __float_as_uint(vref)) * kPUnit;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float x = sc[nt][2 * r], y = sc[nt][2 * r + 1];
+                const float x = sc[nt][2 * r] * ratio, y = sc[nt][2 * r + 1] * ratio;
                 const uint32_t h = pack2<false>(x, y);
                 const float2 hf = Half16<__half>::unpack2(h);
                 ph[nt][r] = movm_trans(h);
                 pl[nt][r] = movm_trans(pack2<false>(x - hf.x, y - hf.y));
             }
-        // ------------------------------------------------ O^T += v_scale * V^T P^T
-        const float vs = ss.y * kUnit;
+        // ------------------------------------------------ O^T += V^T P^T
+        // e4m3 V rows past the context may hold NaN codes: zero them in the operand
+        const uint32_t m01 = (2 * t < ntok ? 0x0000ffffu : 0u) | (2 * t + 1 < ntok ? 0xffff0000u : 0u);
+        const uint32_t m23 = (8 + 2 * t < ntok ? 0x0000ffffu : 0u) | (9 + 2 * t < ntok ? 0xffff0000u : 0u);
 #pragma unroll
         for (int c0 = 0; c0 < NMT; c0 += 2) {
             // matrices (transposed 16-bit words): tokens 0-7, 8-15 of chunk c0, then of chunk c0 + 1
@@ -272,23 +299,28 @@ struct TeMath {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t a[4];
-                a[0] = byte_pair_to_f16x2<E4M3, false>(X[2 * h]);
-                a[1] = byte_pair_to_f16x2<E4M3, true>(X[2 * h]);
-                a[2] = byte_pair_to_f16x2<E4M3, false>(X[2 * h + 1]);
-                a[3] = byte_pair_to_f16x2<E4M3, true>(X[2 * h + 1]);
+                bytes_to_f16<E4M3>(X[2 * h], a[0], a[1]);
+                bytes_to_f16<E4M3>(X[2 * h + 1], a[2], a[3]);
+                if (E4M3 && ntok < kBS) {
+                    a[0] &= m01; a[1] &= m01; a[2] &= m23; a[3] &= m23;
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(acc, a, ph[nt][0], ph[nt][1]);
-                    mma_f16(acc, a, pl[nt][0], pl[nt][1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[nt][c0 + h][i] = fmaf(acc[i], vs, o[nt][c0 + h][i]);
+                    mma_f16(o[nt][c0 + h], a, ph[nt][0], ph[nt][1]);
+                    mma_f16(o[nt][c0 + h], a, pl[nt][0], pl[nt][1]);
                 }
             }
         }
     }
 
     __device__ __forceinline__ void finish(int) {
+        const float unit = vref * (1.f / kPUnit);   // 0 if vref never grew: then every scale was 0, or no block came
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < NMT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][mt][i] *= unit;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
