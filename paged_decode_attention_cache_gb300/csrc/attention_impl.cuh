@@ -305,7 +305,6 @@ struct CcMath {
     static constexpr int TX = 2 * KT;                              // bytes landing per stage
     static constexpr int STAGE = 2 * KT;
     static constexpr int SCRATCH = align_up(kBS * G * 4 + kBS * G * 8 + G * 4, 16);   // per warp
-    static constexpr int kSide = 0;                                // bytes of a stage kept beside the tiles
     static_assert(CPL >= 1 && CH % LPT == 0, "bad lane split");
 
     float2 q2[G][CPL * 4];
@@ -540,7 +539,6 @@ struct TcMath {
     static constexpr int TX = KT + VT;   // bytes the TMA copies deliver
     static constexpr int STAGE = align_up(OFF_V + VT, 1024);
     static constexpr int SCRATCH = 0;
-    static constexpr int kSide = 0;
     static_assert(KIND != PKV_CACHE_K8V4, "K8/V4 runs TqMath");
     static_assert(OFF_V % 1024 == 0 && STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
 
@@ -786,7 +784,6 @@ struct TtMath {
     static constexpr int TX = KT + VT;   // bytes the TMA copies deliver
     static constexpr int STAGE = align_up(OFF_V + VT, 1024);
     static constexpr int SCRATCH = 0;
-    static constexpr int kSide = 0;
     static_assert(KIND != PKV_CACHE_K8V4, "K8/V4 runs TqMath");
     static_assert(OFF_V % 1024 == 0 && STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
 
@@ -1011,7 +1008,6 @@ struct TqMath {
     static constexpr int TX = KT + VT;   // bytes the TMA copies deliver
     static constexpr int STAGE = align_up(OFF_VZ + VS, 1024);
     static constexpr int SCRATCH = 0;
-    static constexpr int kSide = 0;
     static_assert(OFF_V % 1024 == 0 && STAGE % 1024 == 0, "swizzled tiles need 1 KB alignment");
     static_assert(OFF_VS % 16 == 0 && OFF_VZ % 16 == 0, "scale rows are read 16 bytes at a time");
 
@@ -1748,7 +1744,6 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     const bool own_ck = FUSED && !checks_fit(M, QL, D);
     float* ob = reinterpret_cast<float*>(ck + (own_ck ? kCheckBytes * NCW : 0));   // [NCW][M][D], ob_idx order
     uint8_t* scratch = reinterpret_cast<uint8_t*>(ob + size_t(NCW) * M * D);   // [NCW][SCRATCH]
-    uint8_t* side = scratch + NCW * Math::SCRATCH;                             // [S][kSide], 8-byte aligned
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tid = threadIdx.x;
@@ -1850,11 +1845,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                         pb = 0;   // load a valid block; the consumer masks it out
                     }
                     poison[st] = bad;
-                    if constexpr (Math::kSide > 0)
-                        Math::issue(smem + size_t(st) * Math::STAGE, side + st * Math::kSide, &k_map, &v_map, p, sg.kvh,
-                                    pb, &full[st]);
-                    else
-                        Math::issue(smem + size_t(st) * Math::STAGE, &k_map, &v_map, p, sg.kvh, pb, &full[st]);
+                    Math::issue(smem + size_t(st) * Math::STAGE, &k_map, &v_map, p, sg.kvh, pb, &full[st]);
                 }
                 issued += min(grp, n - i0);
                 __syncwarp();
@@ -1979,13 +1970,7 @@ attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
                 __syncwarp();
             }
-            if (ntok > 0) {
-                const uint8_t* stg = smem + size_t(st) * Math::STAGE;
-                if constexpr (Math::kSide > 0)
-                    mth.template block<VAR>(stg, side + st * Math::kSide, b * kBS, ntok, lane);
-                else
-                    mth.template block<VAR>(stg, b * kBS, ntok, my_scratch, lane);
-            }
+            if (ntok > 0) mth.template block<VAR>(smem + size_t(st) * Math::STAGE, b * kBS, ntok, my_scratch, lane);
             // generic writes into a stage the TMA refills: order them before the refill
             if (FUSED && patched) fence_proxy_async_smem();
             __syncwarp();
@@ -2197,8 +2182,7 @@ template <class Math, bool FUSED>
 int smem_bytes(int stages, int M, int QL, int D) {
     constexpr int NCW = Math::NCW;
     return stages * Math::STAGE + 16 * stages + 4 * stages + 16 + kRedSlots * 8 + 16 + 2 * NCW * kMaxRows * 4 +
-           (FUSED && !checks_fit(M, QL, D) ? NCW * kCheckBytes : 0) + NCW * M * D * 4 + NCW * Math::SCRATCH +
-           stages * Math::kSide + 1024 + 64;
+           (FUSED && !checks_fit(M, QL, D) ? NCW * kCheckBytes : 0) + NCW * M * D * 4 + NCW * Math::SCRATCH + 1024 + 64;
 }
 
 template <class Math, bool FUSED, int VAR>
@@ -2212,7 +2196,7 @@ cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& 
     }
     const int M = (p.num_heads / p.num_kv_heads) * p.q_len;
     const int base = smem_bytes<Math, FUSED>(0, M, p.q_len, p.head_dim);
-    int stages = (kSmemLimit - base) / (Math::STAGE + 20 + Math::kSide);
+    int stages = (kSmemLimit - base) / (Math::STAGE + 20);
     if (stages > 9 * Math::NCW) stages = 9 * Math::NCW;
     stages = stages / Math::NCW * Math::NCW;   // every stage always belongs to the same consumer warp
     if (stages < Math::NCW) return cudaErrorInvalidConfiguration;

@@ -212,7 +212,9 @@ def want_attention(st, qr, ctx, q_len, scale, **more):
     return out, biggest, max([1e-30] + [np.abs(x).max() for x in v if x.size])
 
 
-def close(got, want, biggest, vmax, dtype=torch.float32, p_bits=22):
+def close(got, want, biggest, vmax, dtype=torch.float32, p_bits=None):
+    # the 8-bit caches' weights: one fp16 operand (half a step: 2^-11) for a bf16 output, hi + lo for the others
+    p_bits = p_bits or (11 if dtype == torch.bfloat16 else 22)
     a, r = R.tolerance(biggest, vmax, dtype, p_bits)
     got = got.double().cpu().numpy()
     err = np.abs(got - want)

@@ -13,7 +13,7 @@ from tests.test_gpu_blocks import State, close, rows, tables_for
 
 pytestmark = pytest.mark.gpu
 SRC = {"bf16": torch.bfloat16, "f16": torch.float16}
-P_BITS = {"bf16": 17, "f16": 22, "i8": 22, "e4m3": 22}
+P_BITS = {"bf16": 17, "f16": 22}   # 8-bit caches: close() goes by the output type
 K8V4_ABS = 2e-2
 
 
@@ -108,7 +108,7 @@ def run(rng, kind, dt, ctx, H, Hkv, D, ql, window=0, cap=0.0, slopes=None, start
             got = g.out.double().cpu().numpy()
             assert np.isfinite(got).all() and np.abs(got - want).max() <= K8V4_ABS
         else:
-            close(g.out, want, biggest, vmax, odt, P_BITS[kind])
+            close(g.out, want, biggest, vmax, odt, P_BITS.get(kind))
     return g.out, (q, cache, seqs, ws)
 
 
