@@ -15,8 +15,9 @@
 // e4m3 code keeps its value exactly unless it turns subnormal.  The price is up
 // to one part in five of int8's range (a tenth on average).
 //
-// Bound: HBM for prompts (4 bytes read and 2 written per element of K + V),
-// dependent-load latency for a decode step (length -> table -> scale, row).
+// Bound: HBM for prompts (4 bytes read and 2 written per element of K + V: 83 MB in
+// 16.0 us, 5.2 TB/s), dependent-load latency for a decode step (length -> table ->
+// scale; 64 tokens of 8 heads in 2.5 us).
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -54,7 +55,9 @@ __device__ __forceinline__ float scale_for(float amax) {
     return t > 0.f ? fmaxf(up, 1.17549435e-38f) : 0.f;
 }
 
-// Four numbers already divided by the scale -> four codes.
+// Four numbers already divided by the scale -> four codes.  int8: adding 1.5 x 2^23
+// leaves the number rounded half to even in the low mantissa bits (|x| <= 127 by the
+// scale's choice), one addition where rounding and converting take the slow pipe twice.
 template <bool E4M3>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     if constexpr (E4M3) {
@@ -62,8 +65,8 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
         return lo | (hi << 16);
     } else {
-        auto q = [](float x) { return uint32_t(int(fminf(fmaxf(rintf(x), -127.f), 127.f))) & 0xffu; };
-        return q(a) | (q(b) << 8) | (q(c) << 16) | (q(d) << 24);
+        auto q = [](float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); };
+        return __byte_perm(__byte_perm(q(a), q(b), 0x0040), __byte_perm(q(c), q(d), 0x0040), 0x5410);
     }
 }
 
@@ -74,22 +77,29 @@ __device__ __forceinline__ float code_value(uint32_t byte) {
     return float(int(int8_t(byte)));
 }
 
-// The sequence whose new tokens hold unit `u` of the work list, where sequence
-// s's units start at cu[s] / 16 + 2 s (at least as far apart as the blocks its
-// tokens can touch).  All 32 lanes probe the remaining range at once.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int num_seqs, int num_tokens, int u, int lane) {
-    int lo = 0, hi = num_seqs;   // start(lo) <= u, the answer is in [lo, hi)
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int s = lo + lane * step;
-        const bool le = s < hi && min(max(cu[s], 0), num_tokens) / kBlock + 2 * s <= u;
-        const uint32_t m = __ballot_sync(0xffffffffu, le) | 1u;
-        const int last = 31 - __clz(m);   // the last probe that starts at or before u
-        const int nlo = lo + last * step;
-        hi = min(hi, nlo + step);
-        lo = nlo;
+// What unit `u` of the work list belongs to: sequence s, whose units start at
+// cu[s] / 16 + 2 s (at least as far apart as the blocks its tokens can touch), its
+// rows [c0, c1) and its context.  All lanes probe the remaining range at once, and the
+// last round brings what the caller needs next with it.
+struct UnitSeq {
+    int s, c0, c1, ctx;
+};
+__device__ __forceinline__ UnitSeq find_seq(const BlockWriteParams& p, int u, int lane) {
+    int lo = 0, hi = p.num_seqs;   // start(lo) <= u, the answer is in [lo, hi)
+    auto start = [&](int c, int s) { return min(max(c, 0), p.num_tokens) / kBlock + 2 * s; };
+    while (hi - lo > 31) {
+        const int step = (hi - lo + 31) / 32, s = lo + lane * step;
+        const uint32_t m = __ballot_sync(0xffffffffu, s < hi && start(p.cu_new[min(s, p.num_seqs)], s) <= u) | 1u;
+        lo += (31 - __clz(m)) * step;   // the last probe that starts at or before u
+        hi = min(hi, lo + step);
     }
-    return lo;
+    const int s = lo + lane;
+    const int c = min(max(p.cu_new[min(s, p.num_seqs)], 0), p.num_tokens);
+    const int ctx = p.context_lens[min(s, p.num_seqs - 1)];
+    const uint32_t m = __ballot_sync(0xffffffffu, s < hi && start(c, s) <= u) | 1u;
+    const int last = 31 - __clz(m);
+    return {lo + last, __shfl_sync(0xffffffffu, c, last), __shfl_sync(0xffffffffu, c, last + 1),
+            __shfl_sync(0xffffffffu, ctx, last)};
 }
 
 template <typename Src, bool E4M3, int D>
@@ -108,23 +118,23 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParam
     const int u = int((w >> 1) / H);
 
     // ---- this unit's sequence, its new tokens and the block
-    int s, i, n, row0;
+    int s, i, n, row0, ctx;
     if (p.cu_new) {
-        s = find_seq(p.cu_new, p.num_seqs, p.num_tokens, u, lane);
-        const int c0 = min(max(p.cu_new[s], 0), p.num_tokens), c1 = min(max(p.cu_new[s + 1], 0), p.num_tokens);
-        i = u - (c0 / kBlock + 2 * s);
-        n = c1 - c0;
-        row0 = c0;
+        const UnitSeq q = find_seq(p, u, lane);
+        s = q.s;
+        i = u - (q.c0 / kBlock + 2 * s);
+        n = q.c1 - q.c0;
+        row0 = q.c0;
+        ctx = q.ctx;
     } else {
         const int per = (p.q_len + 14) / kBlock + 1;
         s = u / per;
         i = u - s * per;
         n = p.q_len;
         row0 = s * p.q_len;
+        ctx = p.context_lens[s];
     }
-    if (i < 0 || n <= 0) return;
-    const int ctx = p.context_lens[s];
-    if (ctx <= 0) return;
+    if (i < 0 || n <= 0 || ctx <= 0) return;
     const int cap = p.max_blocks * kBlock;
     if (ctx > cap && i == 0 && h == 0 && which == 0 && lane == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
     const int p0 = max(ctx - n, 0), p1 = min(ctx, cap);   // positions written: [p0, p1)
@@ -134,19 +144,11 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParam
     const int b = int(b64);
     const int a = max(p0 - b * kBlock, 0), e = min(p1 - b * kBlock, kBlock);   // new rows [a, e) of the block
     const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
-    if (pb < 0 || pb >= p.num_blocks) {
-        if (h == 0 && which == 0 && lane == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
-        return;
-    }
-    const int64_t meta = int64_t(pb) * H + h;
-    float* scale_at = (which ? p.v_scale : p.k_scale) + meta;
-    uint8_t* codes = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache) + (int64_t(pb) * kBlock * H + h) * D;
     const uint16_t* src = static_cast<const uint16_t*>(which ? p.v_new : p.k_new);
     const int r0 = lane / LPR, d0 = (lane % LPR) * 8;
 
-    // ---- the new rows and their largest magnitude
+    // ---- the new rows, which do not wait for the table entry
     uint4 x[NP];
-    uint32_t m2 = 0;
     const int64_t src_row = int64_t(row0) + int64_t(b) * kBlock - (int64_t(ctx) - n);   // row of offset 0
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
@@ -154,6 +156,16 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParam
         x[k] = make_uint4(0u, 0u, 0u, 0u);
         if (r >= a && r < e) x[k] = __ldg(reinterpret_cast<const uint4*>(src + ((src_row + r) * H + h) * D + d0));
     }
+    if (pb < 0 || pb >= p.num_blocks) {
+        if (h == 0 && which == 0 && lane == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
+        return;
+    }
+    const int64_t meta = int64_t(pb) * H + h;
+    float* scale_at = (which ? p.v_scale : p.k_scale) + meta;
+    uint8_t* codes = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache) + (int64_t(pb) * kBlock * H + h) * D;
+
+    // ---- the scale: the largest magnitude of the new rows, and the block's own
+    uint32_t m2 = 0;
     float s_old = a > 0 ? *scale_at : 0.f;
     if (!(s_old > 0.f) || isinf(s_old)) s_old = 0.f;
 #pragma unroll
@@ -198,15 +210,40 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParam
     if (lane == 0) *scale_at = s_new;
 }
 
-// CTA (b, s) expands logical block b of sequence s; a thread takes 8 dims of
-// one (token, kv head): an 8-byte load and a 16-byte store each for K and V.
+// 16 codes -> 16 values of OutT.
+template <typename OutT, bool E4M3>
+__device__ __forceinline__ void expand16(uint4 c, float scale, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const uint32_t two = (w[q / 2] >> (16 * (q & 1))) & 0xffffu;
+        const float x = code_value<E4M3>(two & 0xffu) * scale, y = code_value<E4M3>(two >> 8) * scale;
+        if constexpr (std::is_same<OutT, __nv_bfloat16>::value) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+            memcpy(o + q, &v, 4);
+        } else {
+            const __half2 v = __floats2half2_rn(x, y);
+            memcpy(o + q, &v, 4);
+        }
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// CTA (b, s) expands logical block b of sequence s.  A thread takes 16 dims of one
+// (token, kv head), K and V: 16-byte loads, two 16-byte stores each; two such items are
+// loaded before the first is stored.  Bound by HBM, which writes two bytes for each it
+// reads: 5.6 TB/s at 375 MB, 4.9 at 149 MB (8-byte loads, one item at a time: 3.3).
 template <typename OutT, bool E4M3, int D>
 __global__ void __launch_bounds__(kThreads) gather_blocks_kernel(GatherParams p) {
     grid_dep_wait();
     grid_dep_launch();
-    constexpr int CPT = D / 8;
+    constexpr int CPT = D / 16, U = 2;
     const int s = blockIdx.y, b = blockIdx.x;
     int ctx = p.context_lens[s];
+    const int64_t row0 = p.cu_seq_lens[s];
+    const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
     const int cap = p.max_blocks * kBlock;
     if (ctx > cap) {
         if (b == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
@@ -215,36 +252,39 @@ __global__ void __launch_bounds__(kThreads) gather_blocks_kernel(GatherParams p)
     const int t0 = b * kBlock;
     if (t0 >= ctx) return;
     const int ntok = min(kBlock, ctx - t0);
-    const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
     if (pb < 0 || pb >= p.num_blocks) {
         if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
         return;
     }
     const int H = p.num_kv_heads;
-    const int64_t src0 = int64_t(pb) * kBlock * H * D, dst0 = (int64_t(p.cu_seq_lens[s]) + t0) * H * D;
+    const int64_t src0 = int64_t(pb) * kBlock * H * D, dst0 = (row0 + t0) * H * D;
     const int n = ntok * H * CPT;   // the block's first ntok token rows are contiguous on both sides
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int h = (i / CPT) % H;
-        const float scales[2] = {__ldg(static_cast<const float*>(p.k_scale) + int64_t(pb) * H + h),
-                                 __ldg(static_cast<const float*>(p.v_scale) + int64_t(pb) * H + h)};
+    for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+        uint4 c[U][2];
+        float sc[U][2];
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(which ? p.v_cache : p.k_cache) + src0) + i);
-            uint32_t o[4];
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i >= n) break;
+            const int64_t meta = int64_t(pb) * H + (i / CPT) % H;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t two = ((q < 2 ? c.x : c.y) >> (16 * (q & 1))) & 0xffffu;
-                const float x = code_value<E4M3>(two & 0xffu) * scales[which], y = code_value<E4M3>(two >> 8) * scales[which];
-                if constexpr (std::is_same<OutT, __nv_bfloat16>::value) {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                    memcpy(o + q, &v, 4);
-                } else {
-                    const __half2 v = __floats2half2_rn(x, y);
-                    memcpy(o + q, &v, 4);
-                }
+            for (int w = 0; w < 2; ++w) {
+                c[u][w] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w ? p.v_cache : p.k_cache) + src0) + i);
+                sc[u][w] = __ldg(static_cast<const float*>(w ? p.v_scale : p.k_scale) + meta);
             }
-            *(reinterpret_cast<uint4*>(static_cast<OutT*>(which ? p.v_out : p.k_out) + dst0) + i) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kThreads;
+            if (i >= n) break;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                uint4* out = reinterpret_cast<uint4*>(static_cast<OutT*>(w ? p.v_out : p.k_out) + dst0);
+                uint4 lo, hi;
+                expand16<OutT, E4M3>(c[u][w], sc[u][w], lo, hi);
+                out[2 * i] = lo;
+                out[2 * i + 1] = hi;
+            }
         }
     }
 }
