@@ -2,7 +2,9 @@
 
 Each translation unit is compiled for sm_103a only, in parallel, then linked
 into one shared library with the CUDA runtime linked statically.  A rebuild
-happens only when a source or header is newer than the library.
+happens only when a source or header is newer than the library.  Beside it,
+g++ builds _binding.so (csrc/binding.cpp, a CPython module against torch's
+headers): the Python side of the decode step's calls.
 
 ``build(timeline=True)`` builds the same sources with -DPKV_TIMELINE into
 libpkv_timeline.so: the attention kernels then stamp %globaltimer at fixed
@@ -23,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpkv.so")
 OBJDIR = os.path.join(PKG, "_build")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 LIB_TIMELINE = os.path.join(PKG, "libpkv_timeline.so")
 OBJDIR_TIMELINE = os.path.join(PKG, "_build_timeline")
 
@@ -54,9 +58,32 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
+def build_binding(force: bool = False) -> str:
+    """_binding.so: reads torch tensors and calls libpkv.so, which it loads when told to."""
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "pkv.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING + f".tmp.{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, timeline: bool = False) -> str:
     lib, objdir = (LIB_TIMELINE, OBJDIR_TIMELINE) if timeline else (LIB, OBJDIR)
     if not force and not stale(lib):
+        build_binding()
         return lib
     nvcc = _nvcc()
     os.makedirs(objdir, exist_ok=True)
@@ -73,8 +100,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         return obj, r.stderr
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(compile_one, srcs))
+        binding.result()
     if verbose or ptxas_info:
         for (_, log), src in zip(results, srcs):
             if log.strip():

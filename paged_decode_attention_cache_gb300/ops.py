@@ -4,7 +4,9 @@ Argument marshalling only: every function checks dtypes, devices and
 contiguity of the torch tensors it is given, passes their device pointers and
 the current CUDA stream to the C entry point of the same name, and raises
 ``PkvError`` with the library's message on a non-OK status.  There is no CPU
-path: if the library is not built, every call raises.
+path: if the library is not built, every call raises.  The calls that a decode
+step makes go through a CPython module (csrc/binding.cpp), the others through
+ctypes.
 """
 from __future__ import annotations
 
@@ -22,9 +24,7 @@ PKV_F16, PKV_BF16, PKV_F32 = 0, 1, 2
 PKV_CACHE_F16, PKV_CACHE_BF16, PKV_CACHE_K8V4, PKV_CACHE_I8, PKV_CACHE_E4M3 = 0, 1, 2, 3, 4
 DEVERR_OOB_BLOCK, DEVERR_OOB_SLOT, DEVERR_CAPACITY, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
-_HALF = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
-_DT = {**_HALF, torch.float32: PKV_F32}
-_ref = ctypes.byref
+_DT = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
 _CACHE_KIND = {"f16": PKV_CACHE_F16, "bf16": PKV_CACHE_BF16, "k8v4": PKV_CACHE_K8V4, "i8": PKV_CACHE_I8,
                "e4m3": PKV_CACHE_E4M3}
 # 8-bit caches with one scale per (block, kv head): the code tensors' dtypes
@@ -156,35 +156,40 @@ def lib():
     return _lib
 
 
+_binding = None
+
+
+def _calls():
+    """The CPython module of the decode step's calls, with the selected library loaded."""
+    global _binding
+    if _binding is None:
+        lib()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"{_build.BINDING} is not built: call __graft_entry__.build()")
+        from . import _binding as module
+        module.load(library_path())
+        _binding = module
+    return _binding
+
+
 def _check(status: int):
     if status != PKV_OK:
         msg = lib().pkv_last_error().decode()
         raise PkvError(status, msg or lib().pkv_status_string(status).decode())
 
 
-def _ptr(t: Optional[torch.Tensor], device: Optional[int] = None):
-    """A tensor's address; with `device` (_current_device()), it has to live there."""
+def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("pkv tensors must live on a CUDA device")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"pkv tensors must live on the current CUDA device ({device}), not {t.device}")
     if not t.is_contiguous():
         raise ValueError("pkv tensors must be contiguous")
     return t.data_ptr()
 
 
-# A decode step's calls are short: the index of the current device and its
-# current stream as integers, without the objects torch.cuda makes for them
-# (current_stream() alone takes 2.9 us of a 19 us call).
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-
-
-def _stream(stream: Optional[torch.cuda.Stream], device: Optional[int] = None) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(_current_device() if device is None else device)
+def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 @dataclass
@@ -210,7 +215,7 @@ class Cache:
     def head_dim(self):
         return int(self.k.shape[3])
 
-    def c_struct(self, device: Optional[int] = None) -> _Cache:
+    def c_struct(self) -> _Cache:
         k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
         nb, bs, hkv, d = shape = k.shape
         codes = _BYTE_CODES.get(self.kind)
@@ -221,8 +226,8 @@ class Cache:
                     ks.dtype != torch.float32 or vs.dtype != torch.float32:
                 raise ValueError(f"a {self.kind} cache has k and v of one shape and float32 scales "
                                  f"[num_blocks, num_kv_heads]")
-        return _Cache(_CACHE_KIND[self.kind], nb, bs, hkv, d, self.v_group, _ptr(k, device), _ptr(v, device),
-                      _ptr(ks, device), _ptr(vs, device), _ptr(self.v_zero, device))
+        return _Cache(_CACHE_KIND[self.kind], nb, bs, hkv, d, self.v_group, _ptr(k), _ptr(v),
+                      _ptr(ks), _ptr(vs), _ptr(self.v_zero))
 
     @staticmethod
     def empty(kind: str, num_blocks: int, num_kv_heads: int, head_dim: int, device="cuda") -> "Cache":
@@ -249,20 +254,20 @@ class Seqs:
     q_len: int = 1
     sliding_window: int = 0      # 0: none; W: only the last W stored tokens are visible
 
-    def c_struct(self, device: Optional[int] = None) -> _Seqs:
+    def c_struct(self) -> _Seqs:
         bt, cl = self.block_tables, self.context_lens
         if bt.dtype != torch.int32 or cl.dtype != torch.int32:
             raise ValueError("block_tables and context_lens must be int32")
         n, mb = bt.shape
-        return _Seqs(_ptr(bt, device), _ptr(cl, device), n, mb, int(self.q_len), int(self.sliding_window))
+        return _Seqs(_ptr(bt), _ptr(cl), n, mb, int(self.q_len), int(self.sliding_window))
 
 
-def _err_ptr(err: Optional[torch.Tensor], device: Optional[int] = None):
+def _err_ptr(err: Optional[torch.Tensor]):
     if err is None:
         return None
     if err.dtype not in (torch.int32, torch.uint32) or err.numel() < 1:
         raise ValueError("err_flags must be a device int32/uint32 tensor")
-    return _ptr(err, device)
+    return _ptr(err)
 
 
 def pkv_reshape_and_cache(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
@@ -289,24 +294,11 @@ def pkv_quantize_kv_blocks(cache: Cache, k_new: torch.Tensor, v_new: torch.Tenso
     """Append each sequence's new tokens (its last ones: rows cu_new_lens[s] ..
     cu_new_lens[s + 1] of k_new / v_new, or q_len rows each) to an "i8" or
     "e4m3" cache; a block's scale grows when they need it."""
-    dt = _HALF.get(k_new.dtype)
-    if dt is None or v_new.dtype != k_new.dtype:
-        raise ValueError("k_new / v_new must both be float16 or both bfloat16")
-    dev = _current_device()
-    c, s = cache.c_struct(dev), seqs.c_struct(dev)
-    shape = k_new.shape
-    if shape[1:] != (c.num_kv_heads, c.head_dim) or v_new.shape != shape:
-        raise ValueError("k_new / v_new must be [num_tokens, num_kv_heads, head_dim]")
-    if seqs.context_lens.numel() != s.num_seqs:
-        raise ValueError("context_lens must be [num_seqs]")
-    if cu_new_lens is not None and (cu_new_lens.dtype != torch.int32 or cu_new_lens.numel() != s.num_seqs + 1):
-        raise ValueError("cu_new_lens must be int32 [num_seqs + 1]")
-    _check((_lib or lib()).pkv_quantize_kv_blocks(_ref(c), _ptr(k_new, dev), _ptr(v_new, dev), dt, shape[0],
-                                                  _ptr(cu_new_lens, dev), _ref(s), _err_ptr(err_flags, dev),
-                                                  _stream(stream, dev)))
+    st = (_binding or _calls()).quantize_kv_blocks(cache, k_new, v_new, seqs, cu_new_lens, err_flags, stream)
+    if st:
+        _check(st)
 
 
-_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 _ROPE_SCALE = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
@@ -317,14 +309,6 @@ class Rope:
     rotary_dim: int
     layout: str = "half"      # "half": pairs (i, i + rotary_dim/2); "interleaved": pairs (2i, 2i + 1)
     mscale: float = 1.0
-
-    def c_struct(self, device: Optional[int] = None) -> _Rope:
-        if self.freq.dtype != torch.int64 or self.freq.numel() * 2 != self.rotary_dim:
-            raise ValueError("freq must be int64 [rotary_dim / 2]")
-        layout = _ROPE_LAYOUT.get(self.layout)
-        if layout is None:
-            raise ValueError(f"layout {self.layout!r}: 'half' or 'interleaved'")
-        return _Rope(_ptr(self.freq, device), self.rotary_dim, layout, self.mscale)
 
 
 def pkv_rope_frequencies(rotary_dim: int, base: float, scaling: str = "none", factor: float = 1.0,
@@ -342,20 +326,6 @@ def pkv_rope_frequencies(rotary_dim: int, base: float, scaling: str = "none", fa
     return freq
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: int):
-    """Address and row stride of a [tokens, heads, head_dim] view whose rows are contiguous."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"pkv tensors must live on the current CUDA device ({device}), not {t.device}")
-    tokens, heads, head_dim = shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != head_dim and heads > 1):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    # one row (or none): any stride will do
-    return t.data_ptr(), s0 if tokens > 1 else heads * head_dim
-
-
 def pkv_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], rope: Rope,
                        positions: torch.Tensor, cache: Optional[Cache] = None,
                        slot_mapping: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
@@ -363,30 +333,10 @@ def pkv_rope_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     """Rotate q into q_out and k into its cache slot and / or k_out, and write v
     into its slot, in one launch.  q, k, v may be views of one packed projection
     (any row stride that is a multiple of 8); q_out may be q and k_out may be k."""
-    dt, shape = q.dtype, q.shape
-    T, H, D = shape
-    kv = (T, k.shape[1], D)
-    if dt not in _HALF:
-        raise ValueError("q must be float16 or bfloat16")
-    if positions.dtype != torch.int64 or positions.numel() != T:
-        raise ValueError("positions must be int64 [num_tokens]")
-    dev = _current_device()
-    qp, qs = _rows(q, "q", shape, dt, dev)
-    qop, qos = (qp, qs) if q_out is q else _rows(q_out, "q_out", shape, dt, dev)
-    kp, ks = _rows(k, "k", kv, dt, dev)
-    kop, kos = _rows(k_out, "k_out", kv, dt, dev) if k_out is not None else (None, 0)
-    c = slots = vp = None
-    vs = 0
-    if cache is not None:
-        if v is None or slot_mapping is None:
-            raise ValueError("a cache write needs v and slot_mapping")
-        if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
-            raise ValueError("slot_mapping must be int64 [num_tokens]")
-        c, slots = _ref(cache.c_struct(dev)), _ptr(slot_mapping, dev)
-        vp, vs = _rows(v, "v", kv, dt, dev)
-    _check((_lib or lib()).pkv_rope_and_cache(c, _ref(rope.c_struct(dev)), qop, qos, qp, qs, H, kop, kos, kp, ks, vp, vs,
-                                              kv[1], D, _HALF[dt], _ptr(positions, dev), slots, T,
-                                              _err_ptr(err_flags, dev), _stream(stream, dev)))
+    st = (_binding or _calls()).rope_and_cache(q_out, q, k, v, rope, positions, cache, slot_mapping, k_out, err_flags,
+                                               stream)
+    if st:
+        _check(st)
     return q_out
 
 
@@ -442,10 +392,9 @@ def balanced_workspace(num_seqs: int, num_kv_heads: int, head_dim: int, device="
 def pkv_paged_attention_balanced(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
                                  workspace: torch.Tensor, err_flags: Optional[torch.Tensor] = None,
                                  stream=None) -> torch.Tensor:
-    c, s = cache.c_struct(), seqs.c_struct()
-    _check((_lib or lib()).pkv_paged_attention_balanced(_ptr(out), _DT[out.dtype], _ptr(q), _DT[q.dtype], q.shape[1],
-                                                        float(scale), _ref(c), _ref(s), _ptr(workspace), workspace.nbytes,
-                                                        _err_ptr(err_flags), _stream(stream)))
+    st = (_binding or _calls()).paged_attention_balanced(out, q, scale, cache, seqs, workspace, err_flags, stream)
+    if st:
+        _check(st)
     return out
 
 
@@ -457,31 +406,14 @@ class Scores:
     doc_starts: Optional[torch.Tensor] = None         # int32 [B]: tokens before it are masked
     prefix_lens: Optional[torch.Tensor] = None        # int32 [B]: the first tokens, visible whatever else is masked
 
-    def c_struct(self, num_seqs: int, num_heads: int, device: Optional[int] = None) -> _Scores:
-        slopes, starts, prefix = self.distance_slopes, self.doc_starts, self.prefix_lens
-        if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != num_heads):
-            raise ValueError(f"distance_slopes must be float32 [{num_heads}]")
-        for name, t in (("doc_starts", starts), ("prefix_lens", prefix)):
-            if t is not None and (t.dtype != torch.int32 or t.numel() != num_seqs):
-                raise ValueError(f"{name} must be int32 [{num_seqs}]")
-        return _Scores(self.softcap, _ptr(slopes, device), _ptr(starts, device), _ptr(prefix, device))
-
 
 def pkv_paged_attention_scored(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
                                scores: Scores, workspace: torch.Tensor, err_flags: Optional[torch.Tensor] = None,
                                stream=None) -> torch.Tensor:
     """The balanced attention with capped and / or distance-biased scores and document / prefix masks."""
-    dev = _current_device()
-    c, s = cache.c_struct(dev), seqs.c_struct(dev)
-    B, H, shape = s.num_seqs, q.shape[1], q.shape
-    if shape != (B * s.q_len, H, c.head_dim) or out.shape != shape or seqs.context_lens.numel() != B:
-        raise ValueError("q and out must be [num_seqs * q_len, num_heads, head_dim], context_lens [num_seqs]")
-    qt, ot = _HALF.get(q.dtype), _DT.get(out.dtype)
-    if qt is None or ot is None:
-        raise ValueError("q must be float16 or bfloat16, out one of them or float32")
-    _check((_lib or lib()).pkv_paged_attention_scored(_ptr(out, dev), ot, _ptr(q, dev), qt, H, scale, _ref(c), _ref(s),
-                                                      _ref(scores.c_struct(B, H, dev)), _ptr(workspace, dev),
-                                                      workspace.nbytes, _err_ptr(err_flags, dev), _stream(stream, dev)))
+    st = (_binding or _calls()).paged_attention_scored(out, q, scale, cache, seqs, scores, workspace, err_flags, stream)
+    if st:
+        _check(st)
     return out
 
 
@@ -622,11 +554,6 @@ def pkv_gather_kv_cache(k_out: torch.Tensor, v_out: torch.Tensor, cu_seq_lens: t
 def pkv_gather_kv_cache_dequant(k_out: torch.Tensor, v_out: torch.Tensor, cu_seq_lens: torch.Tensor, cache: Cache,
                                 seqs: Seqs, err_flags=None, stream=None) -> None:
     """K8/V4, int8 or e4m3 cache -> contiguous fp16/bf16 (the dtype of k_out) K and V rows."""
-    if cu_seq_lens.dtype != torch.int32:
-        raise ValueError("cu_seq_lens must be int32")
-    if k_out.dtype != v_out.dtype or k_out.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError("k_out / v_out must both be float16 or both bfloat16")
-    c, s = cache.c_struct(), seqs.c_struct()
-    _check(lib().pkv_gather_kv_cache_dequant(_ptr(k_out), _ptr(v_out), _DT[k_out.dtype], _ptr(cu_seq_lens),
-                                             ctypes.byref(c), ctypes.byref(s), _err_ptr(err_flags),
-                                             _stream(stream)))
+    st = (_binding or _calls()).gather_kv_cache_dequant(k_out, v_out, cu_seq_lens, cache, seqs, err_flags, stream)
+    if st:
+        _check(st)
