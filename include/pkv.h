@@ -183,7 +183,10 @@ pkv_status pkv_quantize_kv(const pkv_cache *cache, const void *k_new, const void
  * covers all its tokens, so the call is by sequence and position, not by slot:
  * the n_s new tokens of sequence s are its last ones, positions
  * [context_lens[s] - n_s, context_lens[s]).
- *   k_new, v_new  [num_tokens, num_kv_heads, head_dim], src_dtype PKV_F16 or PKV_BF16.
+ *   k_new, v_new  rows of [num_kv_heads, head_dim], num_tokens of them, consecutive
+ *                 rows k_stride / v_stride ELEMENTS apart (a multiple of 8, at least
+ *                 a row: values straight from a packed q/k/v projection);
+ *                 src_dtype PKV_F16 or PKV_BF16.
  *   cu_new_lens   int32 [num_seqs + 1] device: sequence s's rows are cu[s] ..
  *                 cu[s+1] - 1 (n_s may be 0; cu[num_seqs] <= num_tokens), or NULL:
  *                 seqs->q_len rows each, and num_tokens = num_seqs * q_len.
@@ -203,9 +206,10 @@ pkv_status pkv_quantize_kv(const pkv_cache *cache, const void *k_new, const void
  * block (shared prefix blocks are complete, so they never do): its contents
  * would be unspecified.
  */
-pkv_status pkv_quantize_kv_blocks(const pkv_cache *cache, const void *k_new, const void *v_new,
-                                  pkv_dtype src_dtype, int32_t num_tokens, const int32_t *cu_new_lens,
-                                  const pkv_seqs *seqs, uint32_t *err_flags, pkv_stream_t stream);
+pkv_status pkv_quantize_kv_blocks(const pkv_cache *cache, const void *k_new, int64_t k_stride, const void *v_new,
+                                  int64_t v_stride, pkv_dtype src_dtype, int32_t num_tokens,
+                                  const int32_t *cu_new_lens, const pkv_seqs *seqs, uint32_t *err_flags,
+                                  pkv_stream_t stream);
 
 /*
  * Rotary positions.  A head's first rotary_dim dims are turned pair by pair by

@@ -309,9 +309,10 @@ pkv_status pkv_quantize_kv(const pkv_cache* cache, const void* k_new, const void
     return cuda_result(pkv::launch_quantize_kv(p, reinterpret_cast<cudaStream_t>(stream)), "quantize_kv launch");
 }
 
-pkv_status pkv_quantize_kv_blocks(const pkv_cache* cache, const void* k_new, const void* v_new, pkv_dtype src_dtype,
-                                  int32_t num_tokens, const int32_t* cu_new_lens, const pkv_seqs* seqs,
-                                  uint32_t* err_flags, pkv_stream_t stream) {
+pkv_status pkv_quantize_kv_blocks(const pkv_cache* cache, const void* k_new, int64_t k_stride, const void* v_new,
+                                  int64_t v_stride, pkv_dtype src_dtype, int32_t num_tokens,
+                                  const int32_t* cu_new_lens, const pkv_seqs* seqs, uint32_t* err_flags,
+                                  pkv_stream_t stream) {
     pkv_status st = check_cache(cache, false);
     if (st != PKV_OK) return st;
     if (!pkv::is_byte_cache(cache->kind))
@@ -322,10 +323,16 @@ pkv_status pkv_quantize_kv_blocks(const pkv_cache* cache, const void* k_new, con
     if (!cu_new_lens && int64_t(seqs->num_seqs) * seqs->q_len != num_tokens)
         return fail(PKV_ERR_INVALID_ARG, "without cu_new_lens num_tokens (%d) must be num_seqs * q_len (%lld)", num_tokens,
                     (long long)seqs->num_seqs * seqs->q_len);
+    const int64_t width = int64_t(cache->num_kv_heads) * cache->head_dim;
+    if (k_stride < width || k_stride % 8 != 0 || v_stride < width || v_stride % 8 != 0)
+        return fail(PKV_ERR_INVALID_ARG, "k_stride %lld, v_stride %lld: at least a row (%lld) and a multiple of 8",
+                    (long long)k_stride, (long long)v_stride, (long long)width);
     if (num_tokens == 0 || seqs->num_seqs == 0) return ok();
     CHECK_PTR(k_new, "k_new");
     CHECK_PTR(v_new, "v_new");
     pkv::BlockWriteParams p{};
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
     p.k_cache = cache->k;
     p.v_cache = cache->v;
     p.k_scale = static_cast<float*>(cache->k_scale);

@@ -326,6 +326,7 @@ PyObject* py_quantize_kv_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const SeqsArg s(call, a[3]);
         if (k.dim() != 3 || k.size(1) != c.c.num_kv_heads || k.size(2) != c.c.head_dim || v.sizes() != k.sizes())
             raise(PyExc_ValueError, "k_new / v_new must be [num_tokens, num_kv_heads, head_dim]");
+        const Rows rk = rows(call, a[1], "k_new", k.sizes(), k.scalar_type()), rv = rows(call, a[2], "v_new", k.sizes(), k.scalar_type());
         if (s.cl.t->numel() != s.s.num_seqs) raise(PyExc_ValueError, "context_lens must be [num_seqs]");
         const int32_t* cu = nullptr;
         if (a[4] != Py_None) {
@@ -334,11 +335,10 @@ PyObject* py_quantize_kv_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 raise(PyExc_ValueError, "cu_new_lens must be int32 [num_seqs + 1]");
             cu = static_cast<const int32_t*>(call.ptr(t));
         }
-        const void *kp = call.ptr(k), *vp = call.ptr(v);
         const int32_t tokens = fits(k.size(0), "num_tokens");
         uint32_t* err = call.err(a[5]);
         const pkv_stream_t stream = call.stream(a[6]);
-        return status_of([&] { return lib.quantize_kv_blocks(&c.c, kp, vp, dt, tokens, cu, &s.s, err, stream); });
+        return status_of([&] { return lib.quantize_kv_blocks(&c.c, rk.data, rk.stride, rv.data, rv.stride, dt, tokens, cu, &s.s, err, stream); });
     });
 }
 

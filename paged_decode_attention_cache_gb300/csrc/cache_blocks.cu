@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParam
     const int a = max(p0 - b * kBlock, 0), e = min(p1 - b * kBlock, kBlock);   // new rows [a, e) of the block
     const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
     const uint16_t* src = static_cast<const uint16_t*>(which ? p.v_new : p.k_new);
+    const int64_t stride = which ? p.v_stride : p.k_stride;
     const int r0 = lane / LPR, d0 = (lane % LPR) * 8;
 
     // ---- the new rows, which do not wait for the table entry
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParam
     for (int k = 0; k < NP; ++k) {
         const int r = k * RPP + r0;
         x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= a && r < e) x[k] = __ldg(reinterpret_cast<const uint4*>(src + ((src_row + r) * H + h) * D + d0));
+        if (r >= a && r < e) x[k] = __ldg(reinterpret_cast<const uint4*>(src + (src_row + r) * stride + h * D + d0));
     }
     if (pb < 0 || pb >= p.num_blocks) {
         if (h == 0 && which == 0 && lane == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);

@@ -224,8 +224,9 @@ struct BlockWriteParams {
     void* v_cache;
     float* k_scale;               // [num_blocks, num_kv_heads]
     float* v_scale;
-    const void* k_new;            // [num_tokens, num_kv_heads, head_dim], src_dtype
+    const void* k_new;            // rows of [num_kv_heads, head_dim], src_dtype, k_stride elements apart
     const void* v_new;
+    int64_t k_stride, v_stride;
     const int32_t* cu_new;        // [num_seqs + 1] rows of each sequence, or null: q_len rows each
     const int32_t* block_tables;
     const int32_t* context_lens;

@@ -101,7 +101,7 @@ def lib():
         L.pkv_quantize_kv.restype = st
         L.pkv_quantize_kv.argtypes = [_P, _P, _P, ctypes.c_int, _P, _I32, _P, _P]
         L.pkv_quantize_kv_blocks.restype = st
-        L.pkv_quantize_kv_blocks.argtypes = [_P, _P, _P, ctypes.c_int, _I32, _P, _P, _P, _P]
+        L.pkv_quantize_kv_blocks.argtypes = [_P, _P, _I64, _P, _I64, ctypes.c_int, _I32, _P, _P, _P, _P]
         L.pkv_rope_frequencies.restype = st
         L.pkv_rope_frequencies.argtypes = [_P, _I32, ctypes.c_double, _P]
         L.pkv_rope_and_cache.restype = st
@@ -293,7 +293,8 @@ def pkv_quantize_kv_blocks(cache: Cache, k_new: torch.Tensor, v_new: torch.Tenso
                            stream=None) -> None:
     """Append each sequence's new tokens (its last ones: rows cu_new_lens[s] ..
     cu_new_lens[s + 1] of k_new / v_new, or q_len rows each) to an "i8" or
-    "e4m3" cache; a block's scale grows when they need it."""
+    "e4m3" cache; a block's scale grows when they need it.  k_new and v_new may be
+    views of one packed projection (any row stride that is a multiple of 8)."""
     st = (_binding or _calls()).quantize_kv_blocks(cache, k_new, v_new, seqs, cu_new_lens, err_flags, stream)
     if st:
         _check(st)

@@ -23,8 +23,8 @@ def structs(kind=3, scales=(0x50000, 0x60000), q_len=1, num_seqs=4):
     return c, ops._Seqs(0x30000, 0x40000, num_seqs, 8, q_len, 0)
 
 
-def append(lib, c, s, dtype=1, tokens=4, cu=None, k=0x70000, v=0x80000):
-    return lib.pkv_quantize_kv_blocks(ctypes.byref(c), k, v, dtype, tokens, cu, ctypes.byref(s), None, None)
+def append(lib, c, s, dtype=1, tokens=4, cu=None, k=0x70000, v=0x80000, ks=1024, vs=1024):
+    return lib.pkv_quantize_kv_blocks(ctypes.byref(c), k, ks, v, vs, dtype, tokens, cu, ctypes.byref(s), None, None)
 
 
 def test_append_arguments_checked_on_the_host(lib):
@@ -42,6 +42,7 @@ def test_append_arguments_checked_on_the_host(lib):
     assert append(lib, c, s, tokens=-1) == bad
     assert append(lib, c, s, tokens=5) == bad and "q_len" in lib.pkv_last_error().decode()
     assert append(lib, c, s, tokens=2 ** 31 - 1, cu=0x90000) == bad
+    assert append(lib, c, s, ks=1016) == bad and append(lib, c, s, vs=1028) == bad and append(lib, c, s, ks=0) == bad
     assert append(lib, c, s, k=None) == bad and append(lib, c, s, v=0x80008) == bad
     assert append(lib, c, s, tokens=0, cu=0x90000) == ops.PKV_OK      # nothing to append: no launch
     c, s = structs(num_seqs=0)

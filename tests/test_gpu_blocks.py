@@ -169,6 +169,25 @@ def test_append_many_sequences():
     st.same()
 
 
+def test_append_rows_of_a_packed_projection():
+    # k and v as views of one [tokens, (heads + 2 kv heads) * head_dim] tensor: the same codes as from copies
+    rng = np.random.default_rng(9)
+    H, D, ctx = 2, 64, [5, 18, 1, 33]
+    tables, nb = tables_for(rng, ctx)
+    n = sum(ctx)
+    cu = np.concatenate([[0], np.cumsum(ctx)])
+    x = torch.from_numpy(rng.standard_normal((n, 7 * D))).to(torch.bfloat16).cuda()
+    k, v = x[:, 3 * D:5 * D].unflatten(1, (H, D)), x[:, 5 * D:].unflatten(1, (H, D))
+    st = State(rng, "i8", nb, H, D)
+    st.append((k, k.double().cpu().numpy()), (v, v.double().cpu().numpy()), tables, ctx, ctx, cu=cu)
+    st.same()
+    # one token: any stride
+    st = State(rng, "e4m3", nb, H, D)
+    one = (k[:1], k[:1].double().cpu().numpy())
+    st.append(one, one, tables[:1], [1], [1])
+    st.same()
+
+
 @pytest.mark.parametrize("kind", ["i8", "e4m3"])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_gather_dequant(kind, dt):
