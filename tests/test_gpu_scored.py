@@ -179,6 +179,28 @@ def test_many_sequences_of_all_kinds():
     run(rng, "bf16", "bf16", ctx, 4, 1, 64, 1, window=50, starts=starts, prefix=prefix, cap=20.0, slopes=slopes_of(4), loud=1.0)
 
 
+@pytest.mark.parametrize("D,ql", [(64, 1), (128, 1), (128, 4)])
+def test_nan_codes_of_masked_tokens_beside_visible_ones(D, ql):
+    """e4m3: a block holds masked and visible tokens; the masked ones' codes turn to NaN and nothing changes."""
+    rng = np.random.default_rng(41 + ql)
+    ctx, starts, prefix, H, Hkv = [100, 37, 64, 5, 333], [41, 36, 3, 2, 300], [5, 20, 1, 0, 17], 8, 2
+    hidden = masked_out(ctx, 0, starts, prefix)
+    cache, tables, _, _ = make(rng, "e4m3", ctx, Hkv, D, [np.zeros_like(h) for h in hidden], "bf16")
+    q, _ = rows(rng, len(ctx) * ql, H, D, "bf16", 0.5)
+    as_int = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    seqs = ops.Seqs(torch.from_numpy(tables).cuda(), as_int(ctx), ql, 0)
+    scores, ws = ops.Scores(30.0, None, as_int(starts), as_int(prefix)), ops.balanced_workspace(len(ctx), Hkv, D)
+    outs = [torch.full_like(q, float("nan")) for _ in range(2)]
+    ops.pkv_paged_attention_scored(outs[0], q, D ** -0.5, cache, seqs, scores, ws)
+    for t in (cache.k, cache.v):
+        codes = t.view(torch.uint8)
+        for s, h in enumerate(hidden):
+            for at in np.nonzero(h)[0]:
+                codes[int(tables[s, at // 16]), int(at % 16)] = 0x7f
+    ops.pkv_paged_attention_scored(outs[1], q, D ** -0.5, cache, seqs, scores, ws)
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+
+
 def test_without_scores_it_is_the_balanced_attention():
     rng = np.random.default_rng(23)
     for kind in ("bf16", "i8"):
