@@ -4,10 +4,10 @@
 // between the two products.  Compiled apart, like the other instantiations.
 //
 // Bound: HBM behind the start of the launch (plan, first copies) and the merges, about
-// 7 us that every balanced call has; a score costs up to a dozen instructions more than
-// a plain one, which the 16-bit caches hide.  Measured on one GB300: bf16, 88 MB of
-// capped scores in 19.6 us, 68 MB behind a window and a prefix in 17.1 us (4.0 TB/s);
-// int8, 88 MB with document starts in 29.2 us (3.0 TB/s), bound by the scores' instructions.
+// 7 us that every balanced call has (12 over the 8-bit caches); the cap's and the bias's
+// dozen instructions a score hide behind it.  Measured on one GB300: bf16, 88 MB of
+// capped scores in 19.5 us (19.1 without the cap), 68 MB behind a window and a prefix in
+// 17.0 us (4.0 TB/s); int8, 88 MB with document starts in 29.2 us (28.7 without cap and bias).
 #include "attention_byte.cuh"
 
 namespace pkv {
