@@ -95,13 +95,15 @@ __device__ __forceinline__ void flag_slots(const RopeParams& p, int64_t t0, int 
 // 16-byte chunks: the interleaved layout (a pair is a word), and the half layout where
 // rotary_dim % 16 == 0, so that a pair's elements lie at the same place of two chunks.
 // A thread moves two chunks of a row: the two that turn with one another (half), or
-// two side by side (interleaved, and dims that are kept).  D / 16 threads
+// one from each half of what is left (interleaved, and dims that are kept), so that the
+// threads of a row always read and write side by side.  D / 16 threads
 // are a row, so a CTA of 256 has 32 (D = 128) or 64 rows in its hands at once, and
 // loads four such sets before it stores the first.
 // The angles' table in shared memory keeps the four or two float4 (cos, sin, cos, sin)
 // of a chunk apart, so that the threads of a row read 16 bytes side by side.
-// 8192 tokens of 32 + 8 + 8 heads, bf16, D = 128: 33 us (6.0 TB/s, of 6.8 measured);
-// one warp per row with 2-byte accesses took 84.
+// 8192 tokens of 32 + 8 + 8 heads, bf16, D = 128: 32.4 us (6.1 TB/s, of 6.8 measured);
+// one warp per row with 2-byte accesses took 84.  Interleaved 35.9, and 37.7 where a thread
+// takes two chunks side by side, whose halves of a 32-byte sector two stores write.
 template <typename T, bool HALF, int D>
 __global__ void __launch_bounds__(kThreads) rope_chunks_kernel(RopeParams p) {
     constexpr int TPR = D / 16;                 // threads per row
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) rope_chunks_kernel(RopeParams p) {
     const int x = threadIdx.x % TPR, pairs = p.rotary_dim / 2;
     // this thread's two chunks, and which of them turn
     const int nrot = p.rotary_dim / 16;         // half: chunk pairs that turn
-    const int ca = HALF && x < nrot ? x : 2 * x, cb = HALF && x < nrot ? x + nrot : 2 * x + 1;
+    const int ca = HALF && x >= nrot ? nrot + x : x, cb = HALF && x < nrot ? x + nrot : TPR + x;
     const bool ta = HALF ? x < nrot : 8 * ca < p.rotary_dim, tb = HALF ? x < nrot : 8 * cb < p.rotary_dim;
 
     int tok = 0, row = threadIdx.x / TPR;       // the next row to load
