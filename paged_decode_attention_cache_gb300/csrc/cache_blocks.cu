@@ -232,59 +232,70 @@ __device__ __forceinline__ void expand16(uint4 c, float scale, uint4& lo, uint4&
     hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// CTA (b, s) expands logical block b of sequence s.  A thread takes 16 dims of one
-// (token, kv head), K and V: 16-byte loads, two 16-byte stores each; two such items are
-// loaded before the first is stored.  Bound by HBM, which writes two bytes for each it
-// reads: 5.6 TB/s at 375 MB, 4.9 at 149 MB (8-byte loads, one item at a time: 3.3).
+// A CTA expands kGatherItems items of logical block b of sequence s, an item being 16 dims
+// of one (token, kv head), K and V: 16-byte loads, and 32-byte stores where the outputs are
+// aligned for them (two 16-byte stores leave every 32-byte sector to two instructions).
+// Bound by HBM, which writes two bytes for each it reads: 375 MB at 6.5 TB/s (of
+// 6.8 measured for a copy), 149 MB at 6.0, 73 MB at 5.4 (13.4 us).  Measured on the way at
+// 73 MB: 17.1 us with a CTA of 256 threads per block and 16-byte stores, 15.8 with halves of
+// blocks, 14.7 with 32-byte stores too, 14.0 with one item per thread at a time and quarters
+// of 8 heads of 128 dims (256 items), 15.3 with eighths.
+constexpr int kGatherThreads = 128, kGatherItems = 256;
+
+__device__ __forceinline__ void store32(uint4* at, uint4 lo, uint4 hi) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(lo.x), "r"(lo.y), "r"(lo.z),
+                 "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                 : "memory");
+}
+
 template <typename OutT, bool E4M3, int D>
-__global__ void __launch_bounds__(kThreads) gather_blocks_kernel(GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) gather_blocks_kernel(GatherParams p) {
     grid_dep_wait();
     grid_dep_launch();
-    constexpr int CPT = D / 16, U = 2;
-    const int s = blockIdx.y, b = blockIdx.x;
+    constexpr int CPT = D / 16;
+    const int H = p.num_kv_heads, parts = (kBlock * H * CPT + kGatherItems - 1) / kGatherItems;
+    const int s = blockIdx.y, b = blockIdx.x / parts, part = blockIdx.x - b * parts;
     int ctx = p.context_lens[s];
     const int64_t row0 = p.cu_seq_lens[s];
     const int pb = p.block_tables[int64_t(s) * p.max_blocks + b];
     const int cap = p.max_blocks * kBlock;
     if (ctx > cap) {
-        if (b == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
         ctx = cap;
     }
     const int t0 = b * kBlock;
     if (t0 >= ctx) return;
     const int ntok = min(kBlock, ctx - t0);
     if (pb < 0 || pb >= p.num_blocks) {
-        if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
+        if (part == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
         return;
     }
-    const int H = p.num_kv_heads;
     const int64_t src0 = int64_t(pb) * kBlock * H * D, dst0 = (row0 + t0) * H * D;
-    const int n = ntok * H * CPT;   // the block's first ntok token rows are contiguous on both sides
-    for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
-        uint4 c[U][2];
-        float sc[U][2];
+    const uint4* src[2] = {reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + src0),
+                           reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_cache) + src0)};
+    const float* scale[2] = {static_cast<const float*>(p.k_scale) + int64_t(pb) * H, static_cast<const float*>(p.v_scale) + int64_t(pb) * H};
+    uint4* dst[2] = {reinterpret_cast<uint4*>(static_cast<OutT*>(p.k_out) + dst0), reinterpret_cast<uint4*>(static_cast<OutT*>(p.v_out) + dst0)};
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.k_out) | reinterpret_cast<uintptr_t>(p.v_out)) & 31u) == 0;
+    // the block's first ntok token rows are contiguous on both sides
+    const int i1 = min(ntok * H * CPT, (part + 1) * kGatherItems);
+    for (int i = part * kGatherItems + threadIdx.x; i < i1; i += kGatherThreads) {
+        uint4 c[2];
+        float sc[2];
+        const int h = (i / CPT) % H;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kThreads;
-            if (i >= n) break;
-            const int64_t meta = int64_t(pb) * H + (i / CPT) % H;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                c[u][w] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w ? p.v_cache : p.k_cache) + src0) + i);
-                sc[u][w] = __ldg(static_cast<const float*>(w ? p.v_scale : p.k_scale) + meta);
-            }
+        for (int w = 0; w < 2; ++w) {
+            c[w] = __ldcs(src[w] + i);
+            sc[w] = __ldg(scale[w] + h);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kThreads;
-            if (i >= n) break;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                uint4* out = reinterpret_cast<uint4*>(static_cast<OutT*>(w ? p.v_out : p.k_out) + dst0);
-                uint4 lo, hi;
-                expand16<OutT, E4M3>(c[u][w], sc[u][w], lo, hi);
-                out[2 * i] = lo;
-                out[2 * i + 1] = hi;
+        for (int w = 0; w < 2; ++w) {
+            uint4 lo, hi;
+            expand16<OutT, E4M3>(c[w], sc[w], lo, hi);
+            if (wide) {
+                store32(dst[w] + 2 * i, lo, hi);
+            } else {
+                dst[w][2 * i] = lo;
+                dst[w][2 * i + 1] = hi;
             }
         }
     }
@@ -298,8 +309,8 @@ cudaError_t append_d(const BlockWriteParams& p, dim3 grid, cudaStream_t st) {
 
 template <typename OutT, bool E4M3>
 cudaError_t gather_d(const GatherParams& p, dim3 grid, cudaStream_t st) {
-    return p.head_dim == 128 ? launch_kernel(gather_blocks_kernel<OutT, E4M3, 128>, grid, dim3(kThreads), 0, st, p)
-                             : launch_kernel(gather_blocks_kernel<OutT, E4M3, 64>, grid, dim3(kThreads), 0, st, p);
+    return p.head_dim == 128 ? launch_kernel(gather_blocks_kernel<OutT, E4M3, 128>, grid, dim3(kGatherThreads), 0, st, p)
+                             : launch_kernel(gather_blocks_kernel<OutT, E4M3, 64>, grid, dim3(kGatherThreads), 0, st, p);
 }
 
 }  // namespace
@@ -318,7 +329,9 @@ cudaError_t launch_append_blocks(BlockWriteParams p, cudaStream_t stream) {
 }
 
 cudaError_t launch_gather_blocks(const GatherParams& p, int cache_kind, cudaStream_t stream) {
-    const dim3 grid(p.max_blocks, p.num_seqs);
+    const int64_t parts = (int64_t(p.num_kv_heads) * p.head_dim + kGatherItems - 1) / kGatherItems;
+    if (p.max_blocks * parts > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid(unsigned(p.max_blocks * parts), p.num_seqs);
     const bool e4 = cache_kind == PKV_CACHE_E4M3;
     if (p.out_dtype == PKV_BF16)
         return e4 ? gather_d<__nv_bfloat16, true>(p, grid, stream) : gather_d<__nv_bfloat16, false>(p, grid, stream);

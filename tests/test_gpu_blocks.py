@@ -209,6 +209,27 @@ def test_gather_dequant(kind, dt):
         assert torch.equal(g.out.cpu(), torch.from_numpy(want).float().to(SRC[dt]))
 
 
+@pytest.mark.parametrize("H,D", [(1, 64), (3, 64), (8, 64), (17, 128), (40, 128)])
+@pytest.mark.parametrize("offset", [0, 8])
+def test_gather_dequant_rows_of_all_widths_and_alignments(H, D, offset):
+    """Blocks of a part, of one and of several CTAs; outputs on a 32-byte boundary and 16 bytes off it."""
+    rng = np.random.default_rng(9)
+    ctx = [33, 16, 5]
+    tables, nb = tables_for(rng, ctx)
+    st = State(rng, "i8", nb, H, D)
+    n = sum(ctx)
+    cu = np.concatenate([[0], np.cumsum(ctx)])
+    seqs = st.append(rows(rng, n, H, D, "bf16", 1.0), rows(rng, n, H, D, "bf16", 1.0), tables, ctx, ctx, cu=cu)
+    held = [torch.full((n * H * D + 64,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    k, v = (x[offset:offset + n * H * D].view(n, H, D) for x in held)
+    ops.pkv_gather_kv_cache_dequant(k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), st.cache, seqs, st.err)
+    assert int(st.err.item()) == 0
+    for got, whole, codes, scale in ((k, held[0], st.kc, st.ks), (v, held[1], st.vc, st.vs)):
+        want = np.concatenate([R.stored(codes, scale, tables, s, c) for s, c in enumerate(ctx)])
+        assert torch.equal(got.cpu(), torch.from_numpy(want).float().to(torch.bfloat16))
+        assert (whole[:offset] == 7.0).all() and (whole[offset + n * H * D:] == 7.0).all()
+
+
 # ---------------------------------------------------------------- attention
 
 CTX = [1, 15, 16, 17, 40, 100, 301, 0, 64]
