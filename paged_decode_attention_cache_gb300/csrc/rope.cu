@@ -24,7 +24,9 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a CTA: half layout 256 (8192 tokens of 32 + 8 heads of 128 dims 32.5 us, with 128 32.7; 512 tokens 3.1
+// and 4.0), interleaved 128 (34.0, with 256 35.9), half with chunks that do not match 128 (43.4, with 256 68).
+constexpr int kHalfThreads = 256, kPairThreads = 128, kAnyThreads = 128;
 constexpr int kMaxTokens = 4;    // tokens of a CTA
 
 template <typename T>
@@ -97,17 +99,18 @@ __device__ __forceinline__ void flag_slots(const RopeParams& p, int64_t t0, int 
 // A thread moves two chunks of a row: the two that turn with one another (half), or
 // one from each half of what is left (interleaved, and dims that are kept), so that the
 // threads of a row always read and write side by side.  D / 16 threads
-// are a row, so a CTA of 256 has 32 (D = 128) or 64 rows in its hands at once, and
+// are a row, so a CTA of 256 has 32 (D = 128) or 64 rows in its hands at once (of 128, half), and
 // loads four such sets before it stores the first.
 // The angles' table in shared memory keeps the four or two float4 (cos, sin, cos, sin)
 // of a chunk apart, so that the threads of a row read 16 bytes side by side.
 // 8192 tokens of 32 + 8 + 8 heads, bf16, D = 128: 32.4 us (6.1 TB/s, of 6.8 measured);
-// one warp per row with 2-byte accesses took 84.  Interleaved 35.9, and 37.7 where a thread
-// takes two chunks side by side, whose halves of a 32-byte sector two stores write.
+// one warp per row with 2-byte accesses took 84.  Interleaved 34.0; 37.7 with 256 threads and
+// two chunks side by side to a thread, whose halves of a 32-byte sector two stores write.
 template <typename T, bool HALF, int D>
-__global__ void __launch_bounds__(kThreads) rope_chunks_kernel(RopeParams p) {
+__global__ void __launch_bounds__(HALF ? kHalfThreads : kPairThreads) rope_chunks_kernel(RopeParams p) {
+    constexpr int kT = HALF ? kHalfThreads : kPairThreads;
     constexpr int TPR = D / 16;                 // threads per row
-    constexpr int RPB = kThreads / TPR;         // rows of a CTA at once
+    constexpr int RPB = kT / TPR;               // rows of a CTA at once
     constexpr int Q4 = HALF ? 4 : 2;            // float4s of a chunk's angles
     constexpr int U = 4;                        // rows a thread loads ahead
     __shared__ float4 cs[kMaxTokens][Q4][HALF ? 8 : 16];
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) rope_chunks_kernel(RopeParams p) {
         if (!ready) {
             // the first rows are on their way; the angles meanwhile
             flag_slots(p, t0, ntok);
-            for (int y = threadIdx.x; y < ntok * pairs; y += kThreads) {
+            for (int y = threadIdx.x; y < ntok * pairs; y += kT) {
                 const int at = y / pairs, i = y - at * pairs;
                 const int c = i / (2 * Q4), j = (i / 2) % Q4;
                 reinterpret_cast<float2*>(&cs[at][j][c])[i & 1] = angle(p, t0 + at, i);
@@ -217,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) rope_chunks_kernel(RopeParams p) {
 // through shared memory, where a thread finds its elements' partners (a row lies in one
 // warp).  One warp per row, or a thread per pair, spend more on addresses than on this.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_any_kernel(RopeParams p) {
-    constexpr int TPR = D / 16, RPB = kThreads / TPR, U = 4;
+__global__ void __launch_bounds__(kAnyThreads, 6) rope_any_kernel(RopeParams p) {
+    constexpr int TPR = D / 16, RPB = kAnyThreads / TPR, U = 4;
     __shared__ float2 cs[kMaxTokens * 64];
     __shared__ uint4 held[RPB][D / 8 + 1];      // a row set's chunks (rows of a warp in different banks)
     grid_dep_wait();
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(RopeParams p) {
     const int rows = p.num_heads + (p.slot_mapping ? 2 : 1) * p.num_kv_heads, turned = p.num_heads + p.num_kv_heads;
     const int x = threadIdx.x % TPR, mine = threadIdx.x / TPR, pairs = p.rotary_dim / 2, ca = 2 * x;
     flag_slots(p, t0, ntok);
-    for (int y = threadIdx.x; y < ntok * pairs; y += kThreads) cs[y] = angle(p, t0 + y / pairs, y % pairs);
+    for (int y = threadIdx.x; y < ntok * pairs; y += kAnyThreads) cs[y] = angle(p, t0 + y / pairs, y % pairs);
     __syncthreads();
     int tok = 0, row = mine;
     auto settle = [&]() {
@@ -300,9 +303,9 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(RopeParams p) {
 template <typename T, int D>
 cudaError_t launch_layout(const RopeParams& p, dim3 grid, cudaStream_t st) {
     const bool half = p.layout == PKV_ROPE_HALF;
-    if (half && p.rotary_dim % 16 != 0) return launch_kernel(rope_any_kernel<T, D>, grid, dim3(kThreads), 0, st, p);
-    return half ? launch_kernel(rope_chunks_kernel<T, true, D>, grid, dim3(kThreads), 0, st, p)
-                : launch_kernel(rope_chunks_kernel<T, false, D>, grid, dim3(kThreads), 0, st, p);
+    if (half && p.rotary_dim % 16 != 0) return launch_kernel(rope_any_kernel<T, D>, grid, dim3(kAnyThreads), 0, st, p);
+    return half ? launch_kernel(rope_chunks_kernel<T, true, D>, grid, dim3(kHalfThreads), 0, st, p)
+                : launch_kernel(rope_chunks_kernel<T, false, D>, grid, dim3(kPairThreads), 0, st, p);
 }
 
 }  // namespace
