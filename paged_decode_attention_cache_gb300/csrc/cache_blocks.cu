@@ -16,8 +16,8 @@
 // to one part in five of int8's range (a tenth on average).
 //
 // Bound: HBM for prompts (4 bytes read and 2 written per element of K + V: 83 MB in
-// 16.0 us, 5.2 TB/s), dependent-load latency for a decode step (length -> table ->
-// scale; 64 tokens of 8 heads in 2.5 us).
+// 16.2 us, 5.1 TB/s), dependent-load latency for a decode step (length -> table ->
+// scale; 64 tokens of 8 heads in 2.4 us).
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -30,7 +30,7 @@ namespace pkv {
 namespace {
 
 constexpr int kBlock = 16;
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;   // append: 83 MB in 17.2, 16.4, 16.2 us with 256, 128, 64
 
 // The largest magnitude of two 16-bit floats in each half of a and b (packed).
 template <typename Src>
@@ -103,7 +103,7 @@ __device__ __forceinline__ UnitSeq find_seq(const BlockWriteParams& p, int u, in
 }
 
 template <typename Src, bool E4M3, int D>
-__global__ void __launch_bounds__(kThreads) append_blocks_kernel(BlockWriteParams p) {
+__global__ void __launch_bounds__(kThreads, 1) append_blocks_kernel(BlockWriteParams p) {
     grid_dep_wait();
     grid_dep_launch();
     constexpr int LPR = D / 8;           // lanes per row, 8 values each
