@@ -415,8 +415,10 @@ struct TeMath {
                 }
             }
         }
-        // scale / vref is exact but for a subnormal product: 1 / vref is a power of two
-        const float per_ref = __uint_as_float((254u << 23) - __float_as_uint(vref)) * kPUnit;
+        // (scale / vref) * 2^14, in this order: vref is 2^-126 .. 2^126, so 1 / vref is a normal power of two and the quotient
+        // exact and at most 1 (for scales up to 2^126); it is 0 for a scale of 0, a block of zeros, also while vref is still
+        // 2^-126, where 2^14 / vref would be infinite
+        const float inv_ref = __uint_as_float((254u << 23) - __float_as_uint(vref));
         auto weigh = [&](uint8_t* tile, float vscale, int pos, int n, const float (&sb)[NT][4]) {
             if (E4M3 && (n < kBS || (VAR == kScored && pos < lo_))) {
                 // rows past the context (scored: or masked for all) may hold NaN codes, which weight 0 would not stop:
@@ -433,7 +435,7 @@ struct TeMath {
             }
             // -------------------------------------------- P^T operand (tokens 2t.., query column g)
             uint32_t ph[NT][2], pl[NT][2];
-            const float ratio = vscale * per_ref;
+            const float ratio = (vscale * inv_ref) * kPUnit;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -471,7 +473,8 @@ struct TeMath {
     }
 
     __device__ __forceinline__ void finish(int) {
-        const float unit = vref * (1.f / kPUnit);   // 0 if vref never grew: then every scale was 0, or no block came
+        // subnormal (2^-140) if vref never grew: the sums it multiplies are then those of scales up to 2^-126, or zeros
+        const float unit = vref * (1.f / kPUnit);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
