@@ -91,14 +91,20 @@ struct TensorAttr {
 // What the calls of one kind have in common: the device they run on and its stream.
 // check: every tensor has to live on it.
 struct Call {
-    int device;
     bool check;
-    explicit Call(bool check_device) : device(c10::cuda::current_device()), check(check_device) {}
+    mutable int current = -1;
+    explicit Call(bool check_device) : check(check_device) {}
+
+    // asked for when a CUDA tensor is there: without a GPU torch has no current device to name
+    int device() const {
+        if (current < 0) current = c10::cuda::current_device();
+        return current;
+    }
 
     void where(const at::Tensor& t) const {
         if (!t.is_cuda()) raise(PyExc_ValueError, "pkv tensors must live on a CUDA device");
-        if (check && t.get_device() != device)
-            raise(PyExc_ValueError, "pkv tensors must live on the current CUDA device (%d), not cuda:%d", device,
+        if (check && t.get_device() != device())
+            raise(PyExc_ValueError, "pkv tensors must live on the current CUDA device (%d), not cuda:%d", device(),
                   int(t.get_device()));
     }
     void* ptr(const at::Tensor& t) const {
@@ -116,7 +122,7 @@ struct Call {
     }
     pkv_stream_t stream(PyObject* o) const {
         if (o == Py_None)
-            return reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(device)).stream());
+            return reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(device())).stream());
         Ref a(PyObject_GetAttr(o, names.cuda_stream));
         void* s = PyLong_AsVoidPtr(a.o);
         if (!s && PyErr_Occurred()) throw Raised{};
