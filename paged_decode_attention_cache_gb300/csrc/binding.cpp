@@ -88,12 +88,9 @@ struct TensorAttr {
         : ref(PyObject_GetAttr(obj, name)), t(ref.o == Py_None ? nullptr : &tensor(ref.o, text)) {}
 };
 
-// What the calls of one kind have in common: the device they run on and its stream.
-// check: every tensor has to live on it.
+// What the calls have in common: the device they run on, which every tensor has to live on, and its stream.
 struct Call {
-    bool check;
     mutable int current = -1;
-    explicit Call(bool check_device) : check(check_device) {}
 
     // asked for when a CUDA tensor is there: without a GPU torch has no current device to name
     int device() const {
@@ -103,7 +100,7 @@ struct Call {
 
     void where(const at::Tensor& t) const {
         if (!t.is_cuda()) raise(PyExc_ValueError, "pkv tensors must live on a CUDA device");
-        if (check && t.get_device() != device())
+        if (t.get_device() != device())
             raise(PyExc_ValueError, "pkv tensors must live on the current CUDA device (%d), not cuda:%d", device(),
                   int(t.get_device()));
     }
@@ -144,10 +141,12 @@ pkv_dtype any_type(const at::Tensor& t, const char* name) {
     return d;
 }
 
+// A cache's kind and sizes; its addresses after place().  The sizes are checked first, so that what they
+// refuse is refused before any tensor's device matters.
 struct CacheArg {
     TensorAttr k, v, ks, vs, vz;
     pkv_cache c;
-    CacheArg(const Call& call, PyObject* o)
+    explicit CacheArg(PyObject* o)
         : k(o, names.k, "cache.k"), v(o, names.v, "cache.v"), ks(o, names.k_scale, "cache.k_scale"),
           vs(o, names.v_scale, "cache.v_scale"), vz(o, names.v_zero, "cache.v_zero") {
         Ref kind(PyObject_GetAttr(o, names.kind));
@@ -171,23 +170,49 @@ struct CacheArg {
             };
             if (v.t->sizes() != z || !scales(ks) || !scales(vs))
                 raise(PyExc_ValueError, "a %s cache has k and v of one shape and float32 scales [num_blocks, num_kv_heads]", s);
+        } else {
+            // the bytes that k's shape implies, whatever type the tensors call them
+            const int64_t rows = z[0] * z[1] * z[2];
+            auto holds = [&](const TensorAttr& a, int64_t bytes, const char* name) {
+                if (!a.t || int64_t(a.t->nbytes()) < bytes)
+                    raise(PyExc_ValueError, "a %s cache's %s is smaller than k's shape asks for", s, name);
+            };
+            const bool packed = id == PKV_CACHE_K8V4;
+            holds(k, rows * z[3] * (packed ? 1 : 2), "k");
+            holds(v, packed ? rows * z[3] / 2 : rows * z[3] * 2, "v");
+            if (packed) {
+                holds(ks, rows * 2, "k_scale");
+                holds(vs, rows * (z[3] / 32) * 2, "v_scale");
+                holds(vz, rows * (z[3] / 32) * 2, "v_zero");
+            }
         }
         c = pkv_cache{id, fits(z[0], "num_blocks"), fits(z[1], "block_size"), fits(z[2], "num_kv_heads"),
-                      fits(z[3], "head_dim"), fits(as_long(o, names.v_group), "v_group"), call.ptr(k), call.ptr(v),
-                      call.ptr(ks), call.ptr(vs), call.ptr(vz)};
+                      fits(z[3], "head_dim"), fits(as_long(o, names.v_group), "v_group"), nullptr, nullptr, nullptr, nullptr, nullptr};
+    }
+    void place(const Call& call) {
+        c.k = call.ptr(k);
+        c.v = call.ptr(v);
+        c.k_scale = call.ptr(ks);
+        c.v_scale = call.ptr(vs);
+        c.v_zero = call.ptr(vz);
     }
 };
 
+// A batch's sizes; its addresses after place().
 struct SeqsArg {
     TensorAttr bt, cl;
     pkv_seqs s;
-    SeqsArg(const Call& call, PyObject* o) : bt(o, names.block_tables, "block_tables"), cl(o, names.context_lens, "context_lens") {
+    explicit SeqsArg(PyObject* o) : bt(o, names.block_tables, "block_tables"), cl(o, names.context_lens, "context_lens") {
         if (!bt.t || !cl.t || bt.t->scalar_type() != at::kInt || cl.t->scalar_type() != at::kInt)
             raise(PyExc_ValueError, "block_tables and context_lens must be int32");
         if (bt.t->dim() != 2) raise(PyExc_ValueError, "block_tables must be [num_seqs, max_blocks]");
-        s = pkv_seqs{static_cast<const int32_t*>(call.ptr(bt)), static_cast<const int32_t*>(call.ptr(cl)),
-                     fits(bt.t->size(0), "num_seqs"), fits(bt.t->size(1), "max_blocks"),
+        s = pkv_seqs{nullptr, nullptr, fits(bt.t->size(0), "num_seqs"), fits(bt.t->size(1), "max_blocks"),
                      fits(as_long(o, names.q_len), "q_len"), fits(as_long(o, names.sliding_window), "sliding_window")};
+        if (cl.t->numel() < s.num_seqs) raise(PyExc_ValueError, "context_lens must be [num_seqs]");
+    }
+    void place(const Call& call) {
+        s.block_tables = static_cast<const int32_t*>(call.ptr(bt));
+        s.context_lens = static_cast<const int32_t*>(call.ptr(cl));
     }
 };
 
@@ -272,7 +297,7 @@ PyObject* py_load(PyObject*, PyObject* arg) {
 // (q_out, q, k, v, rope, positions, cache, slot_mapping, k_out, err_flags, stream)
 PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 11, [&] {
-        const Call call(true);
+        const Call call;
         const at::Tensor& q = tensor(a[1], "q");
         pkv_dtype dt;
         if (!half_type(q, &dt)) raise(PyExc_ValueError, "q must be float16 or bfloat16");
@@ -294,8 +319,9 @@ PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (a[3] == Py_None || a[7] == Py_None) raise(PyExc_ValueError, "a cache write needs v and slot_mapping");
             const at::Tensor& s = tensor(a[7], "slot_mapping");
             if (s.scalar_type() != at::kLong || s.numel() != T) raise(PyExc_ValueError, "slot_mapping must be int64 [num_tokens]");
+            cache.emplace(a[6]);
+            cache->place(call);
             slots = static_cast<const int64_t*>(call.ptr(s));
-            cache.emplace(call, a[6]);
             rv = rows(call, a[3], "v", kz, ty);
         }
         TensorAttr freq(a[4], names.freq, "freq");
@@ -323,15 +349,17 @@ PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (cache, k_new, v_new, seqs, cu_new_lens, err_flags, stream)
 PyObject* py_quantize_kv_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 7, [&] {
-        const Call call(true);
+        const Call call;
         const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new");
         pkv_dtype dt;
         if (!half_type(k, &dt) || v.scalar_type() != k.scalar_type())
             raise(PyExc_ValueError, "k_new / v_new must both be float16 or both bfloat16");
-        const CacheArg c(call, a[0]);
-        const SeqsArg s(call, a[3]);
+        CacheArg c(a[0]);
+        SeqsArg s(a[3]);
         if (k.dim() != 3 || k.size(1) != c.c.num_kv_heads || k.size(2) != c.c.head_dim || v.sizes() != k.sizes())
             raise(PyExc_ValueError, "k_new / v_new must be [num_tokens, num_kv_heads, head_dim]");
+        c.place(call);
+        s.place(call);
         const Rows rk = rows(call, a[1], "k_new", k.sizes(), k.scalar_type()), rv = rows(call, a[2], "v_new", k.sizes(), k.scalar_type());
         if (s.cl.t->numel() != s.s.num_seqs) raise(PyExc_ValueError, "context_lens must be [num_seqs]");
         const int32_t* cu = nullptr;
@@ -351,9 +379,9 @@ PyObject* py_quantize_kv_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (out, q, scale, cache, seqs, scores, workspace, err_flags, stream)
 PyObject* py_paged_attention_scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 9, [&] {
-        const Call call(true);
-        const CacheArg c(call, a[3]);
-        const SeqsArg s(call, a[4]);
+        const Call call;
+        CacheArg c(a[3]);
+        SeqsArg s(a[4]);
         const at::Tensor &out = tensor(a[0], "out"), &q = tensor(a[1], "q"), &ws = tensor(a[6], "workspace");
         if (q.dim() != 3 || q.size(0) != int64_t(s.s.num_seqs) * s.s.q_len || q.size(2) != c.c.head_dim ||
             out.sizes() != q.sizes() || s.cl.t->numel() != s.s.num_seqs)
@@ -369,6 +397,8 @@ PyObject* py_paged_attention_scored(PyObject*, PyObject* const* a, Py_ssize_t n)
         for (const TensorAttr* t : {&starts, &prefix})
             if (t->t && (t->t->scalar_type() != at::kInt || t->t->numel() != s.s.num_seqs))
                 raise(PyExc_ValueError, "%s must be int32 [%d]", t == &starts ? "doc_starts" : "prefix_lens", int(s.s.num_seqs));
+        c.place(call);
+        s.place(call);
         Ref cap(PyObject_GetAttr(a[5], names.softcap));
         const pkv_scores sc{float(as_double(cap.o)), static_cast<const float*>(call.ptr(slopes)),
                             static_cast<const int32_t*>(call.ptr(starts)), static_cast<const int32_t*>(call.ptr(prefix))};
@@ -387,12 +417,18 @@ PyObject* py_paged_attention_scored(PyObject*, PyObject* const* a, Py_ssize_t n)
 // (out, q, scale, cache, seqs, workspace, err_flags, stream)
 PyObject* py_paged_attention_balanced(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 8, [&] {
-        const Call call(false);
-        const CacheArg c(call, a[3]);
-        const SeqsArg s(call, a[4]);
+        const Call call;
+        CacheArg c(a[3]);
+        SeqsArg s(a[4]);
         const at::Tensor &out = tensor(a[0], "out"), &q = tensor(a[1], "q"), &ws = tensor(a[5], "workspace");
         if (q.dim() < 2) raise(PyExc_ValueError, "q must be [num_seqs * q_len, num_heads, head_dim]");
+        // buffers of a larger batch are taken (their first rows), smaller ones are not
+        const int64_t needed = int64_t(s.s.num_seqs) * s.s.q_len * q.size(1) * c.c.head_dim;
+        if (q.numel() < needed || out.numel() < needed)
+            raise(PyExc_ValueError, "q and out must be [num_seqs * q_len, num_heads, head_dim]");
         const pkv_dtype ot = any_type(out, "out"), qt = any_type(q, "q");
+        c.place(call);
+        s.place(call);
         const float scale = float(as_double(a[2]));
         void *op = call.ptr(out), *wp = call.ptr(ws);
         const void* qp = call.ptr(q);
@@ -407,14 +443,19 @@ PyObject* py_paged_attention_balanced(PyObject*, PyObject* const* a, Py_ssize_t 
 // (k_out, v_out, cu_seq_lens, cache, seqs, err_flags, stream)
 PyObject* py_gather_kv_cache_dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 7, [&] {
-        const Call call(false);
+        const Call call;
         const at::Tensor &k = tensor(a[0], "k_out"), &v = tensor(a[1], "v_out"), &cu = tensor(a[2], "cu_seq_lens");
         if (cu.scalar_type() != at::kInt) raise(PyExc_ValueError, "cu_seq_lens must be int32");
         pkv_dtype dt;
         if (!half_type(k, &dt) || v.scalar_type() != k.scalar_type())
             raise(PyExc_ValueError, "k_out / v_out must both be float16 or both bfloat16");
-        const CacheArg c(call, a[3]);
-        const SeqsArg s(call, a[4]);
+        CacheArg c(a[3]);
+        SeqsArg s(a[4]);
+        if (k.sizes() != v.sizes() || (c.c.head_dim > 0 && c.c.num_kv_heads > 0 && k.numel() % (int64_t(c.c.num_kv_heads) * c.c.head_dim) != 0))
+            raise(PyExc_ValueError, "k_out and v_out must both be [cu_seq_lens[num_seqs], num_kv_heads, head_dim]");
+        if (cu.numel() < int64_t(s.s.num_seqs) + 1) raise(PyExc_ValueError, "cu_seq_lens must be int32 [num_seqs + 1]");
+        c.place(call);
+        s.place(call);
         void *kp = call.ptr(k), *vp = call.ptr(v);
         const int32_t* cp = static_cast<const int32_t*>(call.ptr(cu));
         uint32_t* err = call.err(a[5]);
