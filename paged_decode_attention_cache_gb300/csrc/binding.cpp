@@ -57,9 +57,10 @@ struct Ref {
     Ref& operator=(const Ref&) = delete;
 };
 
+// An attribute as an integer, from whatever int() takes.
 long as_long(PyObject* obj, PyObject* name) {
-    Ref a(PyObject_GetAttr(obj, name));
-    const long v = PyLong_AsLong(a.o);
+    Ref a(PyObject_GetAttr(obj, name)), whole(PyNumber_Long(a.o));
+    const long v = PyLong_AsLong(whole.o);
     if (v == -1 && PyErr_Occurred()) throw Raised{};
     return v;
 }

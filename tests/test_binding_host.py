@@ -78,3 +78,15 @@ def test_a_cache_whose_tensors_disagree_is_refused():
         setattr(c, name, getattr(c, name)[:3])
         refused(name + " is smaller", lambda: call(c))
     refused("v_zero is smaller", lambda: call(ops.Cache("k8v4", packed.k, packed.v, packed.k_scale, packed.v_scale)))
+
+
+def test_lengths_are_whatever_int_takes():
+    # a q_len or a window that comes out of a division or a tensor, as the other calls take them
+    q, k, ws = zeros(B, H, D), zeros(B, HKV, D), torch.zeros(1 << 20, dtype=torch.uint8)
+    for one, window in ((1.0, 32.0), (torch.tensor(1), torch.tensor(32.0)), (True, 32)):
+        s = ops.Seqs(torch.zeros((B, 1), dtype=torch.int32), torch.ones(B, dtype=torch.int32), one, window)
+        refused("CUDA device", lambda: ops.pkv_paged_attention_balanced(q.clone(), q, 0.125, cache(), s, ws))
+        refused("CUDA device", lambda: ops.pkv_gather_kv_cache_dequant(k, k.clone(), torch.zeros(B + 1, dtype=torch.int32), cache(), s))
+    s = ops.Seqs(torch.zeros((B, 1), dtype=torch.int32), torch.ones(B, dtype=torch.int32), None)
+    with pytest.raises(TypeError):
+        ops.pkv_paged_attention_balanced(q.clone(), q, 0.125, cache(), s, ws)
