@@ -1053,13 +1053,9 @@ int byte_smem_bytes(int stages, int M, int mode) {
 
 template <class Math, int VAR>
 cudaError_t launch_byte(AttnParams p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
-    static int num_sms = 0;
-    if (num_sms == 0) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-    }
+    int num_sms = 0;
+    const cudaError_t e = prepare_device<byte_attention_kernel<Math, VAR>>(&num_sms);
+    if (e != cudaSuccess) return e;
     const int M = (p.num_heads / p.num_kv_heads) * p.q_len;
     const int per_stage = byte_smem_bytes<Math, VAR>(1, M, p.mode) - byte_smem_bytes<Math, VAR>(0, M, p.mode);
     int stages = (kSmemLimit - byte_smem_bytes<Math, VAR>(0, M, p.mode)) / per_stage;
@@ -1070,13 +1066,6 @@ cudaError_t launch_byte(AttnParams p, const CUtensorMap& km, const CUtensorMap& 
     if (p.mode == kModeBalanced) {
         p.seg_cost = Math::kSegCost;
         p.min_chunk = kStepUnits * Math::NCW;   // one step for every warp: more CTAs would only add pieces
-    }
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(byte_attention_kernel<Math, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemLimit);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
     }
     const int cap = num_sms < kMaxGrid ? num_sms : kMaxGrid;
     int grid;

@@ -54,6 +54,7 @@
 #pragma once
 
 #include "pkv_device.cuh"
+#include "per_device.h"
 #include "pkv_quant.cuh"
 #include "pkv_internal.h"
 
@@ -2185,15 +2186,27 @@ int smem_bytes(int stages, int M, int QL, int D) {
            (FUSED && !checks_fit(M, QL, D) ? NCW * kCheckBytes : 0) + NCW * M * D * 4 + NCW * Math::SCRATCH + 1024 + 64;
 }
 
+// The current device's SMs, and its permission for `kernel` to take kSmemLimit of shared memory: once per kernel
+// and device (the attribute holds for the device that is current).
+using AttentionKernel = void (*)(CUtensorMap, CUtensorMap, AttnParams);
+template <AttentionKernel kernel>
+cudaError_t prepare_device(int* num_sms) {
+    static PerDevice sms;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return cudaError_t(sms.get(dev, num_sms, [dev](int* n) {
+        cudaError_t r = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        return int(r);
+    }));
+}
+
 template <class Math, bool FUSED, int VAR>
 cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
-    static int num_sms = 0;
-    if (num_sms == 0) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-    }
+    int num_sms = 0;
+    const cudaError_t e = prepare_device<attention_kernel<Math, FUSED, VAR>>(&num_sms);
+    if (e != cudaSuccess) return e;
     const int M = (p.num_heads / p.num_kv_heads) * p.q_len;
     const int base = smem_bytes<Math, FUSED>(0, M, p.q_len, p.head_dim);
     int stages = (kSmemLimit - base) / (Math::STAGE + 20);
@@ -2209,13 +2222,6 @@ cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& 
         if (VAR == kScored && p.head_dim == 64) p.seg_cost = p.seg_cost > 32 ? p.seg_cost : 32;
     }
     const int smem = smem_bytes<Math, FUSED>(stages, M, p.q_len, p.head_dim);
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(attention_kernel<Math, FUSED, VAR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemLimit);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
     const int cap = num_sms < kMaxGrid ? num_sms : kMaxGrid;
     int grid;
     if (p.mode == kModeSingle) {
