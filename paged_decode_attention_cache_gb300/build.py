@@ -26,6 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpkv.so")
 OBJDIR = os.path.join(PKG, "_build")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_ABI = os.path.join(OBJDIR, "binding.abi")   # what it was built for
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 LIB_TIMELINE = os.path.join(PKG, "libpkv_timeline.so")
 OBJDIR_TIMELINE = os.path.join(PKG, "_build_timeline")
@@ -58,10 +59,29 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
+def _binding_abi() -> str:
+    """What _binding.so is compiled for besides its sources: this Python and this torch."""
+    import platform
+    import sysconfig
+    import torch
+    return "\n".join((sysconfig.get_config_var("SOABI") or "", platform.machine(), torch.__version__,
+                      str(int(torch._C._GLIBCXX_USE_CXX11_ABI)))) + "\n"
+
+
+def binding_fits() -> bool:
+    """Whether the _binding.so that is there was built for this Python and this torch."""
+    try:
+        with open(BINDING_ABI) as f:
+            return os.path.exists(BINDING) and f.read() == _binding_abi()
+    except OSError:
+        return False
+
+
 def build_binding(force: bool = False) -> str:
-    """_binding.so: reads torch tensors and calls libpkv.so, which it loads when told to."""
+    """_binding.so: reads torch tensors and calls libpkv.so, which it loads when told to.  Rebuilt when a
+    source is newer, and when it was built for another Python or torch."""
     newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "pkv.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    if not force and binding_fits() and os.path.getmtime(BINDING) >= newest:
         return BINDING
     import sysconfig
     import torch
@@ -76,7 +96,13 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.makedirs(os.path.dirname(BINDING_ABI), exist_ok=True)
+    if os.path.exists(BINDING_ABI):
+        os.remove(BINDING_ABI)   # none while the two files could disagree
     os.replace(tmp, BINDING)
+    with open(BINDING_ABI + f".tmp.{os.getpid()}", "w") as f:
+        f.write(_binding_abi())
+    os.replace(f.name, BINDING_ABI)
     return BINDING
 
 

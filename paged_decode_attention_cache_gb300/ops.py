@@ -166,6 +166,8 @@ def _calls():
         lib()
         if not os.path.exists(_build.BINDING):
             raise RuntimeError(f"{_build.BINDING} is not built: call __graft_entry__.build()")
+        if not _build.binding_fits():
+            raise RuntimeError(f"{_build.BINDING} was built for another Python or torch: call __graft_entry__.build()")
         from . import _binding as module
         module.load(library_path())
         _binding = module
