@@ -195,8 +195,10 @@ pkv_status pkv_quantize_kv(const pkv_cache *cache, const void *k_new, const void
  *   need = t rounded up to three significant bits (I8) or to a power of two (E4M3)
  *   s = need if the first new token opens the block, else max(the block's scale, need);
  *       older rows, if the scale grew: code = round(code * (s_old / s))
- *   new rows: code = round(x * (1 / s)); s = 0 (all zero): code 0
- * so codes and scales are reproducible bit for bit.  Rows behind the last new
+ *   new rows: code = round(x * (1 / s)); s = 0 (all zero) or below 2^-126: code 0
+ * so codes and scales are reproducible bit for bit.  A block's scale that is not
+ * positive and finite counts as 0 (its older rows stand for nothing): only a cache
+ * that its owner filled can hold one.  Rows behind the last new
  * token keep their bytes, and so does every block the call does not touch.  A
  * sequence with context_lens[s] <= 0 is padding and is skipped; new rows before
  * position 0 are skipped; positions past the block table are skipped and flag

@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(kThreads, 1) append_blocks_kernel(BlockWritePa
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s_new = fmaxf(s_old, scale_for<E4M3>(amax));
-    const float inv = s_new > 0.f ? __fdiv_rn(1.f, s_new) : 0.f;
+    // a scale below 2^-126, which only the cache's owner can have put there, stays only for new rows of zeros: their codes
+    // are 0, not 0 times its infinite reciprocal
+    const float inv = s_new >= 1.17549435e-38f ? __fdiv_rn(1.f, s_new) : 0.f;
 
     // ---- the block's older rows, for a scale that grew
     if (a > 0 && s_new > s_old) {

@@ -156,3 +156,30 @@ def test_zeros_under_verify_blocks(schedule, kind):
     got = g.out.double().cpu().numpy()
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= R.tolerance(biggest, vmax)[0] + 2.0 ** -24 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("scale", [2.0 ** -149, 1e-40, 2.0 ** -127, 2.0 ** -126])
+def test_zeros_appended_behind_a_subnormal_scale(kind, scale):
+    # the block's scale stays, so do the older codes, and the new ones are zeros
+    rng = np.random.default_rng(55)
+    D, c = 64, 7
+    st = State(rng, kind, 1, HKV, D)
+    for t in (st.cache.k_scale, st.cache.v_scale):
+        t.fill_(scale)
+    before = [t.view(torch.uint8).clone() for t in (st.cache.k, st.cache.v)]
+    held = st.cache.k_scale.clone()
+    new = torch.zeros((1, HKV, D), dtype=torch.bfloat16, device="cuda")
+    seqs = ops.Seqs(torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([c + 1], dtype=torch.int32, device="cuda"))
+    ops.pkv_quantize_kv_blocks(st.cache, new, -new, seqs, None, st.err)
+    for was, t in zip(before, (st.cache.k, st.cache.v)):
+        got = t.view(torch.uint8)
+        assert torch.equal(got[:, :c], was[:, :c]) and torch.equal(got[:, c + 1:], was[:, c + 1:])
+        assert ((got[:, c] & 0x7f) == 0).all()
+    assert torch.equal(st.cache.k_scale, held) and torch.equal(st.cache.v_scale, held)
+    # something to hold: the scale grows to the grid and the older codes shrink with it
+    k, v = rows(rng, 1, HKV, D, "bf16"), rows(rng, 1, HKV, D, "bf16")
+    st.kc, st.vc = (R.values(t, kind) for t in (st.cache.k, st.cache.v))
+    st.ks, st.vs = (t.cpu().numpy().copy() for t in (st.cache.k_scale, st.cache.v_scale))
+    st.append(k, v, np.zeros((1, 1), np.int32), [c + 2], [1])
+    st.same()
