@@ -246,6 +246,8 @@ typedef struct pkv_rope_scaling {
 /*
  * The frequencies of a rotary table, on the HOST: freq [rotary_dim/2] as 64-bit
  * fractions of a turn, to be copied to the device once.  scaling may be NULL.
+ * Worked out in fp64: an entry is within 2^-53 of a turn of its formula (base and
+ * factor 1 or more).
  */
 pkv_status pkv_rope_frequencies(uint64_t *freq, int32_t rotary_dim, double base, const pkv_rope_scaling *scaling);
 
@@ -262,8 +264,11 @@ pkv_status pkv_rope_frequencies(uint64_t *freq, int32_t rotary_dim, double base,
  *   cache      an fp16 / bf16 cache of `dtype`, or NULL for no write (then v and
  *              slot_mapping are ignored and k_out is needed).  For a quantised cache
  *              take k_out and call its own write.
- *   positions  int64 [num_tokens], any value (negative too): the angle is exact to
- *              2^-25 of a half-turn at every position.
+ *   positions  int64 [num_tokens], any value (negative too): the angle is the position
+ *              times the table's frequency, the product exact and rounded once, to 2^-24
+ *              of a half-turn.  What the table's own rounding adds grows with the
+ *              position: at most 2^-26 of a half-turn up to position 2^26 (see
+ *              pkv_rope_frequencies), 2^-53 of a turn per position beyond.
  *   slot_mapping  as for pkv_reshape_and_cache.  A token without a slot is rotated
  *              all the same.
  * Sums and products are fp32, rounded once.  num_tokens == 0 is a no-op.

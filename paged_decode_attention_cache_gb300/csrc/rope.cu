@@ -5,11 +5,13 @@
 //   (a, b) -> (a c - b s, b c + a s) for the pairs (i, i + R/2) (half layout) or
 //   (2i, 2i + 1) (interleaved) of the first R = rotary_dim dims of a head.
 //
-// The angle is exact whatever the position: f_i is held as a 64-bit fraction of
+// The product is exact whatever the position: f_i is held as a 64-bit fraction of
 // a turn, so the product's low 64 bits are the phase (whole turns fall off the
 // top), one integer multiply where fp32 loses the angle of a far position and
 // fp64 runs at a small part of the fp32 rate.  The phase's top 32 bits are
-// rounded to fp32 half-turns (2^-25 of a half-turn) for sincospif.
+// rounded to fp32 half-turns for sincospif: 2^-25 of a half-turn, and 2^-31 for the
+// bits below them.  The table is fp64's: its entries' 2^-53 of a turn count as often as
+// the position says.
 //
 // Bound: HBM for prompts (each row read once, written once), launch and
 // dependent-load latency for a few tokens.  A CTA takes a few tokens: its

@@ -85,3 +85,46 @@ def test_refusals(ops, change):
 def test_no_tokens_is_a_no_op(ops):
     assert call(ops, T=0, q=None, q_out=None, k=None, v=None) == ops.PKV_OK
     assert call(ops, D=96, cache=False) == ops.PKV_ERR_UNSUPPORTED
+
+
+def test_frequencies_are_within_what_the_header_says(ops):
+    """The table against the formulas in 60 digits: an entry is off by at most 2^-53 turns.  In units of 2^-53 / (2 pi) turns,
+    theta = base^(-x) <= 1 with x = 2i/R: the exponent's rounding x ln(base) base^-x <= 1/e, pow 1, a scaled base's
+    2 x base^-x <= 2 / (e ln(base)) < 0.1, the factor 1, 2 pi's own 1/2, the division 1: 4.  By parts mixes only where
+    theta <= 2 pi high / original, far below 1, so its dozen roundings add nothing that counts.  4 / (2 pi) < 1."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+
+    def exact(r, base, kind, factor, low, high, original):
+        base, factor = Decimal(base), Decimal(factor)
+        if kind == "ntk" and r > 2:
+            base *= (factor.ln() * r / (r - 2)).exp()
+        step, f0 = (base.ln() * -2 / r).exp(), Decimal(1)
+        for _ in range(r // 2):
+            f, f0 = f0, f0 * step
+            if kind == "linear":
+                f /= factor
+            if kind == "by_parts":
+                n = Decimal(original) * f / two_pi
+                m = min(Decimal(1), max(Decimal(0), (n - Decimal(low)) / (Decimal(high) - Decimal(low))))
+                f = f / factor * (1 - m) + f * m
+            yield f / two_pi
+
+    worst = Decimal(0)
+    for r in (2, 6, 20, 50, 64, 96, 128):
+        for base in (10000.0, 150000.0, 500000.0, 1e7):
+            for kind, factor, high in (("none", 1.0, 4.0), ("linear", 3.0, 4.0), ("ntk", 2.5, 4.0), ("ntk", 8.0, 4.0),
+                                       ("by_parts", 8.0, 4.0), ("by_parts", 40.0, 32.0)):
+                got = ops.pkv_rope_frequencies(r, base, kind, factor, 1.0, high, 8192.0).tolist()
+                for g, w in zip(got, exact(r, base, kind, factor, 1.0, high, 8192.0)):
+                    worst = max(worst, abs(Decimal(g % 2 ** 64) / Decimal(2) ** 64 - w))
+    assert worst <= Decimal(2) ** -53, math.log2(worst)
+
+
+def test_the_header_states_the_angle_by_the_table():
+    import os
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "pkv.h")).read()
+    flat = " ".join(text.replace(" * ", " ").split())
+    assert "exact to 2^-25 of a half-turn at every position" not in flat
+    assert "2^-53 of a turn" in flat and "up to position 2^26" in flat
