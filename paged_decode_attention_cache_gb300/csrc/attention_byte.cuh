@@ -799,7 +799,7 @@ byte_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     mth.scale_log2_ = p.scale_log2;
     int st = warp;       // this warp's next stage, and its phase
     uint32_t phase = 0;
-    bool lost = false;   // a copy did not come: no later one is waited for
+    bool lost = false;   // a copy did not come: no later one is read, no stage filled
     while (true) {
         Seg sg;
         bool more, on;   // on: the share goes on behind this segment
@@ -836,6 +836,7 @@ byte_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
             } else {
                 lost = true;
                 if (lane == 0) flag_error(p.err, PKV_DEVERR_TIMEOUT);
+                break;   // st stays at the copy that did not come
             }
             st += NCW;
             if (st >= S) {
@@ -869,11 +870,12 @@ byte_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
         // ---- a part of the pair: left for the merge
         const int i = 2 * warp + ((single || on) ? 0 : 1);
         float* dst = partial(i, sg.s);
+        const bool hold = lost && (i & 1);   // a copy may still be under way into that stage (see below)
         mth.each(M, lane, [&](int q, int d, float x, float y, float Mx, float L) {
-            *reinterpret_cast<float2*>(dst + ob_idx(q, d, D)) = make_float2(x, y);
+            if (!hold) *reinterpret_cast<float2*>(dst + ob_idx(q, d, D)) = make_float2(x, y);
             if (d == 0) {
-                mw[i * MR + q] = Mx;
-                lw[i * MR + q] = L;
+                mw[i * MR + q] = hold ? -INFINITY : Mx;
+                lw[i * MR + q] = hold ? 0.f : L;
             }
         });
         if (lane == 0) {
@@ -895,6 +897,22 @@ byte_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
             }
             __syncthreads();   // the slots are free again
         }
+    }
+    if (lost) {
+        // The stages that were filled when a copy did not come, a ring of them from that one on, are waited for once more
+        // (one that was not filled runs into the limit), so that no copy is under way when the CTA ends.  The partial that
+        // was not written there counts for nothing.
+        for (int n = S / NCW; n > 0; --n) {
+            mbar_wait(&full[st], phase);
+            st += NCW;
+            if (st >= S) {
+                st -= S;
+                phase ^= 1u;
+            }
+        }
+        __syncwarp();
+        for (int i4 = lane; i4 < n4; i4 += 32)
+            reinterpret_cast<float4*>(smem + size_t(warp) * Math::STAGE)[i4] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     // context longer than its table: flagged once per sequence
     for (int s = blockIdx.x * CT + tid; s < p.num_seqs; s += gridDim.x * CT)
