@@ -102,7 +102,9 @@ typedef enum pkv_cache_kind {
  *                   not numbers here)  [num_blocks, 16, num_kv_heads, head_dim]
  *   k_scale, v_scale  fp32 [num_blocks, num_kv_heads]; v_zero, v_group unused
  *   Dequantised values: code * scale.  Attention and gather take any finite
- *   scale; pkv_quantize_kv_blocks writes its own grid of them.
+ *   scale, zero, negative and subnormal ones too, as long as the values and the
+ *   scores stay below 2^100 in magnitude; pkv_quantize_kv_blocks writes its own
+ *   grid of them.
  */
 typedef struct pkv_cache {
     int32_t kind;          /* pkv_cache_kind */
@@ -155,7 +157,8 @@ typedef struct pkv_seqs {
  *                 (PKV_CACHE_F16 or PKV_CACHE_BF16 caches only).
  *   slot_mapping  int64 [num_tokens]; a negative slot is padding and is skipped;
  *                 a slot >= num_blocks*16 is skipped and flags PKV_DEVERR_OOB_SLOT.
- * The copy is bit-exact.  num_tokens == 0 is a no-op.
+ * The copy is bit-exact.  No two tokens of one call may have the same slot (its row
+ * would be unspecified).  num_tokens == 0 is a no-op.
  */
 pkv_status pkv_reshape_and_cache(const pkv_cache *cache, const void *k_new, const void *v_new,
                                  const int64_t *slot_mapping, int32_t num_tokens,

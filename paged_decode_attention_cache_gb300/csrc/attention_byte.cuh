@@ -16,7 +16,7 @@
 // over all the warps a barrier at each segment's end took a third of their time.
 // Measured (one GB300, 8 kv heads of 128 dims): 8 x 65536 int8, 8 query rows a kv head,
 // 703 MB in 120.6 us, 5.8 TB/s of 6.8 measured for a copy; 32 x 4096 e4m3, 4 rows,
-// 172 MB in 36.8 us, 4.7 TB/s, of which the plan before the first copy takes about 5 us
+// 172 MB in 36.9 us, 4.7 TB/s, of which the plan before the first copy takes about 5 us
 // and the merges 4; half the MMAs (both halves of P in one) changed nothing there.
 #pragma once
 

@@ -2218,7 +2218,9 @@ cudaError_t launch_math(AttnParams p, const CUtensorMap& km, const CUtensorMap& 
         p.seg_cost = Math::kSegCost;
         // A block of head_dim 64 is half the work of one of 128, a segment's merge and combine are not.  Scored passes
         // at 24 / 32 / 48 / 64: 16 x 1024 (8 kv heads) 13.5 / 13.1 / 12.4 / 12.3 us, 100 x 700 (2) 16.0 / 15.5 / 15.8 / 16.1,
-        // 8 x 4096 (8) 17.3 / 17.2 / 17.8 / 18.6, 4 x 8000 16.9 / 17.3 / 16.9 / 17.8, 32 x 2000 29.7 / 29.7 / 30.5 / 30.5
+        // 8 x 4096 (8) 17.3 / 17.2 / 17.8 / 18.6, 4 x 8000 16.9 / 17.3 / 16.9 / 17.8, 32 x 2000 29.7 / 29.7 / 30.5 / 30.5.
+        // No value is best for all: 32 has the smallest sum; it costs 4 x 8000 2.4 % against 24, and 16 x 1024 would
+        // gain 6 % at 64.
         if (VAR == kScored && p.head_dim == 64) p.seg_cost = p.seg_cost > 32 ? p.seg_cost : 32;
     }
     const int smem = smem_bytes<Math, FUSED>(stages, M, p.q_len, p.head_dim);

@@ -7,7 +7,7 @@
 // 7 us that every balanced call has (12 over the 8-bit caches); the cap's and the bias's
 // dozen instructions a score hide behind it.  Measured on one GB300: bf16, 88 MB of
 // capped scores in 19.5 us (19.1 without the cap), 68 MB behind a window and a prefix in
-// 17.0 us (4.0 TB/s); int8, 88 MB with document starts in 29.2 us (28.7 without cap and bias).
+// 17.0 us (4.0 TB/s); int8, 88 MB with document starts in 29.5 us (0.5 less without cap and bias).
 #include "attention_byte.cuh"
 
 namespace pkv {

@@ -237,8 +237,10 @@ __device__ __forceinline__ void expand16(uint4 c, float scale, uint4& lo, uint4&
 // A CTA expands kGatherItems items of logical block b of sequence s, an item being 16 dims
 // of one (token, kv head), K and V: 16-byte loads, and 32-byte stores where the outputs are
 // aligned for them (two 16-byte stores leave every 32-byte sector to two instructions).
-// Bound by HBM, which writes two bytes for each it reads: 375 MB at 6.5 TB/s (of
-// 6.8 measured for a copy), 149 MB at 6.0, 73 MB at 5.4 (13.4 us).  Measured on the way at
+// Bound by HBM, which writes two bytes for each it reads, where the outputs pass L2: 375 MB
+// at 6.5 TB/s (of 6.8 measured for a copy), 149 MB at 6.0.  At 73 MB (13.4 us) the 49 MB of
+// outputs stay in the 129 MB L2 (0.6 MB were written to DRAM while it ran): there the start of
+// the launch and the issue of loads and stores count.  Measured on the way at
 // 73 MB: 17.1 us with a CTA of 256 threads per block and 16-byte stores, 15.8 with halves of
 // blocks, 14.7 with 32-byte stores too, 14.0 with one item per thread at a time and quarters
 // of 8 heads of 128 dims (256 items), 15.3 with eighths.
