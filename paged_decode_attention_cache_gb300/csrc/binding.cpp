@@ -229,7 +229,8 @@ Rows rows(const Call& call, PyObject* o, const char* name, at::IntArrayRef shape
               (long long)shape[1], (long long)shape[2]);
     call.where(t);
     const auto st = t.strides();
-    if (st[2] != 1 || (st[1] != shape[2] && shape[1] > 1)) raise(PyExc_ValueError, "%s: a token's heads must be contiguous", name);
+    // no element, no stride that matters (torch keeps what an empty view came with)
+    if (t.numel() > 0 && (st[2] != 1 || (st[1] != shape[2] && shape[1] > 1))) raise(PyExc_ValueError, "%s: a token's heads must be contiguous", name);
     // one row (or none): any stride will do
     return {t.data_ptr(), shape[0] > 1 ? st[0] : shape[1] * shape[2]};
 }
