@@ -5,8 +5,9 @@ contiguity of the torch tensors it is given, passes their device pointers and
 the current CUDA stream to the C entry point of the same name, and raises
 ``PkvError`` with the library's message on a non-OK status.  There is no CPU
 path: if the library is not built, every call raises.  The calls that a decode
-step makes go through a CPython module (csrc/binding.cpp), the others through
-ctypes.
+step makes (rotary, append, balanced and scored attention, dequantising read-back)
+go through a CPython module (csrc/binding.cpp), which also checks the tensors'
+sizes and that they live on the current device; the others go through ctypes.
 """
 from __future__ import annotations
 
