@@ -512,6 +512,80 @@ int32_t pkv_sparse_worthwhile(const int32_t *page_counts, const int32_t *context
                               float min_sparsity);
 
 /*
+ * The pages (16-token blocks) that a cheap score selects, for every query token
+ * and kv head by itself, and the attention over them (this library's own): three
+ * calls, kept apart so that one selection can serve several layers, or a
+ * caller's own lists the attention.
+ *
+ * 1. Bounds.  For each block and kv head, the smallest and the largest stored key, dim
+ *    by dim.
+ *   bounds  [num_blocks, num_kv_heads, 2, head_dim]: lo, then hi.  fp16 / bf16 caches:
+ *           of the cache's type; PKV_CACHE_I8 / E4M3: the smallest and largest CODES
+ *           (the block's K scale multiplies them; it must not be negative, and
+ *           pkv_quantize_kv_blocks writes none that is); PKV_CACHE_K8V4: fp16, code *
+ *           scale rounded down and up.
+ * The n_s new tokens of sequence s are its last ones, [context_lens[s] - n_s,
+ * context_lens[s]), already in the cache; the bounds of every block that holds one are
+ * worked out from all that the block stores (min(16, context_lens[s] - first token)
+ * rows), those of the others are not touched.  So the call follows each cache write.
+ *   cu_new_lens  int32 [num_seqs + 1] device: n_s = cu[s+1] - cu[s]; or NULL: q_len each.
+ * Keys must be finite (the bounds of a block with others are unspecified).  A sequence
+ * with context_lens[s] <= 0 or n_s <= 0 is skipped; positions past the block table are
+ * skipped and flag PKV_DEVERR_CAPACITY, a block id out of range PKV_DEVERR_OOB_BLOCK.
+ */
+pkv_status pkv_key_bounds(void *bounds, const pkv_cache *cache, const int32_t *cu_new_lens, const pkv_seqs *seqs,
+                          uint32_t *err_flags, pkv_stream_t stream);
+
+/*
+ * 2. Selection.  Query token r of sequence s sees the tokens up to its own
+ * position, v of them, in n = ceil(v / 16) pages.  The score of page b for its g
+ * query heads of a kv head is
+ *   sum over the g heads and the dims d of max(q[d] lo_b[d], q[d] hi_b[d]),
+ * which no key of the page exceeds with those queries, summed over them (for a positive
+ * scale).  The list of (r, kv head): every page if n <= max_pages; else the first
+ * keep_first and the last keep_last, and of the others those with the largest scores,
+ * max_pages in all.  The scores decide as if worked out exactly (fp64); the lower page
+ * goes first where two are equal.  A score that is not a number counts as -infinity,
+ * and so does that of a block id out of range (flags PKV_DEVERR_OOB_BLOCK).
+ *   page_lists   out int32 [num_rows, num_kv_heads, max_pages]: logical pages in
+ *                increasing order, -1 behind the last.
+ *   page_counts  out int32 [num_rows, num_kv_heads].
+ *   q            [num_rows, num_heads, head_dim], q_dtype as for pkv_paged_attention.
+ *   bounds       of pkv_key_bounds; of `cache` only the kind, the sizes and, for I8 and
+ *                E4M3, k_scale are used.
+ *   cu_q_lens    int32 [num_seqs + 1] device, not decreasing, cu[0] = 0, cu[num_seqs] <=
+ *                num_rows: sequence s's query tokens are rows cu[s] .. cu[s+1] - 1, its
+ *                last stored tokens (a chunk of a prompt); or NULL: q_len rows each, and
+ *                num_rows = num_seqs * q_len.  q_len has no limit here.
+ * Rows behind cu[num_seqs] keep their lists and counts.  A token that sees nothing gets
+ * an empty list.  keep_first + keep_last <= max_pages.  A sliding window is
+ * PKV_ERR_UNSUPPORTED, and so is max_blocks_per_seq above 425,984.
+ */
+pkv_status pkv_select_pages(int32_t *page_lists, int32_t *page_counts, int32_t max_pages, int32_t keep_first,
+                            int32_t keep_last, const void *q, pkv_dtype q_dtype, int32_t num_heads, int32_t num_rows,
+                            const void *bounds, const pkv_cache *cache, const int32_t *cu_q_lens,
+                            const pkv_seqs *seqs, uint32_t *err_flags, pkv_stream_t stream);
+
+/*
+ * 3. Attention of each (query token, kv head) over its own list: the result of
+ * pkv_paged_attention over the listed pages' visible tokens (those up to the query
+ * token's own position); pages that are not listed are not read.  Every cache kind.
+ *   page_lists, page_counts  as pkv_select_pages writes them; an entry that is not a page
+ *                with a visible token, or not above the entries taken before it, is
+ *                skipped and flags PKV_DEVERR_PAGE_LIST; counts are cut to [0, max_pages].
+ *   cu_q_lens, num_rows  as for pkv_select_pages.
+ * Rows behind cu[num_seqs] keep their outputs; a row without a listed page gets zeros.
+ * No workspace.  K and V of tokens that a row does not see reach no output of it,
+ * whatever they hold.  max_pages above 184,320 and a sliding window are
+ * PKV_ERR_UNSUPPORTED.
+ */
+pkv_status pkv_paged_attention_selected(void *out, pkv_dtype out_dtype, const void *q, pkv_dtype q_dtype,
+                                        int32_t num_heads, int32_t num_rows, float scale, const pkv_cache *cache,
+                                        const int32_t *cu_q_lens, const pkv_seqs *seqs, const int32_t *page_lists,
+                                        const int32_t *page_counts, int32_t max_pages, uint32_t *err_flags,
+                                        pkv_stream_t stream);
+
+/*
  * Host-side grouping for pkv_paged_attention_cascade [MLXCEL §"Paged Decode
  * Storage and Kernels": cascade groups gated by a minimum member count and a
  * minimum number of shared whole pages].  All pointers are HOST memory:

@@ -793,6 +793,141 @@ int32_t pkv_sparse_worthwhile(const int32_t* page_counts, const int32_t* context
     return skipped >= double(min_sparsity) * double(total) * (1.0 - 1e-6) ? 1 : 0;
 }
 
+pkv_status pkv_key_bounds(void* bounds, const pkv_cache* cache, const int32_t* cu_new_lens, const pkv_seqs* seqs,
+                          uint32_t* err_flags, pkv_stream_t stream) {
+    pkv_status st = check_cache(cache, false);
+    if (st != PKV_OK) return st;
+    if ((st = check_seqs(seqs)) != PKV_OK) return st;
+    CHECK_PTR(bounds, "bounds");
+    if (seqs->num_seqs == 0) return ok();
+    pkv::KeyBoundsParams p{};
+    p.bounds = bounds;
+    p.k_cache = cache->k;
+    p.k_scale = cache->k_scale;
+    p.cu_new = cu_new_lens;
+    p.block_tables = seqs->block_tables;
+    p.context_lens = seqs->context_lens;
+    p.num_seqs = seqs->num_seqs;
+    p.max_blocks = seqs->max_blocks_per_seq;
+    p.q_len = seqs->q_len;
+    p.num_blocks = cache->num_blocks;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.head_dim = cache->head_dim;
+    p.err = err_flags;
+    return cuda_result(pkv::launch_key_bounds(p, cache->kind, reinterpret_cast<cudaStream_t>(stream)), "key_bounds launch");
+}
+
+// What the selection and the attention over it check alike.
+static pkv_status selected_args(const pkv_cache* cache, const pkv_seqs* seqs, pkv_dtype q_dtype, int32_t num_heads,
+                                int32_t num_rows, const int32_t* cu_q_lens, int32_t max_pages) {
+    pkv_status st = check_cache(cache, false);
+    if (st != PKV_OK) return st;
+    if ((st = check_seqs(seqs)) != PKV_OK) return st;
+    if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return fail(PKV_ERR_INVALID_ARG, "q_dtype %d", q_dtype);
+    if ((cache->kind == PKV_CACHE_F16 || cache->kind == PKV_CACHE_BF16) && q_dtype != cache_dtype(cache))
+        return fail(PKV_ERR_INVALID_ARG, "q_dtype must match the fp16/bf16 cache dtype");
+    if (num_heads < 1 || num_heads % cache->num_kv_heads != 0)
+        return fail(PKV_ERR_INVALID_ARG, "num_heads %d is not a multiple of num_kv_heads %d", num_heads,
+                    cache->num_kv_heads);
+    const int g = num_heads / cache->num_kv_heads;
+    if (g != 1 && g != 2 && g != 4 && g != 8) return fail(PKV_ERR_UNSUPPORTED, "group size %d (1, 2, 4 or 8)", g);
+    if (seqs->sliding_window != 0) return fail(PKV_ERR_UNSUPPORTED, "selected pages with a sliding window");
+    if (max_pages < 1) return fail(PKV_ERR_INVALID_ARG, "max_pages %d", max_pages);
+    if (num_rows < 0 || num_rows > INT32_MAX / 16) return fail(PKV_ERR_INVALID_ARG, "num_rows %d", num_rows);
+    if (!cu_q_lens && int64_t(seqs->num_seqs) * seqs->q_len != num_rows)
+        return fail(PKV_ERR_INVALID_ARG, "without cu_q_lens num_rows (%d) must be num_seqs * q_len (%lld)", num_rows,
+                    (long long)seqs->num_seqs * seqs->q_len);
+    return PKV_OK;
+}
+
+pkv_status pkv_select_pages(int32_t* page_lists, int32_t* page_counts, int32_t max_pages, int32_t keep_first,
+                            int32_t keep_last, const void* q, pkv_dtype q_dtype, int32_t num_heads, int32_t num_rows,
+                            const void* bounds, const pkv_cache* cache, const int32_t* cu_q_lens, const pkv_seqs* seqs,
+                            uint32_t* err_flags, pkv_stream_t stream) {
+    pkv_status st = selected_args(cache, seqs, q_dtype, num_heads, num_rows, cu_q_lens, max_pages);
+    if (st != PKV_OK) return st;
+    if (keep_first < 0 || keep_last < 0 || int64_t(keep_first) + keep_last > max_pages)
+        return fail(PKV_ERR_INVALID_ARG, "keep_first %d and keep_last %d must fit max_pages %d", keep_first, keep_last,
+                    max_pages);
+    if (seqs->max_blocks_per_seq > pkv::kSelectMaxBlocks)
+        return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq %d (at most %d)", seqs->max_blocks_per_seq,
+                    pkv::kSelectMaxBlocks);
+    if (num_rows == 0 || seqs->num_seqs == 0) return ok();
+    CHECK_PTR(q, "q");
+    CHECK_PTR(bounds, "bounds");
+    if (!page_lists || !page_counts) return fail(PKV_ERR_INVALID_ARG, "page_lists / page_counts is NULL");
+    pkv::SelectParams p{};
+    p.lists = page_lists;
+    p.counts = page_counts;
+    p.q = q;
+    p.q_dtype = q_dtype;
+    p.bounds = bounds;
+    p.k_scale = pkv::is_byte_cache(cache->kind) ? static_cast<const float*>(cache->k_scale) : nullptr;
+    p.cu_q = cu_q_lens;
+    p.block_tables = seqs->block_tables;
+    p.context_lens = seqs->context_lens;
+    p.num_rows = num_rows;
+    p.num_seqs = seqs->num_seqs;
+    p.max_blocks = seqs->max_blocks_per_seq;
+    p.q_len = seqs->q_len;
+    p.num_heads = num_heads;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.head_dim = cache->head_dim;
+    p.num_blocks = cache->num_blocks;
+    p.max_pages = max_pages;
+    p.keep_first = keep_first;
+    p.keep_last = keep_last;
+    p.err = err_flags;
+    return cuda_result(pkv::launch_select_pages(p, cache->kind, reinterpret_cast<cudaStream_t>(stream)),
+                       "select_pages launch");
+}
+
+pkv_status pkv_paged_attention_selected(void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype,
+                                        int32_t num_heads, int32_t num_rows, float scale, const pkv_cache* cache,
+                                        const int32_t* cu_q_lens, const pkv_seqs* seqs, const int32_t* page_lists,
+                                        const int32_t* page_counts, int32_t max_pages, uint32_t* err_flags,
+                                        pkv_stream_t stream) {
+    pkv_status st = selected_args(cache, seqs, q_dtype, num_heads, num_rows, cu_q_lens, max_pages);
+    if (st != PKV_OK) return st;
+    if (out_dtype != PKV_F16 && out_dtype != PKV_BF16 && out_dtype != PKV_F32)
+        return fail(PKV_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
+    if (!(scale == scale)) return fail(PKV_ERR_INVALID_ARG, "scale is NaN");
+    if (max_pages > pkv::kSelectedMaxPages)
+        return fail(PKV_ERR_UNSUPPORTED, "max_pages %d (at most %d)", max_pages, pkv::kSelectedMaxPages);
+    if (num_rows == 0 || seqs->num_seqs == 0) return ok();
+    CHECK_PTR(out, "out");
+    CHECK_PTR(q, "q");
+    if (!page_lists || !page_counts) return fail(PKV_ERR_INVALID_ARG, "page_lists / page_counts is NULL");
+    pkv::SelectedParams p{};
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.q = q;
+    p.q_dtype = q_dtype;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.k = cache->k;
+    p.v = cache->v;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.v_zero = cache->v_zero;
+    p.lists = page_lists;
+    p.counts = page_counts;
+    p.cu_q = cu_q_lens;
+    p.block_tables = seqs->block_tables;
+    p.context_lens = seqs->context_lens;
+    p.num_rows = num_rows;
+    p.num_seqs = seqs->num_seqs;
+    p.max_blocks = seqs->max_blocks_per_seq;
+    p.q_len = seqs->q_len;
+    p.num_heads = num_heads;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.head_dim = cache->head_dim;
+    p.num_blocks = cache->num_blocks;
+    p.max_pages = max_pages;
+    p.err = err_flags;
+    return cuda_result(pkv::launch_attention_selected(p, cache->kind, reinterpret_cast<cudaStream_t>(stream)),
+                       "selected attention launch");
+}
+
 pkv_status pkv_decode_step_balanced(void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype,
                                     int32_t num_heads, float scale, const pkv_cache* cache, const pkv_seqs* seqs,
                                     const void* k_new, const void* v_new, pkv_dtype src_dtype,

@@ -242,6 +242,9 @@ struct Lib {
     decltype(&pkv_paged_attention_scored) paged_attention_scored;
     decltype(&pkv_paged_attention_balanced) paged_attention_balanced;
     decltype(&pkv_gather_kv_cache_dequant) gather_kv_cache_dequant;
+    decltype(&pkv_key_bounds) key_bounds;
+    decltype(&pkv_select_pages) select_pages;
+    decltype(&pkv_paged_attention_selected) paged_attention_selected;
 } lib;
 void* handle = nullptr;
 
@@ -290,6 +293,9 @@ PyObject* py_load(PyObject*, PyObject* arg) {
     PKV_LOOKUP(paged_attention_scored)
     PKV_LOOKUP(paged_attention_balanced)
     PKV_LOOKUP(gather_kv_cache_dequant)
+    PKV_LOOKUP(key_bounds)
+    PKV_LOOKUP(select_pages)
+    PKV_LOOKUP(paged_attention_selected)
 #undef PKV_LOOKUP
     lib = l;
     handle = h;   // kept for the life of the process
@@ -466,6 +472,115 @@ PyObject* py_gather_kv_cache_dequant(PyObject*, PyObject* const* a, Py_ssize_t n
     });
 }
 
+// A cache's key bounds: their type and shape; `at` after the other sizes have been checked.
+const at::Tensor& bounds_tensor(PyObject* o, const CacheArg& c) {
+    const at::Tensor& b = tensor(o, "bounds");
+    const at::ScalarType t = b.scalar_type();
+    const bool fits_type = c.c.kind == PKV_CACHE_BF16 ? t == at::kBFloat16
+                         : c.c.kind == PKV_CACHE_I8   ? t == at::kChar
+                         : c.c.kind == PKV_CACHE_E4M3 ? t == at::ScalarType::Float8_e4m3fn || t == at::kByte
+                                                      : t == at::kHalf;
+    const int64_t shape[4] = {c.c.num_blocks, c.c.num_kv_heads, 2, c.c.head_dim};
+    if (!fits_type || b.sizes() != at::IntArrayRef(shape, 4))
+        raise(PyExc_ValueError, "bounds must be [num_blocks, num_kv_heads, 2, head_dim] of the cache's key type (k8v4: float16)");
+    return b;
+}
+
+// int32 [num_seqs + 1] or None
+const int32_t* prefix_sums(const Call& call, PyObject* o, const char* name, int32_t num_seqs) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != at::kInt || t.numel() != int64_t(num_seqs) + 1)
+        raise(PyExc_ValueError, "%s must be int32 [num_seqs + 1]", name);
+    return static_cast<const int32_t*>(call.ptr(t));
+}
+
+// The lists of pages of each (query token, kv head): their address and width.
+int32_t page_lists(const at::Tensor& lists, const at::Tensor& counts, int64_t rows, int32_t kv_heads) {
+    if (lists.scalar_type() != at::kInt || counts.scalar_type() != at::kInt)
+        raise(PyExc_ValueError, "page_lists / page_counts must be int32");
+    if (lists.dim() != 3 || lists.size(0) != rows || lists.size(1) != kv_heads || counts.dim() != 2 || counts.size(0) != rows ||
+        counts.size(1) != kv_heads)
+        raise(PyExc_ValueError, "page_lists must be [num_rows, num_kv_heads, max_pages] and page_counts [num_rows, num_kv_heads]");
+    return fits(lists.size(2), "max_pages");
+}
+
+// (bounds, cache, seqs, cu_new_lens, err_flags, stream)
+PyObject* py_key_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&] {
+        const Call call;
+        CacheArg c(a[1]);
+        SeqsArg s(a[2]);
+        const at::Tensor& b = bounds_tensor(a[0], c);
+        if (s.cl.t->numel() != s.s.num_seqs) raise(PyExc_ValueError, "context_lens must be [num_seqs]");
+        c.place(call);
+        s.place(call);
+        void* bp = call.ptr(b);
+        const int32_t* cu = prefix_sums(call, a[3], "cu_new_lens", s.s.num_seqs);
+        uint32_t* err = call.err(a[4]);
+        const pkv_stream_t stream = call.stream(a[5]);
+        return status_of([&] { return lib.key_bounds(bp, &c.c, cu, &s.s, err, stream); });
+    });
+}
+
+// (page_lists, page_counts, q, bounds, cache, seqs, cu_q_lens, keep_first, keep_last, err_flags, stream)
+PyObject* py_select_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&] {
+        const Call call;
+        const at::Tensor &lists = tensor(a[0], "page_lists"), &counts = tensor(a[1], "page_counts"), &q = tensor(a[2], "q");
+        CacheArg c(a[4]);
+        SeqsArg s(a[5]);
+        const at::Tensor& b = bounds_tensor(a[3], c);
+        pkv_dtype qt;
+        if (!half_type(q, &qt)) raise(PyExc_ValueError, "q must be float16 or bfloat16");
+        if (q.dim() != 3 || q.size(2) != c.c.head_dim || s.cl.t->numel() != s.s.num_seqs)
+            raise(PyExc_ValueError, "q must be [num_rows, num_heads, head_dim], context_lens [num_seqs]");
+        const int32_t pages = page_lists(lists, counts, q.size(0), c.c.num_kv_heads);
+        const long first = PyLong_AsLong(a[7]), last = PyLong_AsLong(a[8]);
+        if (PyErr_Occurred()) throw Raised{};
+        c.place(call);
+        s.place(call);
+        int32_t *lp = static_cast<int32_t*>(call.ptr(lists)), *cp = static_cast<int32_t*>(call.ptr(counts));
+        const void *qp = call.ptr(q), *bp = call.ptr(b);
+        const int32_t* cu = prefix_sums(call, a[6], "cu_q_lens", s.s.num_seqs);
+        const int32_t h = fits(q.size(1), "num_heads"), rows = fits(q.size(0), "num_rows"), kf = fits(first, "keep_first"),
+                      kl = fits(last, "keep_last");
+        uint32_t* err = call.err(a[9]);
+        const pkv_stream_t stream = call.stream(a[10]);
+        return status_of([&] { return lib.select_pages(lp, cp, pages, kf, kl, qp, qt, h, rows, bp, &c.c, cu, &s.s, err, stream); });
+    });
+}
+
+// (out, q, scale, cache, seqs, page_lists, page_counts, cu_q_lens, err_flags, stream)
+PyObject* py_paged_attention_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const Call call;
+        CacheArg c(a[3]);
+        SeqsArg s(a[4]);
+        const at::Tensor &out = tensor(a[0], "out"), &q = tensor(a[1], "q"), &lists = tensor(a[5], "page_lists"),
+                         &counts = tensor(a[6], "page_counts");
+        if (q.dim() != 3 || q.size(2) != c.c.head_dim || out.sizes() != q.sizes() || s.cl.t->numel() != s.s.num_seqs)
+            raise(PyExc_ValueError, "q and out must be [num_rows, num_heads, head_dim], context_lens [num_seqs]");
+        pkv_dtype qt;
+        if (!half_type(q, &qt)) raise(PyExc_ValueError, "q must be float16 or bfloat16");
+        const pkv_dtype ot = any_type(out, "out");
+        const int32_t pages = page_lists(lists, counts, q.size(0), c.c.num_kv_heads);
+        c.place(call);
+        s.place(call);
+        const float scale = float(as_double(a[2]));
+        void* op = call.ptr(out);
+        const void* qp = call.ptr(q);
+        const int32_t *lp = static_cast<const int32_t*>(call.ptr(lists)), *cp = static_cast<const int32_t*>(call.ptr(counts));
+        const int32_t* cu = prefix_sums(call, a[7], "cu_q_lens", s.s.num_seqs);
+        const int32_t h = fits(q.size(1), "num_heads"), rows = fits(q.size(0), "num_rows");
+        uint32_t* err = call.err(a[8]);
+        const pkv_stream_t stream = call.stream(a[9]);
+        return status_of([&] {
+            return lib.paged_attention_selected(op, ot, qp, qt, h, rows, scale, &c.c, cu, &s.s, lp, cp, pages, err, stream);
+        });
+    });
+}
+
 #define PKV_METHOD(n) {#n, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##n)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"load", py_load, METH_O, nullptr},
                          PKV_METHOD(rope_and_cache),
@@ -473,6 +588,9 @@ PyMethodDef methods[] = {{"load", py_load, METH_O, nullptr},
                          PKV_METHOD(paged_attention_scored),
                          PKV_METHOD(paged_attention_balanced),
                          PKV_METHOD(gather_kv_cache_dequant),
+                         PKV_METHOD(key_bounds),
+                         PKV_METHOD(select_pages),
+                         PKV_METHOD(paged_attention_selected),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

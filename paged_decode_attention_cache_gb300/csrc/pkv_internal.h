@@ -32,6 +32,27 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
+// The same with clusters of `cluster` CTAs along x (grid.x is a multiple of it).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem,
+                                  cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
 // Everything the attention kernels read besides the two tensor maps.
 struct AttnParams {
     // outputs: exactly one of {out} or {tmp_out, max_logits, exp_sums} is set
@@ -259,6 +280,65 @@ struct RopeParams {
     uint32_t* err;
 };
 cudaError_t launch_rope(RopeParams p, cudaStream_t stream);
+
+// The bounds of the pages that hold new tokens, and the selection of pages by them (select_pages.cu).
+struct KeyBoundsParams {
+    void* bounds;                 // [num_blocks, num_kv_heads, 2, head_dim]: lo, hi
+    const void* k_cache;
+    const void* k_scale;          // K8V4
+    const int32_t* cu_new;        // [num_seqs + 1] new tokens of each sequence, or null: q_len each
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int32_t num_seqs, max_blocks, q_len;
+    int32_t num_blocks, num_kv_heads, head_dim;
+    uint32_t* err;
+};
+cudaError_t launch_key_bounds(const KeyBoundsParams& p, int cache_kind, cudaStream_t stream);
+
+struct SelectParams {
+    int32_t* lists;               // out [num_rows, num_kv_heads, max_pages]
+    int32_t* counts;              // out [num_rows, num_kv_heads]
+    const void* q;                // [num_rows, num_heads, head_dim]
+    int32_t q_dtype;
+    const void* bounds;
+    const float* k_scale;         // 8-bit caches: [num_blocks, num_kv_heads]
+    const int32_t* cu_q;          // [num_seqs + 1] rows of each sequence, or null: q_len each
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int32_t num_rows, num_seqs, max_blocks, q_len;
+    int32_t num_heads, num_kv_heads, head_dim, num_blocks;
+    int32_t max_pages, keep_first, keep_last;
+    uint32_t* err;
+};
+// The pages that a cluster of 8 CTAs holds scores for in shared memory.
+constexpr int kSelectSmem = 208 * 1024, kSelectMaxBlocks = 8 * kSelectSmem / 4;
+cudaError_t launch_select_pages(const SelectParams& p, int cache_kind, cudaStream_t stream);
+
+// Attention of each (query token, kv head) over its own list of pages (attention_selected.cu).
+struct SelectedParams {
+    void* out;                    // [num_rows, num_heads, head_dim]
+    int32_t out_dtype;
+    const void* q;
+    int32_t q_dtype;
+    float scale_log2;
+    const void* k;
+    const void* v;
+    const void* k_scale;
+    const void* v_scale;
+    const void* v_zero;
+    const int32_t* lists;         // [num_rows, num_kv_heads, max_pages]
+    const int32_t* counts;        // [num_rows, num_kv_heads]
+    const int32_t* cu_q;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int32_t num_rows, num_seqs, max_blocks, q_len;
+    int32_t num_heads, num_kv_heads, head_dim, num_blocks;
+    int32_t max_pages;
+    uint32_t* err;
+};
+// The list entries that a cluster of 8 CTAs holds.
+constexpr int kSelectedSmem = 180 * 1024, kSelectedMaxPages = 8 * kSelectedSmem / 8;
+cudaError_t launch_attention_selected(const SelectedParams& p, int cache_kind, cudaStream_t stream);
 
 struct GatherParams {
     void* k_out;

@@ -5,8 +5,8 @@ contiguity of the torch tensors it is given, passes their device pointers and
 the current CUDA stream to the C entry point of the same name, and raises
 ``PkvError`` with the library's message on a non-OK status.  There is no CPU
 path: if the library is not built, every call raises.  The calls that a decode
-step makes (rotary, append, balanced and scored attention, dequantising read-back)
-go through a CPython module (csrc/binding.cpp), which also checks the tensors'
+step makes (rotary, append, balanced and scored attention, dequantising read-back,
+key bounds, page selection and the attention over it) go through a CPython module (csrc/binding.cpp), which also checks the tensors'
 sizes and that they live on the current device; the others go through ctypes.
 """
 from __future__ import annotations
@@ -544,6 +544,50 @@ def pkv_sparse_worthwhile(page_counts: torch.Tensor, context_lens: torch.Tensor,
         raise ValueError("page_counts and context_lens disagree on num_seqs")
     return bool(lib().pkv_sparse_worthwhile(ctypes.c_void_p(pc.data_ptr()), ctypes.c_void_p(cl.data_ptr()),
                                             int(pc.numel()), float(min_sparsity)))
+
+
+def key_bounds(cache: Cache) -> torch.Tensor:
+    """Caller-side storage for pkv_key_bounds: [num_blocks, num_kv_heads, 2, head_dim], lo then hi, of the cache's key
+    type (k8v4: float16)."""
+    dtype = torch.float16 if cache.kind == "k8v4" else cache.k.dtype
+    shape = (cache.num_blocks, cache.num_kv_heads, 2, cache.head_dim)
+    if dtype == torch.float8_e4m3fn:
+        return torch.zeros(shape, dtype=torch.uint8, device=cache.k.device).view(dtype)
+    return torch.zeros(shape, dtype=dtype, device=cache.k.device)
+
+
+def pkv_key_bounds(bounds: torch.Tensor, cache: Cache, seqs: Seqs, cu_new_lens: Optional[torch.Tensor] = None,
+                   err_flags: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The smallest and largest key, dim by dim, of every block that holds one of each sequence's new tokens (its last
+    ones: cu_new_lens[s + 1] - cu_new_lens[s], or q_len each).  Call it after the cache write."""
+    st = (_binding or _calls()).key_bounds(bounds, cache, seqs, cu_new_lens, err_flags, stream)
+    if st:
+        _check(st)
+    return bounds
+
+
+def pkv_select_pages(page_lists: torch.Tensor, page_counts: torch.Tensor, q: torch.Tensor, bounds: torch.Tensor,
+                     cache: Cache, seqs: Seqs, cu_q_lens: Optional[torch.Tensor] = None, keep_first: int = 1,
+                     keep_last: int = 1, err_flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """For each query token and kv head, the pages that its queries' products with the bounds put first (int32
+    page_lists [num_rows, num_kv_heads, max_pages], page_counts [num_rows, num_kv_heads]); the first keep_first and
+    last keep_last visible pages always.  cu_q_lens: the sequences' rows of q, each one's last tokens (else q_len each)."""
+    st = (_binding or _calls()).select_pages(page_lists, page_counts, q, bounds, cache, seqs, cu_q_lens, keep_first,
+                                             keep_last, err_flags, stream)
+    if st:
+        _check(st)
+
+
+def pkv_paged_attention_selected(out: torch.Tensor, q: torch.Tensor, scale: float, cache: Cache, seqs: Seqs,
+                                 page_lists: torch.Tensor, page_counts: torch.Tensor,
+                                 cu_q_lens: Optional[torch.Tensor] = None, err_flags: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """Attention of each query token and kv head over its own list of pages (pkv_select_pages, or the caller's own)."""
+    st = (_binding or _calls()).paged_attention_selected(out, q, scale, cache, seqs, page_lists, page_counts, cu_q_lens,
+                                                         err_flags, stream)
+    if st:
+        _check(st)
+    return out
 
 
 def pkv_gather_kv_cache(k_out: torch.Tensor, v_out: torch.Tensor, cu_seq_lens: torch.Tensor, cache: Cache,
