@@ -559,7 +559,7 @@ pkv_status pkv_key_bounds(void *bounds, const pkv_cache *cache, const int32_t *c
  *                num_rows = num_seqs * q_len.  q_len has no limit here.
  * Rows behind cu[num_seqs] keep their lists and counts.  A token that sees nothing gets
  * an empty list.  keep_first + keep_last <= max_pages.  A sliding window is
- * PKV_ERR_UNSUPPORTED, and so is max_blocks_per_seq above 425,984.
+ * PKV_ERR_UNSUPPORTED, and so is max_blocks_per_seq above 327,680.
  */
 pkv_status pkv_select_pages(int32_t *page_lists, int32_t *page_counts, int32_t max_pages, int32_t keep_first,
                             int32_t keep_last, const void *q, pkv_dtype q_dtype, int32_t num_heads, int32_t num_rows,

@@ -308,11 +308,15 @@ struct SelectParams {
     int32_t num_rows, num_seqs, max_blocks, q_len;
     int32_t num_heads, num_kv_heads, head_dim, num_blocks;
     int32_t max_pages, keep_first, keep_last;
+    int32_t tile_rows, stride;    // rows of a tile, room for a row's scores (set by the launcher)
     uint32_t* err;
 };
-// The pages that a cluster of 8 CTAs holds scores for in shared memory.
-constexpr int kSelectSmem = 208 * 1024, kSelectMaxBlocks = 8 * kSelectSmem / 4;
+// The pages of one row that a cluster of 8 CTAs holds scores for in shared memory.
+constexpr int kSelectSmem = 180 * 1024, kSelectMaxBlocks = 8 * 160 * 1024 / 4;
 cudaError_t launch_select_pages(const SelectParams& p, int cache_kind, cudaStream_t stream);
+cudaError_t launch_select_half(const SelectParams& p, cudaStream_t stream);   // select_half.cu, and so on
+cudaError_t launch_select_i8(const SelectParams& p, cudaStream_t stream);
+cudaError_t launch_select_e4m3(const SelectParams& p, cudaStream_t stream);
 
 // Attention of each (query token, kv head) over its own list of pages (attention_selected.cu).
 struct SelectedParams {
@@ -334,11 +338,12 @@ struct SelectedParams {
     int32_t num_rows, num_seqs, max_blocks, q_len;
     int32_t num_heads, num_kv_heads, head_dim, num_blocks;
     int32_t max_pages;
+    int32_t tile_rows, entries;   // query tokens of a CTA, room for its pages (set by the launcher)
     uint32_t* err;
 };
 // The list entries that a cluster of 8 CTAs holds.
 constexpr int kSelectedSmem = 180 * 1024, kSelectedMaxPages = 8 * kSelectedSmem / 8;
-cudaError_t launch_attention_selected(const SelectedParams& p, int cache_kind, cudaStream_t stream);
+cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, cudaStream_t stream);
 
 struct GatherParams {
     void* k_out;

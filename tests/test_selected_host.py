@@ -65,7 +65,7 @@ SHARED = [dict(kind=-1), dict(q_dtype=0), dict(q_dtype=2), dict(heads=24), dict(
 
 
 @pytest.mark.parametrize("change", SHARED + [dict(first=-1), dict(last=-1), dict(first=4), dict(pages=2), dict(bounds=None),
-                                             dict(first=2 ** 31 - 1, last=2 ** 31 - 1), dict(bounds=0x90004), dict(max_blocks=425985)])
+                                             dict(first=2 ** 31 - 1, last=2 ** 31 - 1), dict(bounds=0x90004), dict(max_blocks=327681)])
 def test_selection_refusals(ops, change):
     refused(ops, call_select(ops, **change))
 
