@@ -576,7 +576,7 @@ pkv_status pkv_select_pages(int32_t *page_lists, int32_t *page_counts, int32_t m
  *   cu_q_lens, num_rows  as for pkv_select_pages.
  * Rows behind cu[num_seqs] keep their outputs; a row without a listed page gets zeros.
  * No workspace.  K and V of tokens that a row does not see reach no output of it,
- * whatever they hold.  max_pages above 184,320 and a sliding window are
+ * whatever they hold.  max_pages above 131,072 and a sliding window are
  * PKV_ERR_UNSUPPORTED.
  */
 pkv_status pkv_paged_attention_selected(void *out, pkv_dtype out_dtype, const void *q, pkv_dtype q_dtype,

@@ -924,7 +924,9 @@ pkv_status pkv_paged_attention_selected(void* out, pkv_dtype out_dtype, const vo
     p.num_blocks = cache->num_blocks;
     p.max_pages = max_pages;
     p.err = err_flags;
-    return cuda_result(pkv::launch_attention_selected(p, cache->kind, reinterpret_cast<cudaStream_t>(stream)),
+    CUtensorMap km, vm;
+    if ((st = cache_maps(cache, &km, &vm, true)) != PKV_OK) return st;
+    return cuda_result(pkv::launch_attention_selected(p, cache->kind, km, vm, reinterpret_cast<cudaStream_t>(stream)),
                        "selected attention launch");
 }
 

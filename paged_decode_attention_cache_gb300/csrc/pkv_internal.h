@@ -341,9 +341,14 @@ struct SelectedParams {
     int32_t tile_rows, entries;   // query tokens of a CTA, room for its pages (set by the launcher)
     uint32_t* err;
 };
-// The list entries that a cluster of 8 CTAs holds.
-constexpr int kSelectedSmem = 180 * 1024, kSelectedMaxPages = 8 * kSelectedSmem / 8;
-cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, cudaStream_t stream);
+// Shared memory for a CTA's list entries (8 bytes each), and what the kernel may take with them.
+constexpr int kSelectedLists = 128 * 1024, kSelectedSmem = kSelectedLists + 72 * 1024;
+constexpr int kSelectedMaxPages = 8 * kSelectedLists / 8;
+cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                      cudaStream_t stream);
+// Several query tokens to a cluster (attention_selected_rows.cu): tiles, CTAs of a cluster, bytes of a CTA's lists.
+cudaError_t launch_attention_rows(const SelectedParams& p, int cache_kind, int64_t units, int cluster, size_t lists,
+                                  const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 
 struct GatherParams {
     void* k_out;

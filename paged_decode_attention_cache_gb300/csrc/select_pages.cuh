@@ -375,23 +375,18 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 
     // ---- the first tile's bounds, on their way while the queries are folded
     const int32_t* table = p.block_tables + int64_t(tile.s) * p.max_blocks + p0;
-    auto entry = [&](int i0) {   // block of page i0 + lane (lanes 0 .. 15), -1: none
-        int pb = -1;
-        if (lane < 16 && i0 + lane < np) {
-            pb = table[i0 + lane];
-            if (pb < 0 || pb >= p.num_blocks) {
-                flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
-                pb = -1;
-            }
-        }
-        return pb;
-    };
+    // block of page i0 + lane (lanes 0 .. 15); it is looked at a tile's time later, when it has come
+    auto entry = [&](int i0) { return lane < 16 && i0 + lane < np ? table[i0 + lane] : -1; };
     struct Source {               // where pages g and g + 8 of a tile come from
         const uint8_t* at[2];     // null: not a page
         float scale[2];           // 8-bit caches
     };
-    auto source = [&](int pb) {
+    auto source = [&](int pb, int i0) {
         Source f;
+        if (pb < 0 || pb >= p.num_blocks) {
+            if (lane < 16 && i0 + lane < np) flag_error(p.err, PKV_DEVERR_OOB_BLOCK);
+            pb = -1;
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int b = __shfl_sync(0xffffffffu, pb, g + 8 * r);
@@ -410,7 +405,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
                 x[c][part][r] = f.at[r] ? __ldg(reinterpret_cast<const uint4*>(f.at[r] + part * D * Math::E + 64 * c))
                                         : make_uint4(0u, 0u, 0u, 0u);
     };
-    Source now = source(entry(warp * 16));
+    Source now = source(entry(warp * 16), warp * 16);
     if constexpr (NT == 1)   // 16 rows: the registers are needed for folding
 #pragma unroll
         for (int c = 0; c < Math::NKC; ++c) load(now, c);
@@ -518,7 +513,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) am[mt][0] = am[mt][1] = 0.f;
         for (int i0 = warp * 16; i0 < np; i0 += kWarps * 16) {
-            const Source then = source(next);
+            const Source then = source(next, i0 + kWarps * 16);
             next = entry(i0 + 2 * kWarps * 16);
             // Four k steps to a chain of MMAs, and the chains' sums added in fp32: a chain's error is then 2^-18 of its own
             // terms'.  A chunk's registers take the next tile's as soon as its MMAs have read them.

@@ -360,6 +360,30 @@ def test_unlisted_pages_are_not_read():
     assert not got[1, :2].any()
 
 
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_what_one_token_lists_reaches_no_other(kind, d, value):
+    # neighbouring tokens share a pass over the union of their lists; an infinity or NaN in the V of a page that one of them
+    # lists, or of a token that only the later ones see, reaches their rows alone
+    w = ref.World(kind, [200, 100], 2, d, seed=21)
+    q_lens = [5, 3]
+    q = queries(w, 8, 8)
+    lists = [[[0, 3, 5], [12]], [[3, 5, 12], [1, 12]], [[2, 3], [2]], [[3, 11, 12], [12]], [[7, 12], [0, 12]],
+             [[6], [6]], [[1, 6], [0, 6]], [[6], [3]]]
+    w.cache.v[int(w.tables[0, 5]), 3, 0] = value           # sequence 0, kv head 0: tokens 0 and 1 list page 5
+    w.cache.v[int(w.tables[0, 2]), 1, 1, 7] = value        # kv head 1, one dim: token 2
+    w.cache.v[int(w.tables[0, 12]), 198 % 16] = value      # position 198, seen by the last two tokens
+    w.cache.v[int(w.tables[1, 6]), 99 % 16, 1] = value     # the last position of sequence 1
+    w.v64 = w.cache.v.double()
+    want, mag, big = ref.attention(w, q, 0.2, q_lens, lists)
+    got = run_attention(w, q, q_lens, lists, 4, torch.float32, ragged=True, scale=0.2).double().cpu()
+    fine = torch.isfinite(want)
+    assert 0 < int((~fine).sum()) < fine.numel() / 2
+    assert torch.equal(torch.isfinite(got), fine)
+    tol = mag * (2.0 ** -15 + big[..., None] * 2.0 ** -18)
+    assert ((got - want).abs()[fine] <= tol[fine] + want.abs()[fine] * 2.0 ** -24).all()
+
+
 def test_bad_entries_are_skipped_and_flagged():
     w = ref.World("f16", [100, 64, 40, 600], 1, 64, seed=12)
     q = queries(w, 4, 4)

@@ -71,7 +71,7 @@ def test_selection_refusals(ops, change):
 
 
 @pytest.mark.parametrize("change", SHARED + [dict(out=None), dict(out=0xc0008), dict(out_dtype=3), dict(scale=float("nan")),
-                                             dict(pages=184321)])
+                                             dict(pages=131073)])
 def test_attention_refusals(ops, change):
     refused(ops, call_attention(ops, **change))
 
