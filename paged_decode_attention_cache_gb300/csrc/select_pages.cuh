@@ -149,6 +149,12 @@ __device__ __forceinline__ bool in_bins(const RowState& s, float x) {
     return true;
 }
 
+// x[k], x[k + 32], x[k + 64] and x[k + 96], as far as they lie in front of `end`.
+__device__ __forceinline__ void read4(const float* x, int k, int end, float (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = k + 32 * j < end ? x[k + 32 * j] : -INFINITY;
+}
+
 // Exclusive prefix sum of v over the CTA's threads; the total in `total`.
 template <int kWarps>
 __device__ __forceinline__ int block_scan(int v, int (&warps)[kWarps], int& total) {
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     const int share = ((n_max + C - 1) / C + 15) & ~15;
     const int p0 = min(rank * share, n_max), np = min(share, n_max - p0);   // this CTA's pages [p0, p0 + np)
 
-    // ---- the first tile's bounds, on their way while the queries are folded
+    // ---- where the bounds come from
     const int32_t* table = p.block_tables + int64_t(tile.s) * p.max_blocks + p0;
     // block of page i0 + lane (lanes 0 .. 15); it is looked at a tile's time later, when it has come
     auto entry = [&](int i0) { return lane < 16 && i0 + lane < np ? table[i0 + lane] : -1; };
@@ -396,21 +402,17 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         }
         return f;
     };
-    uint4 x[Math::NKC][2][2];     // chunks of lo and hi, of pages g and g + 8
+    // chunks of lo and hi, of pages g and g + 8: all of a tile's, or (16 rows, for the registers) two ahead
+    constexpr int AHEAD = NT == 1 || Math::NKC < 2 ? Math::NKC : 2;
+    uint4 x[AHEAD][2][2];
     auto load = [&](const Source& f, int c) {
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                x[c][part][r] = f.at[r] ? __ldg(reinterpret_cast<const uint4*>(f.at[r] + part * D * Math::E + 64 * c))
+                x[c % AHEAD][part][r] = f.at[r] ? __ldg(reinterpret_cast<const uint4*>(f.at[r] + part * D * Math::E + 64 * c))
                                         : make_uint4(0u, 0u, 0u, 0u);
     };
-    Source now = source(entry(warp * 16), warp * 16);
-    if constexpr (NT == 1)   // 16 rows: the registers are needed for folding
-#pragma unroll
-        for (int c = 0; c < Math::NKC; ++c) load(now, c);
-    int next = entry((warp + kWarps) * 16);
-
     // ---- the queries, folded
     if (threadIdx.x < R) {
         const int i = threadIdx.x;
@@ -428,17 +430,32 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     // a thread takes four dims of a row: item = (k step, row, lane position)
     constexpr int ITEMS = NKS * R * 4, PER = (ITEMS + kThreads - 1) / kThreads;
     float w[PER][8];   // the sums of four dims' negative parts, then of their positive parts
+    const int entry0 = entry(warp * 16);
+    uint2 qv[NT == 1 ? PER : 1][8];   // a few rows: the queries' loads go first, then the first tile's bounds, then the sums
+    auto queries = [&](int k, int h) {
+        const int item = threadIdx.x + k * kThreads, tt = item & 3, i = (item >> 2) % R, ks = (item >> 2) / R;
+        if (item >= ITEMS || i >= rows || h >= G) return make_uint2(0u, 0u);
+        return __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + ((int64_t(tile.r0) + i) * p.num_heads +
+                                                                                         int64_t(kvh) * G + h) * D + Math::dim(ks, tt)));
+    };
+    if constexpr (NT == 1)
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int h = 0; h < 8; ++h) qv[k][h] = queries(k, h);
+    Source now = source(entry0, warp * 16);
+    if constexpr (NT == 1)
+#pragma unroll
+        for (int c = 0; c < AHEAD; ++c) load(now, c);
+    int next = entry((warp + kWarps) * 16);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int item = threadIdx.x + k * kThreads, tt = item & 3, i = (item >> 2) % R, ks = (item >> 2) / R;
 #pragma unroll
         for (int d = 0; d < 8; ++d) w[k][d] = 0.f;
-        if (item >= ITEMS || i >= rows) continue;
-        const uint16_t* q = static_cast<const uint16_t*>(p.q) +
-                            ((int64_t(tile.r0) + i) * p.num_heads + int64_t(kvh) * G) * D + Math::dim(ks, tt);
-#pragma unroll 4
-        for (int h = 0; h < G; ++h) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q + int64_t(h) * D));
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            if (h >= G) break;
+            const uint2 v = NT == 1 ? qv[NT == 1 ? k : 0][h] : queries(k, h);
             float2 a, b;
             if (p.q_dtype == PKV_BF16) {
                 a = Half16<__nv_bfloat16>::unpack2(v.x);
@@ -502,7 +519,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     // ---- scores
     if constexpr (NT > 1)
 #pragma unroll
-        for (int c = 0; c < Math::NKC; ++c) load(now, c);
+        for (int c = 0; c < AHEAD; ++c) load(now, c);
     {
         float lo_[NT], hi_[NT], am[MT][2];   // of rows 4 nt + t, and 8 mt + 2 t, + 1
 #pragma unroll
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             const Source then = source(next, i0 + kWarps * 16);
             next = entry(i0 + 2 * kWarps * 16);
             // Four k steps to a chain of MMAs, and the chains' sums added in fp32: a chain's error is then 2^-18 of its own
-            // terms'.  A chunk's registers take the next tile's as soon as its MMAs have read them.
+            // terms'.  A chunk's registers take a later one as soon as its MMAs have read them.
             float sum[NT][2], mag[MT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
@@ -533,8 +550,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
                     for (int j = j0; j < j0 + 2; ++j) {
                         const int ks = c * Math::SPC + j;
                         uint32_t a[2][4];
-                        Math::operand(x[c][0], j, a[0]);
-                        Math::operand(x[c][1], j, a[1]);
+                        Math::operand(x[c % AHEAD][0], j, a[0]);
+                        Math::operand(x[c % AHEAD][1], j, a[1]);
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -557,7 +574,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
                         sum[nt][1] += acc[nt][2] + acc[nt][3];
                     }
                 }
-                load(then, c);
+                if (c + AHEAD < Math::NKC) load(now, c + AHEAD);
+                else load(then, c + AHEAD - Math::NKC);
             }
             const float scale[2] = {now.scale[0], now.scale[1]};
             const bool ok[2] = {now.at[0] != nullptr, now.at[1] != nullptr};
@@ -662,13 +680,17 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             decided(s, l0, l1);
             const float lo = s.lo[level], inv = s.inv[level];
             const float* x = scores + i * p.stride;
-            if (level == 0) {
-#pragma unroll 4
-                for (int k = l0 + lane; k < l1; k += 32) atomicAdd(&sh.hist[i][bin_of(x[k], lo, inv, NB)], 1u);
-            } else {
+            if (level == 0)
+                for (int k0 = l0; k0 < l1; k0 += 128) {
+                    float v[4];
+                    read4(x, k0 + lane, l1, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (k0 + 32 * j + lane < l1) atomicAdd(&sh.hist[i][bin_of(v[j], lo, inv, NB)], 1u);
+                }
+            else
                 for (int k = l0 + lane; k < l1; k += 32)
                     if (in_bins<NB>(s, x[k])) atomicAdd(&sh.hist[i][bin_of(x[k], lo, inv, NB)], 1u);
-            }
         }
         team_sync(cl, C);
         if (CL) {
@@ -739,16 +761,19 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             decided(s, l0, l1);
             const float* x = scores + i * p.stride;
             const float above = s.above, below = s.below;
-#pragma unroll 4
-            for (int k = l0 + lane; k < l1; k += 32) {
-                const float v = x[k];
-                if (v > above) {
-                    ++c;
-                } else if (v >= below) {
-                    const int at = atomicAdd(&sh.list_n[i], 1);
-                    if (at < LT) {
-                        sh.list_page[i][at] = p0 + k;
-                        sh.list_score[i][at] = v;
+            for (int k0 = l0; k0 < l1; k0 += 128) {
+                float v[4];
+                read4(x, k0 + lane, l1, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = k0 + 32 * j + lane;
+                    c += k < l1 && v[j] > above;
+                    if (k < l1 && !(v[j] > above) && v[j] >= below) {
+                        const int at = atomicAdd(&sh.list_n[i], 1);
+                        if (at < LT) {
+                            sh.list_page[i][at] = p0 + k;
+                            sh.list_score[i][at] = v[j];
+                        }
                     }
                 }
             }
@@ -889,15 +914,22 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         const float* x = scores + i * p.stride;
         const float above = s.above;
         const int c0 = p.keep_first, c1 = s.n - p.keep_last;
-#pragma unroll 4
-        for (int k0 = a0; k0 < min(a1, s.n - p0); k0 += 32) {
-            const int k = k0 + lane, page = p0 + k;
-            bool in = k < a1 && page < s.n;
-            if (in && page >= c0 && page < c1) in = !none && x[k] > above;
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            const int to = at + __popc(who & ((1u << lane) - 1u));
-            if (in && to < p.max_pages) list[to] = page;
-            at += __popc(who);
+        const int end = min(a1, s.n - p0);
+        for (int k0 = a0; k0 < end; k0 += 128) {
+            float v[4];
+            read4(x, k0 + lane, end, v);
+            uint32_t who[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = k0 + 32 * j + lane, page = p0 + k;
+                who[j] = __ballot_sync(0xffffffffu, k < end && (page < c0 || page >= c1 || (!none && v[j] > above)));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int to = at + __popc(who[j] & ((1u << lane) - 1u));
+                if ((who[j] >> lane & 1u) && to < p.max_pages) list[to] = p0 + k0 + 32 * j + lane;
+                at += __popc(who[j]);
+            }
         }
     }
 
