@@ -31,6 +31,7 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    if (C > 1) cluster_arrive();   // waited for before anything is sent to another CTA
     if (threadIdx.x < COLS) q_most[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSelWarps * STAGES; ++i) {
@@ -45,19 +46,30 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
     grid_dep_launch();
     const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
     const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, 1, int(blockIdx.x / C), lane);
-    if (tile.s < 0) return;   // no row: the same in every CTA of the cluster
+    if (tile.s < 0) {   // no row: the same in every CTA of the cluster
+        if (C > 1) cluster_wait();
+        return;
+    }
+    Queries<Math, COLS, D> queries;
+    queries.load(p, tile.r0, G, kvh, G);
     const SelectedTile mine(p, tile, kvh);
     if (mine.over() && rank == 0 && kvh == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
     const int vis = mine.visible(0);
 
     // ---- the list: each entry in range and above the one before it, with a block, or the slow way
     const int32_t* list = mine.list(0);
+    // the first entries come with the count, not after it
+    int e = int(threadIdx.x) < p.max_pages ? list[threadIdx.x] : -1;
+    int before = threadIdx.x > 0 && int(threadIdx.x) < p.max_pages ? list[threadIdx.x - 1] : -1;
     const int count = mine.count(0), pages = mine.pages(0);
     const int i0 = int(int64_t(count) * rank / C), i1 = int(int64_t(count) * (rank + 1) / C);
     int n = i1 - i0;
     bool rising = true, whole = true;
     for (int i = threadIdx.x; i < count; i += kSelThreads) {
-        const int e = list[i], before = i ? list[i - 1] : -1;
+        if (i >= kSelThreads) {
+            e = list[i];
+            before = list[i - 1];
+        }
         rising &= e > before && e < pages;
         if (i >= i0 && i < i1) {
             const int b = e >= 0 && e < pages ? mine.block(e) : -1;
@@ -86,7 +98,7 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
     Ring<Math, false> ring{p, &k_map, &v_map, entry, n, kvh, warp, lane, smem + warp * RING, sides + warp * STAGES * Math::SIDE,
                            k_full + warp * STAGES, v_full + warp * STAGES, 0, 0, 0u, 0u};
     ring.begin();
-    load_queries<Math, COLS, D>(p, tile.r0, G, kvh, G, Q, q_most);
+    queries.store(p, Q, q_most);
     __syncthreads();
     uint2 q[NKS];
 #pragma unroll
@@ -222,7 +234,8 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
             }
         }
     }
-    merge_and_store<COLS, D>(p, cl, part, reinterpret_cast<float*>(smem), RING / 4, tile.r0, G, kvh, G);
+    merge_and_store<COLS, D>(p, cl, part, reinterpret_cast<float*>(smem), RING / 4,
+                             reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(entry) + p.list_bytes), tile.r0, G, kvh, G);
 }
 
 // The kernel may take kSelectedSmem of dynamic shared memory: said once per kernel and device.
@@ -239,7 +252,7 @@ cudaError_t launch_one(const SelectedParams& p, int64_t units, int cluster, size
     }));
     if (e != cudaSuccess) return e;
     return launch_cluster_kernel(attention_selected_kernel<KIND, D>, dim3(unsigned(units * cluster), p.num_kv_heads), dim3(kSelThreads),
-                                 unsigned(cluster), ring_bytes<PageMath<KIND, D>>() + lists, st, km, vm, p);
+                                 unsigned(cluster), ring_bytes<PageMath<KIND, D>>() + lists + (cluster > 1 ? exchange_bytes<8, D>() : 0), st, km, vm, p);
 }
 
 template <int KIND>
@@ -260,7 +273,8 @@ cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CU
     size_t lists = 0;
     auto size = [&] {   // the CTA's entries, and a byte for each page where rows share them
         p.entries = int((most + C - 1) / C);
-        lists = size_t(p.entries) * 8 + (p.tile_rows > 1 ? (size_t(p.max_blocks) + 3) / 4 * 4 : 0);
+        lists = (size_t(p.entries) * 8 + (p.tile_rows > 1 ? (size_t(p.max_blocks) + 3) / 4 * 4 : 0) + 15) / 16 * 16;
+        p.list_bytes = int(lists);
         return lists <= kSelectedLists;
     };
     auto tiles = [&](int rows) {
@@ -269,7 +283,7 @@ cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CU
         most = int64_t(rows) * p.max_pages;
         if (rows > 1 && most > p.max_blocks) most = p.max_blocks;
         // as many clusters as run at once
-        const int64_t room = 152 * sel_ctas(p.head_dim, rows > 1);
+        const int64_t room = 152 * (rows > 1 ? 2 : sel_ctas(p.head_dim, false));
         C = 1;
         while (C < kSelCluster && units * p.num_kv_heads * C * 2 <= room && most >= 2 * C * 2 * kSelWarps) C *= 2;
         while (!size() && C < kSelCluster) C *= 2;

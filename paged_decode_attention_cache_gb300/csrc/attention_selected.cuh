@@ -298,14 +298,24 @@ struct Ring {
     }
 };
 
+// The cluster's barrier in two halves, by all its threads.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // What a CTA's warps leave to merge, COLS query columns each: sums o in the warps' rings, [COLS][D + 4] (padded against
 // bank conflicts), running maxima (base 2) and sums of weights here.
 template <int COLS>
 struct Partials {
     float m[kSelWarps][COLS], l[kSelWarps][COLS];
-    float mine_m[COLS], mine_l[COLS];                   // the CTA's
     float weight[kSelCluster][COLS], total[COLS];       // of the merges
+    float from_m[kSelCluster][COLS], from_l[kSelCluster][COLS];   // the cluster's CTAs'
 };
+
+// Room for the other CTAs' sums of a CTA's share of the outputs (clusters only).
+template <int COLS, int D>
+constexpr size_t exchange_bytes() {
+    return size_t(COLS * D / 4 + kSelCluster) * 16;
+}
 
 // A column's weight for one of n partials, by n neighbouring threads (n a power of two): the weighted sum L, the maximum M.
 __device__ __forceinline__ float weigh(int n, float m, float l, float& L, float& M) {
@@ -318,20 +328,27 @@ __device__ __forceinline__ float weigh(int n, float m, float l, float& L, float&
 }
 
 // The warps' partials, then the cluster's CTAs', into the outputs of rows r0 .. : column = row * G + head.  The weights of all
-// partials first (a lane each), then the sums.
+// partials first (a lane each), then the sums.  In a cluster each CTA sends every other its sums of that one's share of the
+// outputs (`exchange`): one barrier, and nothing is read from another CTA.
 template <int COLS, int D>
 __device__ __forceinline__ void merge_and_store(const SelectedParams& p, cg::cluster_group& cl, Partials<COLS>& part, float* o,
-                                                int warp_stride, int r0, int cols, int kvh, int G) {
+                                                int warp_stride, float4* exchange, int r0, int cols, int kvh, int G) {
     constexpr int OW = D + 4;
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    const int items = cols * (D / 4), share = (items + C - 1) / C;   // four dims of a column; a CTA's share of them
     __syncthreads();
+    if (C > 1) cluster_wait();   // the others have begun
     if (threadIdx.x < kSelWarps * COLS) {
         const int col = threadIdx.x / kSelWarps, k = threadIdx.x % kSelWarps;
         float L, M;
         part.weight[k][col] = weigh(kSelWarps, part.m[k][col], part.l[k][col], L, M);
-        if (k == 0) {
-            part.total[col] = part.mine_l[col] = L;
-            part.mine_m[col] = M;
+        if (C == 1) {
+            if (k == 0) part.total[col] = L;
+        } else {
+            for (int r = k; r < C; r += kSelWarps) {
+                *cl.map_shared_rank(&part.from_m[rank][col], r) = M;
+                *cl.map_shared_rank(&part.from_l[rank][col], r) = L;
+            }
         }
     }
     __syncthreads();
@@ -348,38 +365,34 @@ __device__ __forceinline__ void merge_and_store(const SelectedParams& p, cg::clu
         sum.z += w * v.z;
         sum.w += w * v.w;
     };
-    const int items = cols * (D / 4);
     for (int i = threadIdx.x; i < items; i += kSelThreads) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kSelWarps; ++k)
             add(sum, part.weight[k][col], *reinterpret_cast<const float4*>(o + k * warp_stride + col * OW + d));
-        if (C == 1) store(i, sum);
-        else *reinterpret_cast<float4*>(o + col * OW + d) = sum;   // the CTA's, in the first warp's place
+        if (C == 1) {
+            store(i, sum);
+        } else {
+            const int r = i / share;
+            cl.map_shared_rank(exchange, r)[rank * share + (i - r * share)] = sum;
+        }
     }
     if (C == 1) return;
-    cl.sync();
+    cl.sync();   // what was sent has come
     for (int i = threadIdx.x; i < kSelCluster * COLS; i += kSelThreads) {
         const int col = i / kSelCluster, k = i % kSelCluster;
-        const float m = *cl.map_shared_rank(&part.mine_m[col], k < C ? k : 0);
-        const float l = k < C ? *cl.map_shared_rank(&part.mine_l[col], k) : 0.f;
         float L, M;
-        part.weight[k][col] = weigh(kSelCluster, m, l, L, M);
+        part.weight[k][col] = weigh(kSelCluster, k < C ? part.from_m[k][col] : 0.f, k < C ? part.from_l[k][col] : 0.f, L, M);
         if (k == 0) part.total[col] = L;
     }
     __syncthreads();
-    for (int i = rank * kSelThreads + threadIdx.x; i < items; i += C * kSelThreads) {
-        const int col = i / (D / 4), d = (i % (D / 4)) * 4;
-        float4 v[kSelCluster], sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kSelCluster; ++k)
-            v[k] = *reinterpret_cast<const float4*>(cl.map_shared_rank(o, k < C ? k : 0) + col * OW + d);
-#pragma unroll
-        for (int k = 0; k < kSelCluster; ++k) add(sum, part.weight[k][col], v[k]);
+    for (int j = threadIdx.x; j < share && rank * share + j < items; j += kSelThreads) {
+        const int i = rank * share + j;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < C; ++k) add(sum, part.weight[k][i / (D / 4)], exchange[k * share + j]);
         store(i, sum);
     }
-    cl.sync();   // no CTA leaves while another reads its partial
 }
 
 // What the query tokens of a CTA see and list.
@@ -451,46 +464,52 @@ struct SelectedTile {
 // brings their column's largest magnitude to [256, 512); q_most [columns] holds the exponents (cleared before).
 // With two column tiles their words lie side by side: Q[2 * (k step * 32 + lane)], the MMA's A operand {tile 0, 1 word 0; 0, 1 word 1}.
 template <class Math, int COLS, int D>
-__device__ __forceinline__ void load_queries(const SelectedParams& p, int r0, int cols, int kvh, int G, uint2* Q, uint32_t* q_most) {
-    constexpr int NKS = D / 16, PER = COLS / 8 * NKS * 32 / kSelThreads;
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-    auto item_col = [&](int k) { return 8 * (((threadIdx.x + k * kSelThreads) >> 5) / NKS) + g; };
+struct Queries {
+    static constexpr int NKS = D / 16, PER = COLS / 8 * NKS * 32 / kSelThreads;
     uint2 x[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int kk = ((threadIdx.x + k * kSelThreads) >> 5) % NKS, col = item_col(k);
-        x[k] = make_uint2(0u, 0u);
-        if (col >= cols) continue;
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((int64_t(r0) + col / G) * p.num_heads + int64_t(kvh) * G + col % G) * D;
-        x[k].x = __ldg(reinterpret_cast<const uint32_t*>(src + Math::q_dim(kk, 0, t)));
-        x[k].y = __ldg(reinterpret_cast<const uint32_t*>(src + Math::q_dim(kk, 1, t)));
+    static __device__ __forceinline__ int col(int k) {
+        return 8 * (((threadIdx.x + k * kSelThreads) >> 5) / NKS) + (int(threadIdx.x & 31) >> 2);
     }
-    if (!Math::kHalf && p.q_dtype == PKV_BF16) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-            atomicMax(&q_most[item_col(k)], max(max((x[k].x >> 7) & 0xffu, (x[k].x >> 23) & 0xffu),
-                                                max((x[k].y >> 7) & 0xffu, (x[k].y >> 23) & 0xffu)));
-        __syncthreads();
+    // the loads, which depend on nothing but the rows
+    __device__ __forceinline__ void load(const SelectedParams& p, int r0, int cols, int kvh, int G) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const float up = __uint_as_float((262u - min(max(q_most[item_col(k)], 16u), 254u)) << 23);
-            const float2 a = Half16<__nv_bfloat16>::unpack2(x[k].x), b = Half16<__nv_bfloat16>::unpack2(x[k].y);
-            x[k] = make_uint2(pack2<false>(a.x * up, a.y * up), pack2<false>(b.x * up, b.y * up));
+            const int kk = ((threadIdx.x + k * kSelThreads) >> 5) % NKS, c = col(k), t = threadIdx.x & 3;
+            x[k] = make_uint2(0u, 0u);
+            if (c >= cols) continue;
+            const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((int64_t(r0) + c / G) * p.num_heads + int64_t(kvh) * G + c % G) * D;
+            x[k].x = __ldg(reinterpret_cast<const uint32_t*>(src + Math::q_dim(kk, 0, t)));
+            x[k].y = __ldg(reinterpret_cast<const uint32_t*>(src + Math::q_dim(kk, 1, t)));
         }
     }
+    __device__ __forceinline__ void store(const SelectedParams& p, uint2* Q, uint32_t* q_most) {
+        if (!Math::kHalf && p.q_dtype == PKV_BF16) {
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int item = threadIdx.x + k * kSelThreads;
-        if constexpr (COLS == 8) {
-            Q[item] = x[k];
-        } else {
-            const int nt = item / (NKS * 32);
-            uint32_t* to = reinterpret_cast<uint32_t*>(Q) + 4 * (item - nt * NKS * 32) + nt;
-            to[0] = x[k].x;
-            to[2] = x[k].y;
+            for (int k = 0; k < PER; ++k)
+                atomicMax(&q_most[col(k)], max(max((x[k].x >> 7) & 0xffu, (x[k].x >> 23) & 0xffu),
+                                               max((x[k].y >> 7) & 0xffu, (x[k].y >> 23) & 0xffu)));
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const float up = __uint_as_float((262u - min(max(q_most[col(k)], 16u), 254u)) << 23);
+                const float2 a = Half16<__nv_bfloat16>::unpack2(x[k].x), b = Half16<__nv_bfloat16>::unpack2(x[k].y);
+                x[k] = make_uint2(pack2<false>(a.x * up, a.y * up), pack2<false>(b.x * up, b.y * up));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int item = threadIdx.x + k * kSelThreads;
+            if constexpr (COLS == 8) {
+                Q[item] = x[k];
+            } else {
+                const int nt = item / (NKS * 32);
+                uint32_t* to = reinterpret_cast<uint32_t*>(Q) + 4 * (item - nt * NKS * 32) + nt;
+                to[0] = x[k].x;
+                to[2] = x[k].y;
+            }
         }
     }
-}
+};
 // what turns a column's products into base-2 scores
 template <class Math>
 __device__ __forceinline__ float column_scale(const SelectedParams& p, const uint32_t* q_most, int col) {

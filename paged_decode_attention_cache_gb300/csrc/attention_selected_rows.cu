@@ -32,6 +32,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    if (C > 1) cluster_arrive();   // waited for before anything is sent to another CTA
     if (threadIdx.x < COLS) q_most[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSelWarps * STAGES; ++i) {
@@ -46,7 +47,12 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     grid_dep_launch();
     const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
     const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, p.tile_rows, int(blockIdx.x / C), lane);
-    if (tile.s < 0) return;   // no row: the same in every CTA of the cluster
+    if (tile.s < 0) {   // no row: the same in every CTA of the cluster
+        if (C > 1) cluster_wait();
+        return;
+    }
+    Queries<Math, COLS, D> queries;
+    queries.load(p, tile.r0, tile.rows * G, kvh, G);
     const SelectedTile mine(p, tile, kvh);
     if (mine.over() && rank == 0 && kvh == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
     const int rows = tile.rows, cols = rows * G;
@@ -60,12 +66,20 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     bool rising = true;
     for (int row = warp; row < rows; row += kSelWarps) {
         const int32_t* list = mine.list(row);
+        int e = lane < p.max_pages ? list[lane] : -1;   // comes with the count, not after it
         const int count = mine.count(row), pages = mine.pages(row);
-        for (int i = lane; i < count; i += 32) {
-            const int e = list[i], before = i ? list[i - 1] : -1;
+        int last = -1;   // the entry before this 32
+        for (int i = lane; i - lane < count; i += 32) {
+            const int ahead = i + 32 < p.max_pages ? list[i + 32] : -1;
+            int before = __shfl_up_sync(0xffffffffu, e, 1);
+            if (lane == 0) before = last;
             const bool ok = e > before && e < pages;
-            rising &= ok;
-            if (ok) atomicOr(bytes + (e >> 2), 1u << (8 * (e & 3) + row));
+            if (i < count) {
+                rising &= ok;
+                if (ok) atomicOr(bytes + (e >> 2), 1u << (8 * (e & 3) + row));
+            }
+            last = __shfl_sync(0xffffffffu, e, 31);
+            e = ahead;
         }
     }
     if (__syncthreads_or(!rising)) {
@@ -130,7 +144,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     Ring<Math, true> ring{p, &k_map, &v_map, entry, n, kvh, warp, lane, smem + warp * RING, sides + warp * STAGES * Math::SIDE,
                           k_full + warp * STAGES, v_full + warp * STAGES, 0, 0, 0u, 0u};
     ring.begin();
-    load_queries<Math, COLS, D>(p, tile.r0, cols, kvh, G, Q, q_most);
+    queries.store(p, Q, q_most);
     __syncthreads();
     float krow[2];       // what turns the products of rows g, g + 8 into base-2 scores
     uint32_t bit[2];     // their query token, as a bit (0: no row)
@@ -346,7 +360,8 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
                     for (int c = 0; c < 2; ++c) to[Math::dim(mt, 2 * t + c) + j * Math::kNext] = o[mt][j][2 * r + c] * back;
         }
     }
-    merge_and_store<COLS, D>(p, cl, part, reinterpret_cast<float*>(smem), RING / 4, tile.r0, cols, kvh, G);
+    merge_and_store<COLS, D>(p, cl, part, reinterpret_cast<float*>(smem), RING / 4,
+                             reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(entry) + p.list_bytes), tile.r0, cols, kvh, G);
 }
 
 // The kernel may take kSelectedSmem of dynamic shared memory: said once per kernel and device.
@@ -363,7 +378,7 @@ cudaError_t launch_rows(const SelectedParams& p, int64_t units, int cluster, siz
     }));
     if (e != cudaSuccess) return e;
     return launch_cluster_kernel(attention_rows_kernel<KIND, D>, dim3(unsigned(units * cluster), p.num_kv_heads), dim3(kSelThreads),
-                                 unsigned(cluster), ring_bytes<PageMath<KIND, D>>() + lists, st, km, vm, p);
+                                 unsigned(cluster), ring_bytes<PageMath<KIND, D>>() + lists + (cluster > 1 ? exchange_bytes<16, D>() : 0), st, km, vm, p);
 }
 
 template <int KIND>

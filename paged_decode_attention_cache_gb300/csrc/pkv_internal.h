@@ -338,11 +338,11 @@ struct SelectedParams {
     int32_t num_rows, num_seqs, max_blocks, q_len;
     int32_t num_heads, num_kv_heads, head_dim, num_blocks;
     int32_t max_pages;
-    int32_t tile_rows, entries;   // query tokens of a CTA, room for its pages (set by the launcher)
+    int32_t tile_rows, entries, list_bytes;   // query tokens of a CTA, room for its pages, for its lists (set by the launcher)
     uint32_t* err;
 };
 // Shared memory for a CTA's list entries (8 bytes each), and what the kernel may take with them.
-constexpr int kSelectedLists = 128 * 1024, kSelectedSmem = kSelectedLists + 72 * 1024;
+constexpr int kSelectedLists = 128 * 1024, kSelectedSmem = kSelectedLists + 80 * 1024;
 constexpr int kSelectedMaxPages = 8 * kSelectedLists / 8;
 cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                       cudaStream_t stream);
