@@ -496,7 +496,11 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         }
         float most[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) most[d] = fmaxf(fabsf(w[k][d]), fabsf(w[k][4 + d])) * up;
+        for (int d = 0; d < 4; ++d) {
+            most[d] = fmaxf(fabsf(w[k][d]), fabsf(w[k][4 + d])) * up;
+            // fp16's second term is off by 2^-25 at most, however small the weight: 2^-18 of the magnitude counted for it
+            if (!Math::kBf && sh.wmax[i] > 0) most[d] = most[d] < 0.0078125f ? 0.0078125f : most[d];   // a NaN stays
+        }
         WM[(ks * MT + i / 8) * 32 + (i % 8) * 4 + tt] = make_uint2(pack2<Math::kBf>(most[0], most[1]), pack2<Math::kBf>(most[2], most[3]));
         if (R < 8) WM[ks * MT * 32 + (i + 4) * 4 + tt] = make_uint2(0u, 0u);   // columns of no row
 #pragma unroll

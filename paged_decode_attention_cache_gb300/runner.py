@@ -30,13 +30,16 @@ def cascade_plan_for(w: Workload, min_members: int = 2, min_shared_blocks: int =
 class DecodeStep:
     def __init__(self, w: Workload, device: str = "cuda", partition_size: Optional[int] = None,
                  out_dtype: Optional[torch.dtype] = None, schedule: Optional[str] = None,
-                 cascade_min_members: int = 2, cascade_min_shared_blocks: int = 8):
+                 cascade_min_members: int = 2, cascade_min_shared_blocks: int = 8, max_pages: int = 64,
+                 keep_first: int = 1, keep_last: int = 1):
         """schedule: "single" (one CTA per sequence and kv head), "split"
         (fixed partitions of partition_size tokens + LSE reduce) or "balanced"
         (equal block ranges per SM, combine fused) or "fused" (balanced, with the
         step's cache write in the same launch) or "cascade" (shared whole-page
         prefixes read once per group, balanced) or "sparse" (only the workload's
-        listed pages, balanced); by default split when the workload names a
+        listed pages, balanced) or "selected" (the step keeps the bounds of the
+        pages' keys, and each query token and kv head attends the max_pages pages
+        that they put first); by default split when the workload names a
         partition size, else single."""
         self.w = w
         self.device = device
@@ -44,7 +47,7 @@ class DecodeStep:
         self.partition_size = w.partition_size if partition_size is None else partition_size
         if schedule is None:
             schedule = "split" if self.partition_size > 0 else "single"
-        if schedule not in ("single", "split", "balanced", "fused", "cascade", "sparse"):
+        if schedule not in ("single", "split", "balanced", "fused", "cascade", "sparse", "selected"):
             raise ValueError(schedule)
         if schedule != "split":
             self.partition_size = 0
@@ -78,6 +81,14 @@ class DecodeStep:
             self.ws = ops.split_workspace(w.num_rows, w.num_heads, w.head_dim, nparts, device=dev)
         elif schedule in ("balanced", "fused"):
             self.bal_ws = ops.balanced_workspace(w.num_seqs, w.num_kv_heads, w.head_dim, device=dev)
+        elif schedule == "selected":
+            if w.sliding_window:
+                raise ValueError("selected pages are for workloads without a sliding window")
+            self.keep = {"keep_first": keep_first, "keep_last": keep_last}
+            self.key_bounds = ops.key_bounds(self.cache)
+            ops.pkv_key_bounds(self.key_bounds, self.cache, self.seqs, w.cu_seq_lens().to(dev), self.err)
+            self.page_lists = torch.empty((w.num_rows, w.num_kv_heads, max_pages), dtype=torch.int32, device=dev)
+            self.page_counts = torch.empty((w.num_rows, w.num_kv_heads), dtype=torch.int32, device=dev)
         elif schedule == "sparse":
             if w.page_lists is None:
                 raise ValueError("the workload lists no pages")
@@ -106,6 +117,8 @@ class DecodeStep:
             ops.pkv_quantize_kv(self.cache, self.k_new, self.v_new, self.slot_new, self.err, stream)
         else:
             ops.pkv_reshape_and_cache(self.cache, self.k_new, self.v_new, self.slot_new, self.err, stream)
+        if self.schedule == "selected":
+            ops.pkv_key_bounds(self.key_bounds, self.cache, self.seqs, None, self.err, stream)
 
     def attend_phase1(self, stream=None):
         """The dominant kernel: single-pass / balanced attention, or split-KV phase 1."""
@@ -119,6 +132,11 @@ class DecodeStep:
         elif self.schedule == "sparse":
             ops.pkv_paged_attention_sparse(self.out, self.q, self.w.scale, self.cache, self.seqs, self.page_lists,
                                            self.page_counts, self.sparse_ws, self.err, stream)
+        elif self.schedule == "selected":
+            ops.pkv_select_pages(self.page_lists, self.page_counts, self.q, self.key_bounds, self.cache, self.seqs, None,
+                                 **self.keep, err_flags=self.err, stream=stream)
+            ops.pkv_paged_attention_selected(self.out, self.q, self.w.scale, self.cache, self.seqs, self.page_lists,
+                                             self.page_counts, None, self.err, stream)
         elif self.schedule == "cascade":
             ops.pkv_paged_attention_cascade(self.out, self.q, self.w.scale, self.cache, self.seqs, self.members,
                                             self.item_blocks, self.cascade_ws, self.err, stream)
@@ -146,6 +164,8 @@ class DecodeStep:
             return wr + 3   # set-up, attention, reduce
         if self.schedule == "sparse":
             return wr + 2   # set-up, attention
+        if self.schedule == "selected":
+            return 2 * wr + 2   # write and bounds, selection, attention
         return wr + 1 + int(self.split)
 
     def gather(self, stream=None):

@@ -191,6 +191,23 @@ def test_equal_scores_go_to_the_lower_page(ctx, same):
         check_lists(lists, counts, ref.select(w, q, b, [1], pages, 1, 1), pages)
 
 
+def test_a_query_dim_that_outweighs_the_others():
+    # its keys are zero everywhere: the scores lie 2^25 below the largest weight, where the other weights' fp16 terms run out of
+    # bits, and differ by less than those are worth
+    w = ref.World("f16", [2000], 1, 64, seed=22)
+    b = torch.zeros_like(full_bounds(w))
+    q = torch.zeros(1, 8, 64).half()
+    q[:, :, 3] = 2.0 ** 14
+    q[:, :, 4:] = grid((1, 8, 60), 2.0 ** -22, 2.0 ** -12, 23).half()
+    base = grid((60,), 2.0 ** -6, 4.0, 24)
+    for p in range(125):
+        x = torch.cat([torch.zeros(4), base + grid((60,), 2.0 ** -6, 0.125, 25 + p)]).half()
+        b[int(w.tables[0, p]), 0] = torch.stack([x, x])
+    for pages in (3, 40):
+        lists, counts = run_select(w, q, b.cuda(), [1], pages, 1, 0)
+        check_lists(lists, counts, ref.select(w, q, b, [1], pages, 1, 0), pages)
+
+
 @pytest.mark.parametrize("pages", [3, 30, 64])
 def test_scores_closer_than_fp32_tells(pages):
     # every page the same but for one dim, whose 2^-14 steps leave scores of about 2^11 apart by less than fp32's error
@@ -439,6 +456,37 @@ def test_scales_of_every_size(kind):
 
 
 # ---------------------------------------------------------------- the three together
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "k8v4"])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_a_decode_step_that_selects(kind, q_len):
+    """DecodeStep's schedule: with room for every page the oracle's whole attention, else that of the selected ones."""
+    from paged_decode_attention_cache_gb300 import workloads as W
+    from paged_decode_attention_cache_gb300.runner import DecodeStep
+    from tests.helpers import oracle_attention
+    w = W.build(name="t", seed=31, context_lens=[40, 17, 260, 129], num_heads=8, num_kv_heads=2, head_dim=64, cache=kind, q_len=q_len)
+    st = DecodeStep(w, "cuda", out_dtype=torch.float32, schedule="selected", max_pages=17)
+    st.step()
+    assert st.error_flags() == 0 and st.launches_per_step() == 4
+    assert np.abs(st.out.double().cpu().numpy() - oracle_attention(w, threads=8)).max() <= (2e-2 if kind == "k8v4" else 2e-3)
+    few = DecodeStep(w, "cuda", out_dtype=torch.float32, schedule="selected", max_pages=5, keep_first=0, keep_last=2)
+    few.step()
+    assert few.error_flags() == 0
+    n = [-(-(c - q_len + j + 1) // 16) for c in w.context_lens.tolist() for j in range(q_len)]
+    assert few.page_counts.tolist() == [[min(5, k)] * 2 for k in n]
+    for r, k in enumerate(n):
+        assert {k - 1, max(k - 2, 0)} <= set(few.page_lists[r, 0].tolist())
+    # the lists' attention by the framework's other call, where that has one list for all kv heads
+    if q_len == 1:
+        one = few.page_lists[:, :1].expand(-1, 2, -1).contiguous()
+        a, b = torch.empty_like(few.out), torch.empty_like(few.out)
+        ops.pkv_paged_attention_selected(a, few.q, w.scale, few.cache, few.seqs, one, few.page_counts, None, few.err)
+        ws = ops.sparse_workspace(w.num_seqs, 2, 64, 5)
+        ops.pkv_paged_attention_sparse(b, few.q, w.scale, few.cache, few.seqs, one[:, 0].contiguous(), few.page_counts[:, 0].contiguous(),
+                                       ws, few.err)
+        assert few.error_flags() == 0
+        assert (a - b).abs().max() <= (2e-2 if kind == "k8v4" else 2e-3)
 
 
 def test_all_pages_is_the_whole_attention():
