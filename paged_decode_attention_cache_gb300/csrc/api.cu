@@ -925,6 +925,13 @@ pkv_status pkv_paged_attention_selected(void* out, pkv_dtype out_dtype, const vo
     p.max_pages = max_pages;
     p.err = err_flags;
     CUtensorMap km, vm;
+    if (pkv::prompt_tiles(p, cache->kind)) {
+        const int64_t rows = int64_t(cache->num_blocks) * 16, row_bytes = int64_t(cache->num_kv_heads) * cache->head_dim * 2;
+        if ((st = tile_map(&km, cache->k, rows, row_bytes, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != PKV_OK) return st;
+        if ((st = tile_map(&vm, cache->v, rows, row_bytes, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != PKV_OK) return st;
+        return cuda_result(pkv::launch_attention_prompt(p, cache->kind, km, vm, reinterpret_cast<cudaStream_t>(stream)),
+                           "selected attention launch (prompt)");
+    }
     if ((st = cache_maps(cache, &km, &vm, true)) != PKV_OK) return st;
     return cuda_result(pkv::launch_attention_selected(p, cache->kind, km, vm, reinterpret_cast<cudaStream_t>(stream)),
                        "selected attention launch");

@@ -1,0 +1,506 @@
+// attention_prompt.cu -- attention over lists of pages for chunks of prompts over fp16 and
+// bf16 caches (attention_selected.cuh): 128 query rows to a CTA on tcgen05.
+//
+// 128 / g neighbouring query tokens with a kv head's g query heads are the M side of the MMAs; the
+// CTA reads the union of their lists once, 8 pages (128 tokens) at a step, and masks by row:
+//   S = Q K^T   both operands in shared memory (K-major, 128-byte swizzle), S in TMEM;
+//   softmax     a thread owns a row: no shuffles, its maximum and sum stay with it;
+//   O += P V    P from TMEM, where it takes S's place 32 columns at a time, as two 16-bit halves
+//               (hi, lo) and so two MMAs a k step; V as the cache has it (N-major); O in TMEM.
+// One thread issues the copies and the MMAs, four warps do the softmax.  256 columns of TMEM and
+// 96 KB of tiles to a CTA: two CTAs to an SM, and one's softmax runs under the other's MMAs.
+//
+// Whatever the lists have in common, the union is no larger than what smaller tiles would read
+// together, and a page costs 128 rows here what 16 rows cost mma.sync.
+#include <algorithm>
+
+#include "attention_selected.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRows = 128, kStepPages = 8, kStepTokens = kStepPages * kBS;
+constexpr int kSoftWarps = 4, kPromptThreads = (kSoftWarps + 1) * 32;
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The barrier's phase completes when this thread's MMAs so far have.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// d (+)= A B, A in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
+        "l"(b), "r"(idesc), "r"(uint32_t(add))
+        : "memory");
+}
+// d (+)= A B, A in TMEM
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
+        "l"(b), "r"(idesc), "r"(uint32_t(add))
+        : "memory");
+}
+
+#define PKV_R32(X) \
+    X(0), X(1), X(2), X(3), X(4), X(5), X(6), X(7), X(8), X(9), X(10), X(11), X(12), X(13), X(14), X(15), X(16), X(17), X(18), X(19), \
+        X(20), X(21), X(22), X(23), X(24), X(25), X(26), X(27), X(28), X(29), X(30), X(31)
+
+// 32 columns of this warp's 32 lanes of TMEM, a lane to a thread
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
+#define PKV_OUT(i) "=r"(r[i])
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : PKV_R32(PKV_OUT)
+        : "r"(at)
+        : "memory");
+#undef PKV_OUT
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+#define PKV_IN(i) "r"(r[i])
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::PKV_R32(PKV_IN),
+        "r"(at)
+        : "memory");
+#undef PKV_IN
+}
+#undef PKV_R32
+
+// Shared-memory operand with the 128-byte swizzle: address, and the strides in bytes between its 8-row (K-major) or
+// 8-k (N-major) groups and, N-major, between its 64-element groups along N.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return uint64_t((addr >> 4) & 0x3fffu) | uint64_t((lbo >> 4) & 0x3fffu) << 16 | uint64_t((sbo >> 4) & 0x3fffu) << 32 |
+           uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+// fp32 sums of 16-bit products, M = 128
+template <bool BF>
+__device__ __forceinline__ constexpr uint32_t instruction(int n, bool b_n_major) {
+    return 1u << 4 | (BF ? 1u << 7 | 1u << 10 : 0u) | (b_n_major ? 1u << 16 : 0u) | uint32_t(n / 8) << 17 | uint32_t(kRows / 16) << 24;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <bool BF, int D>
+__global__ void __launch_bounds__(kPromptThreads, 2)
+attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const SelectedParams p) {
+    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int NC = D / 64;                      // 64-dim chunks of a row
+    constexpr int CHUNK = kRows * 128;              // bytes of a chunk of 128 rows or tokens
+    constexpr int TILE = NC * CHUNK;                // Q, K, V alike
+    constexpr float kSlack = BF ? 8.f : 1.f, kPUnit = BF ? 1.f : 16384.f;   // as PageMath's
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *const sq = smem, *const sk = smem + TILE, *const sv = smem + 2 * TILE;
+    int2* const entry = reinterpret_cast<int2*>(smem + 3 * TILE);             // the union's pages: page, block
+    uint32_t* const marks = reinterpret_cast<uint32_t*>(entry + p.entries);   // [pages][mark words]: the tokens that list a page
+    __shared__ uint64_t k_full, v_full, s_done, p_done, o_done;
+    __shared__ uint32_t tmem_at;
+    __shared__ int scan[kSoftWarps + 1], kept, failed;
+    __shared__ uint32_t redo[kRows / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        mbar_init(&k_full, 1);
+        mbar_init(&v_full, 1);
+        mbar_init(&s_done, 1);
+        mbar_init(&p_done, kSoftWarps);
+        mbar_init(&o_done, 1);
+        fence_barrier_init();
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+        failed = 0;
+    }
+    if (threadIdx.x < kRows / 32) redo[threadIdx.x] = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
+    const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, p.tile_rows, int(blockIdx.x), lane);
+    if (tile.s < 0) return;
+    const SelectedTile mine(p, tile, kvh);
+    if (mine.over() && kvh == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_CAPACITY);
+    const int rows = tile.rows, MW = (p.tile_rows + 31) / 32;   // query tokens; words of a page's marks
+    const int pages = mine.pages(rows - 1);
+
+    // ---- the queries, swizzled as TMA would have them; rows of no token are zeros
+    for (int i = threadIdx.x; i < kRows * NC * 8; i += kPromptThreads) {
+        const int c = i % (NC * 8), row = i / (NC * 8);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows * G)
+            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                     ((int64_t(tile.r0) + row / G) * p.num_heads + int64_t(kvh) * G + row % G) * D) + c);
+        *reinterpret_cast<uint4*>(sq + (c >> 3) * CHUNK + row * 128 + 16 * ((c & 7) ^ (row & 7))) = x;
+    }
+    fence_proxy_async_smem();
+
+    // ---- the union of the lists, if every entry is in range and above the one before it; else the slow way
+    for (int i = threadIdx.x; i < pages * MW; i += kPromptThreads) marks[i] = 0;
+    if (warp == 0) tmem_alloc(&tmem_at, 256);
+    __syncthreads();
+    bool rising = true;
+    for (int row = warp; row < rows; row += kSoftWarps + 1) {
+        const int32_t* list = mine.list(row);
+        int e = lane < p.max_pages ? list[lane] : -1;   // comes with the count, not after it
+        const int count = mine.count(row), limit = mine.pages(row);
+        int last = -1;   // the entry before this 32
+        for (int i = lane; i - lane < count; i += 32) {
+            const int ahead = i + 32 < p.max_pages ? list[i + 32] : -1;
+            int before = __shfl_up_sync(0xffffffffu, e, 1);
+            if (lane == 0) before = last;
+            const bool ok = e > before && e < limit;
+            if (i < count) {
+                rising &= ok;
+                if (ok) atomicOr(marks + e * MW + (row >> 5), 1u << (row & 31));
+            }
+            last = __shfl_sync(0xffffffffu, e, 31);
+            e = ahead;
+        }
+    }
+    if (__syncthreads_or(!rising)) {
+        for (int i = threadIdx.x; i < pages * MW; i += kPromptThreads) marks[i] = 0;
+        __syncthreads();
+        for (int row = warp; row < rows; row += kSoftWarps + 1)
+            mine.in_order(row, lane, [&](int, bool, bool taken, int e) {
+                if (taken) atomicOr(marks + e * MW + (row >> 5), 1u << (row & 31));
+            });
+        if (threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_PAGE_LIST);
+        __syncthreads();
+    }
+    int n;
+    {
+        const int per = (pages + kPromptThreads - 1) / kPromptThreads, a = min(int(threadIdx.x) * per, pages), b = min(a + per, pages);
+        auto listed = [&](int page) {
+            uint32_t any = 0;
+            for (int w = 0; w < MW; ++w) any |= marks[page * MW + w];
+            return any != 0;
+        };
+        int c = 0;
+        for (int i = a; i < b; ++i) c += listed(i);
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        int at = incl - c;
+        n = 0;
+        for (int w = 0; w <= kSoftWarps; ++w) {
+            if (w < warp) at += scan[w];
+            n += scan[w];
+        }
+        bool whole = true;
+        for (int i = a; i < b; ++i)
+            if (listed(i)) {
+                const int block = mine.block(i);
+                whole &= block >= 0;
+                entry[at++] = make_int2(i, block);
+            }
+        if (__syncthreads_or(!whole)) {
+            if (warp == 0) {
+                const int k = mine.close_up(entry, n, lane);
+                if (lane == 0) kept = k;
+            }
+            __syncthreads();
+            n = kept;
+        }
+    }
+    const uint32_t tmem = tmem_at, tmem_s = tmem, tmem_o = tmem + 128;
+    fence_after_sync();
+    const int steps = (n + kStepPages - 1) / kStepPages;
+
+    if (warp == kSoftWarps) {
+        // ---- the copies and the MMAs, by one thread
+        if (lane == 0 && steps > 0) {
+            auto copy = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int step) {
+                const int first = step * kStepPages, k = min(kStepPages, n - first);
+                mbar_arrive_expect_tx(bar, k * kBS * D * 2);
+                for (int i = 0; i < k; ++i)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        tma_load_2d(dst + c * CHUNK + i * kBS * 128, map, kvh * D * 2 + c * 128, entry[first + i].y * kBS, bar);
+            };
+            copy(&k_map, sk, &k_full, 0);
+            copy(&v_map, sv, &v_full, 0);
+            const uint32_t qa = smem_addr(sq), ka = smem_addr(sk), va = smem_addr(sv);
+            bool came = true;
+            for (int i = 0; i < steps && came; ++i) {
+                const uint32_t parity = i & 1;
+                came = mbar_wait(&k_full, parity);
+                if (!came) break;
+                fence_after_sync();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * CHUNK + (ks & 3) * 32;
+                    mma_ss(tmem_s, operand(qa + off, 16, 1024), operand(ka + off, 16, 1024), instruction<BF>(kStepTokens, false), ks > 0);
+                }
+                mma_commit(&s_done);
+                came = mbar_wait(&s_done, parity);
+                if (!came) break;
+                if (i + 1 < steps) copy(&k_map, sk, &k_full, i + 1);
+                came = mbar_wait(&v_full, parity) && mbar_wait(&p_done, parity);
+                if (!came) break;
+                fence_after_sync();
+#pragma unroll
+                for (int ks = 0; ks < kStepTokens / 16; ++ks) {
+                    const uint32_t pa = tmem_s + 32 * (ks >> 1) + 8 * (ks & 1);   // hi; lo is 16 columns on
+                    const uint64_t b = operand(va + ks * 16 * 128, CHUNK, 1024);
+                    mma_ts(tmem_o, pa, b, instruction<BF>(D, true), i > 0 || ks > 0);
+                    mma_ts(tmem_o, pa + 16, b, instruction<BF>(D, true), true);
+                }
+                mma_commit(&o_done);
+                came = mbar_wait(&o_done, parity);
+                if (!came) break;
+                if (i + 1 < steps) copy(&v_map, sv, &v_full, i + 1);
+            }
+            if (!came) {
+                // something did not come: nothing is under way when the CTA ends (what was not started runs into the limit)
+                flag_error(p.err, PKV_DEVERR_TIMEOUT);
+                failed = 1;
+                mbar_wait(&k_full, 0);
+                mbar_wait(&k_full, 1);
+                mbar_wait(&v_full, 0);
+                mbar_wait(&v_full, 1);
+                mma_commit(&s_done);
+                mbar_wait(&s_done, 0);
+                mbar_wait(&s_done, 1);
+            }
+        }
+    } else {
+        // ---- a row to a thread
+        const int row = warp * 32 + lane, token = min(row / G, rows - 1);
+        const bool on = row < rows * G;
+        const int vis = mine.visible(token), vis_all = mine.visible(0), vis_most = mine.visible(rows - 1);
+        const uint32_t lanes = uint32_t(warp * 32) << 16;   // this warp's lanes of TMEM
+        const uint32_t* my_marks = marks + (token >> 5);
+        const uint32_t my_bit = on ? 1u << (token & 31) : 0u;
+        float m = -INFINITY, l = 0.f;
+        bool came = true;
+        for (int i = 0; i < steps; ++i) {
+            came = __all_sync(0xffffffffu, mbar_wait(&s_done, i & 1));
+            if (!came) break;
+            fence_after_sync();
+            const int first = i * kStepPages, k = min(kStepPages, n - first);
+            // the row's tokens in each page of the step
+            int live[kStepPages];
+            bool all = true, cut = k < kStepPages;
+#pragma unroll
+            for (int b = 0; b < kStepPages; ++b) {
+                live[b] = 0;
+                if (b < k) {
+                    const int page = entry[first + b].x;
+                    if (my_marks[page * MW] & my_bit) live[b] = vis - page * kBS;
+                    cut |= page * kBS + kBS > vis_most;
+                }
+                all &= live[b] >= kBS;
+            }
+            all = __all_sync(0xffffffffu, all);
+            // the maximum
+            float most = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_load(tmem_s + lanes + 32 * c, r);
+                wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float x = __uint_as_float(r[j]) * p.scale_log2;
+                    if (!all) x = (j & 15) < live[2 * c + (j >> 4)] ? x : -INFINITY;
+                    most = fmaxf(most, x);
+                }
+            }
+            const bool grow = most > m + kSlack;
+            const float now = grow ? most : m, ref = now == -INFINITY ? 0.f : now;
+            const float f = grow && m > -INFINITY ? exp2_ftz(m - ref) : 1.f;
+            m = now;
+            l *= f;
+            if (__any_sync(0xffffffffu, f != 1.f)) {   // the sums so far; their MMAs have ended before S's began
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_load(tmem_o + lanes + 32 * c, r);
+                    wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+                    tmem_store(tmem_o + lanes + 32 * c, r);
+                }
+            }
+            // the weights, in the place of the scores
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32], w[32];
+                tmem_load(tmem_s + lanes + 32 * c, r);
+                wait_ld();
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = __uint_as_float(r[j + e]) * p.scale_log2;
+                        if (!all) x[e] = ((j + e) & 15) < live[2 * c + (j >> 4)] ? x[e] : -INFINITY;
+                        x[e] = exp2_ftz(x[e] - ref);
+                    }
+                    sum += x[0] + x[1];
+                    const float a = x[0] * kPUnit, b = x[1] * kPUnit;
+                    w[j / 2] = pack2<BF>(a, b);
+                    const float2 back = Half16<T>::unpack2(w[j / 2]);
+                    w[16 + j / 2] = pack2<BF>(a - back.x, b - back.y);
+                }
+                l += sum;
+                tmem_store(tmem_s + lanes + 32 * c, w);
+            }
+            if (cut) {   // tokens behind the last one, and pages that are none, may hold anything: 0 times it would not be 0
+                came = __all_sync(0xffffffffu, mbar_wait(&v_full, i & 1));
+                if (!came) break;
+                for (int j = threadIdx.x; j < kStepTokens * NC * 8; j += kSoftWarps * 32) {
+                    const int tok = j / (NC * 8), c = j % (NC * 8), b = tok / kBS;
+                    const bool keep = b < k && entry[first + b].x * kBS + tok % kBS < vis_most;
+                    if (!keep) *reinterpret_cast<uint4*>(sv + (c >> 3) * CHUNK + tok * 128 + 16 * (c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_done);
+        }
+        // ---- the outputs
+        if (came && steps > 0) came = __all_sync(0xffffffffu, mbar_wait(&o_done, (steps - 1) & 1));
+        if (came) {
+            fence_after_sync();
+            const float inv = (l > 0.f ? 1.f / l : (l == l ? 0.f : l)) * (1.f / kPUnit);   // no visible token: zeros
+            const size_t at = (size_t(tile.r0 + token) * p.num_heads + size_t(kvh) * G + row % G) * D;
+            bool finite = true;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                if (steps > 0) {
+                    tmem_load(tmem_o + lanes + 32 * c, r);
+                    wait_ld();
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (steps > 0 && l != 0.f)
+                        v = make_float4(__uint_as_float(r[j]) * inv, __uint_as_float(r[j + 1]) * inv, __uint_as_float(r[j + 2]) * inv,
+                                        __uint_as_float(r[j + 3]) * inv);
+                    finite &= fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY;
+                    if (on) store_out4(p.out, p.out_dtype, at + 32 * c + j, v);
+                }
+            }
+            if (on && !finite) atomicOr(&redo[row >> 5], 1u << (row & 31));
+            fence_before_sync();
+        } else {
+            failed = 1;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        fence_after_sync();
+        tmem_free(tmem, 256);
+    }
+    if (failed) return;
+
+    // ---- rows that are not finite, again one by one: an infinity or NaN in V that the row does not see, times its weight of 0,
+    // may have reached it
+    for (int row = warp; row < rows * G; row += kSoftWarps + 1) {
+        if (!(redo[row >> 5] >> (row & 31) & 1u)) continue;
+        const int token = row / G, vis = mine.visible(token);
+        const int64_t head = (int64_t(tile.r0) + token) * p.num_heads + int64_t(kvh) * G + row % G;
+        constexpr int E = D / 32;
+        float q[E], o[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int d = 0; d < E; ++d) {
+            q[d] = load_q(p.q, p.q_dtype, head * D + lane * E + d) * p.scale_log2;
+            o[d] = 0.f;
+        }
+        for (int i = 0; i < n; ++i) {
+            const int2 e = entry[i];
+            if (!(marks[e.x * MW + (token >> 5)] >> (token & 31) & 1u)) continue;
+            const int live = min(vis - e.x * kBS, kBS);
+            for (int t = 0; t < live; ++t) {
+                const int64_t at = ((int64_t(e.y) * kBS + t) * p.num_kv_heads + kvh) * D + lane * E;
+                float s = 0.f;
+#pragma unroll
+                for (int d = 0; d < E; ++d) s = fmaf(q[d], Half16<T>::to_float(static_cast<const uint16_t*>(p.k)[at + d]), s);
+#pragma unroll
+                for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+                const float now = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - now), w = exp2f(s - now);
+                m = now;
+                l = l * f + w;
+#pragma unroll
+                for (int d = 0; d < E; ++d)
+                    o[d] = (l == w ? 0.f : o[d] * f) + w * Half16<T>::to_float(static_cast<const uint16_t*>(p.v)[at + d]);
+            }
+        }
+        for (int d = 0; d < E; ++d)
+            store_out(p.out, p.out_dtype, size_t(head) * D + lane * E + d, l == 0.f ? 0.f : o[d] / l);
+    }
+}
+
+// The kernel may take kPromptSmem of dynamic shared memory: said once per kernel and device.
+constexpr int kPromptSmem = 220 * 1024;
+template <bool BF, int D>
+cudaError_t launch_prompt(const SelectedParams& p, int64_t units, size_t smem, const CUtensorMap& km, const CUtensorMap& vm,
+                          cudaStream_t st) {
+    static PerDevice ready;
+    int dev = 0, one = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cudaError_t(ready.get(dev, &one, [](int* v) {
+        *v = 1;
+        return int(cudaFuncSetAttribute(attention_prompt_kernel<BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem));
+    }));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(attention_prompt_kernel<BF, D>, dim3(unsigned(units), p.num_kv_heads), dim3(kPromptThreads), smem, st, km, vm, p);
+}
+
+// Query tokens to a CTA, and its shared memory.
+int prompt_tokens(const SelectedParams& p) { return kRows / (p.num_heads / p.num_kv_heads); }
+size_t prompt_smem(const SelectedParams& p) {
+    int64_t most = int64_t(prompt_tokens(p)) * p.max_pages;
+    if (most > p.max_blocks) most = p.max_blocks;
+    const int64_t words = (prompt_tokens(p) + 31) / 32;
+    return 1024 + 3 * size_t(kRows) * p.head_dim * 2 + size_t(most) * 8 + size_t(p.max_blocks) * words * 4;
+}
+
+}  // namespace
+
+// Half of the rows or more of a sequence's average tile, 16-bit caches, and lists that fit.
+bool prompt_tiles(const SelectedParams& p, int cache_kind) {
+    if (cache_kind != PKV_CACHE_F16 && cache_kind != PKV_CACHE_BF16) return false;
+    const int64_t hint = p.cu_q ? int64_t(p.num_rows) / p.num_seqs : p.q_len;   // rows of a sequence
+    return hint * 2 >= prompt_tokens(p) && prompt_smem(p) <= kPromptSmem;
+}
+
+cudaError_t launch_attention_prompt(SelectedParams p, int cache_kind, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
+    const size_t smem = prompt_smem(p);
+    p.tile_rows = prompt_tokens(p);
+    p.entries = int(std::min<int64_t>(int64_t(p.tile_rows) * p.max_pages, p.max_blocks));
+    const int64_t units = p.cu_q ? int64_t(p.num_rows) / p.tile_rows + p.num_seqs
+                                 : int64_t(p.num_seqs) * ((int64_t(p.q_len) + p.tile_rows - 1) / p.tile_rows);
+    if (units > 0x7fffffff) return cudaErrorInvalidValue;
+    if (cache_kind == PKV_CACHE_BF16)
+        return p.head_dim == 128 ? launch_prompt<true, 128>(p, units, smem, km, vm, stream)
+                                 : launch_prompt<true, 64>(p, units, smem, km, vm, stream);
+    return p.head_dim == 128 ? launch_prompt<false, 128>(p, units, smem, km, vm, stream)
+                             : launch_prompt<false, 64>(p, units, smem, km, vm, stream);
+}
+
+}  // namespace pkv

@@ -350,6 +350,12 @@ cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CU
 cudaError_t launch_attention_rows(const SelectedParams& p, int cache_kind, int64_t units, int cluster, size_t lists,
                                   const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 
+// Chunks of prompts over 16-bit caches (attention_prompt.cu): whether this call is one, and the call (maps whose boxes are
+// 16 rows of 128 bytes, with the 128-byte swizzle).
+bool prompt_tiles(const SelectedParams& p, int cache_kind);
+cudaError_t launch_attention_prompt(SelectedParams p, int cache_kind, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                    cudaStream_t stream);
+
 struct GatherParams {
     void* k_out;
     void* v_out;

@@ -352,6 +352,65 @@ def test_attention_of_several_tokens(kind, qd, q_lens, ragged):
     check_out(got, *want, kind, torch.float32)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("H,hkv,d", [(8, 2, 128), (4, 2, 64), (8, 1, 128), (2, 2, 64), (2, 2, 128), (8, 1, 64)])
+@pytest.mark.parametrize("ctx,q_lens,width", [([300, 150, 101], [130, 129, 64], 9), ([1000], [200], 40), ([90, 16, 400], [90, 0, 300], 3),
+                                              ([5, 2000], [70, 260], 64)])
+def test_chunks_of_prompts(kind, H, hkv, d, ctx, q_lens, width):
+    # the first tokens of a sequence shorter than its query tokens see nothing
+    w = ref.World(kind, ctx, hkv, d, seed=d + H)
+    q = queries(w, sum(q_lens), H)
+    lists = random_lists(ctx, q_lens, hkv, width, 4)
+    want = ref.attention(w, q, 0.15, q_lens, lists)
+    e = err()
+    for dtype in (torch.float32, w.q_dtype):
+        got = run_attention(w, q, q_lens, lists, width, dtype, ragged=True, extra=5, scale=0.15, e=e)
+        check_out(got, *want, kind, dtype)
+    assert int(e) == 0
+
+
+def test_chunks_of_prompts_with_bad_entries_and_tables():
+    w = ref.World("bf16", [400, 300], 2, 64, seed=23)
+    q_lens = [64, 64]
+    q = queries(w, 128, 8)
+    given, taken = [], []
+    for _, vis in ref.rows_of(w.ctx, q_lens):
+        n = -(-vis // 16)
+        given.append([[0, n + 3, 2, 2, 1, n - 1], [-1, 5, 4, n]])
+        taken.append([[0, 2, n - 1], [5]])
+    e = err()
+    got = run_attention(w, q, q_lens, given, 6, torch.float32, ragged=True, scale=0.15, e=e)
+    assert int(e) == PAGE_LIST
+    check_out(got, *ref.attention(w, q, 0.15, q_lens, taken), "bf16", torch.float32)
+    good = w.tables.clone()
+    w.tables[0, 2], w.tables[1, 5] = -1, 10 ** 6
+    e.zero_()
+    got = run_attention(w, q, q_lens, taken, 6, torch.float32, ragged=True, scale=0.15, e=e)
+    assert int(e) == OOB_BLOCK
+    w.tables = good
+    left = [[[p for p in h if p != (2 if r < 64 else 5)] for h in heads] for r, heads in enumerate(taken)]
+    check_out(got, *ref.attention(w, q, 0.15, q_lens, left), "bf16", torch.float32)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_chunks_of_prompts_keep_what_they_do_not_see(value):
+    w = ref.World("bf16", [200, 330], 2, 128, seed=24)
+    q_lens = [60, 40]
+    q = queries(w, 100, 8)
+    lists = random_lists(w.ctx, q_lens, 2, 6, 8)
+    lists[3][0] = sorted(set(lists[3][0][:4]) | {2})
+    w.cache.v[int(w.tables[0, 2]), 5, 0, 77] = value    # kv head 0, page 2: the rows that list it
+    w.cache.v[int(w.tables[0, 12]), 199 % 16] = value   # the last token of sequence 0
+    w.v64 = w.cache.v.double()
+    want, mag, big = ref.attention(w, q, 0.15, q_lens, lists)
+    got = run_attention(w, q, q_lens, lists, 6, torch.float32, ragged=True, scale=0.15).double().cpu()
+    fine = torch.isfinite(want)
+    assert 0 < int((~fine).sum()) < fine.numel() / 2
+    assert torch.equal(torch.isfinite(got), fine)
+    tol = mag * (2.0 ** -15 + big[..., None] * 2.0 ** -18)
+    assert ((got - want).abs()[fine] <= tol[fine] + want.abs()[fine] * 2.0 ** -24).all()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_long_lists_by_clusters(kind):
     w = ref.World(kind, [20000], 1, 64, seed=9)
