@@ -7,7 +7,7 @@
 //   softmax     a thread owns a row: no shuffles, its maximum and sum stay with it;
 //   O += P V    P from TMEM, where it takes S's place 32 columns at a time, as two 16-bit halves
 //               (hi, lo) and so two MMAs a k step; V as the cache has it (N-major); O in TMEM.
-// One thread issues the copies and the MMAs, four warps do the softmax.  256 columns of TMEM and
+// One thread issues the copies, one the MMAs, four warps do the softmax.  256 columns of TMEM and
 // 96 KB of tiles to a CTA: two CTAs to an SM, and one's softmax runs under the other's MMAs.
 //
 // Whatever the lists have in common, the union is no larger than what smaller tiles would read
@@ -21,7 +21,7 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 128, kStepPages = 8, kStepTokens = kStepPages * kBS;
-constexpr int kSoftWarps = 4, kPromptThreads = (kSoftWarps + 1) * 32;
+constexpr int kSoftWarps = 4, kPromptWarps = kSoftWarps + 2, kPromptThreads = kPromptWarps * 32;
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -34,8 +34,20 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
 }
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_wait without the long suspension, whose end costs more than these waits last (the limit is the same).
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_addr(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(a, parity)) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+}
 
 // The barrier's phase completes when this thread's MMAs so far have.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -71,6 +83,12 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
         : "memory");
 #undef PKV_OUT
 }
+// The loads so far have come: r may be used behind it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+#define PKV_TIE(i) "+r"(r[i])
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_R32(PKV_TIE)::"memory");
+#undef PKV_TIE
+}
 __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
 #define PKV_IN(i) "r"(r[i])
     asm volatile(
@@ -103,7 +121,8 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     constexpr int NC = D / 64;                      // 64-dim chunks of a row
     constexpr int CHUNK = kRows * 128;              // bytes of a chunk of 128 rows or tokens
     constexpr int TILE = NC * CHUNK;                // Q, K, V alike
-    constexpr float kSlack = BF ? 8.f : 1.f, kPUnit = BF ? 1.f : 16384.f;   // as PageMath's
+    // as PageMath's; here the sums of the weights have fp16's unit too, 2^kShift
+    constexpr float kSlack = BF ? 8.f : 1.f, kShift = BF ? 0.f : 14.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *const sq = smem, *const sk = smem + TILE, *const sv = smem + 2 * TILE;
@@ -111,7 +130,7 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     uint32_t* const marks = reinterpret_cast<uint32_t*>(entry + p.entries);   // [pages][mark words]: the tokens that list a page
     __shared__ uint64_t k_full, v_full, s_done, p_done, o_done;
     __shared__ uint32_t tmem_at;
-    __shared__ int scan[kSoftWarps + 1], kept, failed;
+    __shared__ int scan[kPromptWarps], kept, failed, counts[kRows];
     __shared__ uint32_t redo[kRows / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -137,43 +156,56 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     const int pages = mine.pages(rows - 1);
 
     // ---- the queries, swizzled as TMA would have them; rows of no token are zeros
-    for (int i = threadIdx.x; i < kRows * NC * 8; i += kPromptThreads) {
-        const int c = i % (NC * 8), row = i / (NC * 8);
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows * G)
-            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                     ((int64_t(tile.r0) + row / G) * p.num_heads + int64_t(kvh) * G + row % G) * D) + c);
-        *reinterpret_cast<uint4*>(sq + (c >> 3) * CHUNK + row * 128 + 16 * ((c & 7) ^ (row & 7))) = x;
+    for (int i0 = threadIdx.x; i0 < kRows * NC * 8; i0 += 8 * kPromptThreads) {
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kPromptThreads, c = i % (NC * 8), row = i / (NC * 8);
+            x[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows * G)
+                x[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                            ((int64_t(tile.r0) + row / G) * p.num_heads + int64_t(kvh) * G + row % G) * D) + c);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kPromptThreads, c = i % (NC * 8), row = i / (NC * 8);
+            if (i < kRows * NC * 8) *reinterpret_cast<uint4*>(sq + (c >> 3) * CHUNK + row * 128 + 16 * ((c & 7) ^ (row & 7))) = x[j];
+        }
     }
     fence_proxy_async_smem();
 
     // ---- the union of the lists, if every entry is in range and above the one before it; else the slow way
     for (int i = threadIdx.x; i < pages * MW; i += kPromptThreads) marks[i] = 0;
+    if (threadIdx.x < rows) counts[threadIdx.x] = mine.count(threadIdx.x);
     if (warp == 0) tmem_alloc(&tmem_at, 256);
     __syncthreads();
+    // a thread takes entries far apart, eight at a time: their loads are in flight together
     bool rising = true;
-    for (int row = warp; row < rows; row += kSoftWarps + 1) {
-        const int32_t* list = mine.list(row);
-        int e = lane < p.max_pages ? list[lane] : -1;   // comes with the count, not after it
-        const int count = mine.count(row), limit = mine.pages(row);
-        int last = -1;   // the entry before this 32
-        for (int i = lane; i - lane < count; i += 32) {
-            const int ahead = i + 32 < p.max_pages ? list[i + 32] : -1;
-            int before = __shfl_up_sync(0xffffffffu, e, 1);
-            if (lane == 0) before = last;
-            const bool ok = e > before && e < limit;
-            if (i < count) {
-                rising &= ok;
-                if (ok) atomicOr(marks + e * MW + (row >> 5), 1u << (row & 31));
-            }
-            last = __shfl_sync(0xffffffffu, e, 31);
-            e = ahead;
+    const int entries = rows * p.max_pages;
+    const int32_t* const lists = mine.list(0);
+    const int64_t next_row = int64_t(p.num_kv_heads) * p.max_pages;
+    for (int i0 = threadIdx.x; i0 < entries; i0 += 8 * kPromptThreads) {
+        int e[8], before[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kPromptThreads, row = i / p.max_pages, k = i - row * p.max_pages;
+            const bool in = i < entries && k < counts[row];
+            e[j] = in ? lists[row * next_row + k] : INT_MAX;
+            before[j] = in && k > 0 ? lists[row * next_row + k - 1] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kPromptThreads, row = i / p.max_pages, k = i - row * p.max_pages;
+            if (i >= entries || k >= counts[row]) continue;
+            const bool ok = e[j] > before[j] && e[j] < mine.pages(row);
+            rising &= ok;
+            if (ok) atomicOr(marks + e[j] * MW + (row >> 5), 1u << (row & 31));
         }
     }
     if (__syncthreads_or(!rising)) {
         for (int i = threadIdx.x; i < pages * MW; i += kPromptThreads) marks[i] = 0;
         __syncthreads();
-        for (int row = warp; row < rows; row += kSoftWarps + 1)
+        for (int row = warp; row < rows; row += kPromptWarps)
             mine.in_order(row, lane, [&](int, bool, bool taken, int e) {
                 if (taken) atomicOr(marks + e * MW + (row >> 5), 1u << (row & 31));
             });
@@ -200,17 +232,19 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         __syncthreads();
         int at = incl - c;
         n = 0;
-        for (int w = 0; w <= kSoftWarps; ++w) {
+        for (int w = 0; w < kPromptWarps; ++w) {
             if (w < warp) at += scan[w];
             n += scan[w];
         }
-        bool whole = true;
         for (int i = a; i < b; ++i)
-            if (listed(i)) {
-                const int block = mine.block(i);
-                whole &= block >= 0;
-                entry[at++] = make_int2(i, block);
-            }
+            if (listed(i)) entry[at++].x = i;
+        __syncthreads();
+        bool whole = true;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kPromptThreads) {
+            entry[i].y = mine.block(entry[i].x);
+            whole &= entry[i].y >= 0;
+        }
         if (__syncthreads_or(!whole)) {
             if (warp == 0) {
                 const int k = mine.close_up(entry, n, lane);
@@ -224,9 +258,9 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     fence_after_sync();
     const int steps = (n + kStepPages - 1) / kStepPages;
 
-    if (warp == kSoftWarps) {
-        // ---- the copies and the MMAs, by one thread
-        if (lane == 0 && steps > 0) {
+    if (warp == kSoftWarps + 1) {
+        // ---- the copies, by one thread: K's tile is free when S has been worked out, V's when it has been added
+        if (lane == 0) {
             auto copy = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int step) {
                 const int first = step * kStepPages, k = min(kStepPages, n - first);
                 mbar_arrive_expect_tx(bar, k * kBS * D * 2);
@@ -235,38 +269,42 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                     for (int c = 0; c < NC; ++c)
                         tma_load_2d(dst + c * CHUNK + i * kBS * 128, map, kvh * D * 2 + c * 128, entry[first + i].y * kBS, bar);
             };
-            copy(&k_map, sk, &k_full, 0);
-            copy(&v_map, sv, &v_full, 0);
-            const uint32_t qa = smem_addr(sq), ka = smem_addr(sk), va = smem_addr(sv);
+            for (int i = 0; i < steps; ++i) {
+                if (i > 0 && !wait_soon(&s_done, (i - 1) & 1)) break;
+                copy(&k_map, sk, &k_full, i);
+                if (i > 0 && !wait_soon(&o_done, (i - 1) & 1)) break;
+                copy(&v_map, sv, &v_full, i);
+            }
+        }
+    } else if (warp == kSoftWarps) {
+        // ---- the MMAs, by one thread
+        if (lane == 0) {
+            // the operands' descriptors: an offset is added to their address field
+            const uint64_t q0 = operand(smem_addr(sq), 16, 1024), k0 = operand(smem_addr(sk), 16, 1024);
+            const uint64_t v0 = operand(smem_addr(sv), CHUNK, 1024);
             bool came = true;
-            for (int i = 0; i < steps && came; ++i) {
+            for (int i = 0; i < steps; ++i) {
                 const uint32_t parity = i & 1;
-                came = mbar_wait(&k_full, parity);
-                if (!came) break;
+                if (!(came = wait_soon(&k_full, parity))) break;
                 fence_after_sync();
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * CHUNK + (ks & 3) * 32;
-                    mma_ss(tmem_s, operand(qa + off, 16, 1024), operand(ka + off, 16, 1024), instruction<BF>(kStepTokens, false), ks > 0);
+                    const uint32_t off = ((ks >> 2) * CHUNK + (ks & 3) * 32) >> 4;
+                    mma_ss(tmem_s, q0 + off, k0 + off, instruction<BF>(kStepTokens, false), ks > 0);
                 }
                 mma_commit(&s_done);
-                came = mbar_wait(&s_done, parity);
-                if (!came) break;
-                if (i + 1 < steps) copy(&k_map, sk, &k_full, i + 1);
-                came = mbar_wait(&v_full, parity) && mbar_wait(&p_done, parity);
-                if (!came) break;
+                if (!(came = wait_soon(&v_full, parity) && wait_soon(&p_done, parity))) break;
                 fence_after_sync();
+                mma_ts(tmem_o, tmem_s, v0, instruction<BF>(D, true), i > 0);
+                mma_ts(tmem_o, tmem_s + 16, v0, instruction<BF>(D, true), true);
 #pragma unroll
-                for (int ks = 0; ks < kStepTokens / 16; ++ks) {
+                for (int ks = 1; ks < kStepTokens / 16; ++ks) {
                     const uint32_t pa = tmem_s + 32 * (ks >> 1) + 8 * (ks & 1);   // hi; lo is 16 columns on
-                    const uint64_t b = operand(va + ks * 16 * 128, CHUNK, 1024);
-                    mma_ts(tmem_o, pa, b, instruction<BF>(D, true), i > 0 || ks > 0);
-                    mma_ts(tmem_o, pa + 16, b, instruction<BF>(D, true), true);
+                    mma_ts(tmem_o, pa, v0 + ks * 128, instruction<BF>(D, true), true);
+                    mma_ts(tmem_o, pa + 16, v0 + ks * 128, instruction<BF>(D, true), true);
                 }
                 mma_commit(&o_done);
-                came = mbar_wait(&o_done, parity);
-                if (!came) break;
-                if (i + 1 < steps) copy(&v_map, sv, &v_full, i + 1);
+                if (!(came = wait_soon(&o_done, parity))) break;   // the next S takes P's place
             }
             if (!came) {
                 // something did not come: nothing is under way when the CTA ends (what was not started runs into the limit)
@@ -292,78 +330,109 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         float m = -INFINITY, l = 0.f;
         bool came = true;
         for (int i = 0; i < steps; ++i) {
-            came = __all_sync(0xffffffffu, mbar_wait(&s_done, i & 1));
-            if (!came) break;
-            fence_after_sync();
             const int first = i * kStepPages, k = min(kStepPages, n - first);
-            // the row's tokens in each page of the step
-            int live[kStepPages];
-            bool all = true, cut = k < kStepPages;
+            // What is added to the scores of the step's pages: 0, or -inf where the row does not list the page.  Where some row
+            // sees a page in part, or there are fewer than 8, tokens are left out one by one instead.
+            float bias[kStepPages];
+            bool cut = k < kStepPages, edge = cut;
 #pragma unroll
             for (int b = 0; b < kStepPages; ++b) {
-                live[b] = 0;
-                if (b < k) {
-                    const int page = entry[first + b].x;
-                    if (my_marks[page * MW] & my_bit) live[b] = vis - page * kBS;
-                    cut |= page * kBS + kBS > vis_most;
-                }
-                all &= live[b] >= kBS;
+                const int page = entry[b < k ? first + b : first].x;
+                bias[b] = b < k && (my_marks[page * MW] & my_bit) ? 0.f : -INFINITY;
+                cut |= page * kBS + kBS > vis_most;
+                edge |= page * kBS + kBS > vis_all;
             }
-            all = __all_sync(0xffffffffu, all);
-            // the maximum
-            float most = -INFINITY;
+            came = __all_sync(0xffffffffu, wait_soon(&s_done, i & 1));
+            if (!came) break;
+            fence_after_sync();
+            // A chunk is 32 tokens, two pages; the next one's scores are on their way while one is worked on.
+            uint32_t r[2][32];
+            float most = -INFINITY, ref = 0.f, f = 1.f;
+            auto reference = [&] {
+                const bool grow = most > m + kSlack;
+                const float now = grow ? most : m;
+                ref = now == -INFINITY ? 0.f : now;
+                f = grow && m > -INFINITY ? exp2_ftz(m - ref) : 1.f;
+                m = now;
+                l *= f;
+                if (__any_sync(0xffffffffu, f != 1.f)) {   // the sums so far; their MMAs have ended before S's began
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t r[32];
-                tmem_load(tmem_s + lanes + 32 * c, r);
-                wait_ld();
+                    for (int c = 0; c < D / 32; ++c) {
+                        tmem_load(tmem_o + lanes + 32 * c, r[0]);
+                        wait_ld(r[0]);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float x = __uint_as_float(r[j]) * p.scale_log2;
-                    if (!all) x = (j & 15) < live[2 * c + (j >> 4)] ? x : -INFINITY;
-                    most = fmaxf(most, x);
-                }
-            }
-            const bool grow = most > m + kSlack;
-            const float now = grow ? most : m, ref = now == -INFINITY ? 0.f : now;
-            const float f = grow && m > -INFINITY ? exp2_ftz(m - ref) : 1.f;
-            m = now;
-            l *= f;
-            if (__any_sync(0xffffffffu, f != 1.f)) {   // the sums so far; their MMAs have ended before S's began
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_load(tmem_o + lanes + 32 * c, r);
-                    wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-                    tmem_store(tmem_o + lanes + 32 * c, r);
-                }
-            }
-            // the weights, in the place of the scores
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t r[32], w[32];
-                tmem_load(tmem_s + lanes + 32 * c, r);
-                wait_ld();
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    float x[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = __uint_as_float(r[j + e]) * p.scale_log2;
-                        if (!all) x[e] = ((j + e) & 15) < live[2 * c + (j >> 4)] ? x[e] : -INFINITY;
-                        x[e] = exp2_ftz(x[e] - ref);
+                        for (int j = 0; j < 32; ++j) r[0][j] = __float_as_uint(__uint_as_float(r[0][j]) * f);
+                        tmem_store(tmem_o + lanes + 32 * c, r[0]);
                     }
-                    sum += x[0] + x[1];
-                    const float a = x[0] * kPUnit, b = x[1] * kPUnit;
-                    w[j / 2] = pack2<BF>(a, b);
-                    const float2 back = Half16<T>::unpack2(w[j / 2]);
-                    w[16 + j / 2] = pack2<BF>(a - back.x, b - back.y);
                 }
-                l += sum;
-                tmem_store(tmem_s + lanes + 32 * c, w);
+            };
+            // the weights of two tokens in the place of their scores: the pair's 16-bit halves, and what they leave
+            auto weights = [&](float x, float y, uint32_t& hi, uint32_t& lo) {
+                x = exp2_ftz(x);
+                y = exp2_ftz(y);
+                l += x + y;
+                hi = pack2<BF>(x, y);
+                const float2 back = Half16<T>::unpack2(hi);
+                lo = pack2<BF>(x - back.x, y - back.y);
+            };
+            if (!edge) {
+                tmem_load(tmem_s + lanes, r[0]);
+                wait_ld(r[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) tmem_load(tmem_s + lanes + 32 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        most = fmaxf(most, fmaf(__uint_as_float(r[c & 1][j]), p.scale_log2, bias[2 * c + (j >> 4)]));
+                    if (c < 3) wait_ld(r[(c + 1) & 1]);
+                }
+                reference();
+                tmem_load(tmem_s + lanes, r[0]);
+#pragma unroll
+                for (int b = 0; b < kStepPages; ++b) bias[b] += kShift - ref;
+                wait_ld(r[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) tmem_load(tmem_s + lanes + 32 * (c + 1), r[(c + 1) & 1]);
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        weights(fmaf(__uint_as_float(r[c & 1][j]), p.scale_log2, bias[2 * c + (j >> 4)]),
+                                fmaf(__uint_as_float(r[c & 1][j + 1]), p.scale_log2, bias[2 * c + (j >> 4)]), w[j / 2], w[16 + j / 2]);
+                    if (c < 3) wait_ld(r[(c + 1) & 1]);
+                    tmem_store(tmem_s + lanes + 32 * c, w);
+                }
+            } else {
+                // what the row sees of a chunk's pages
+                auto live = [&](int c, int h) {
+                    if (2 * c + h >= k) return 0;
+                    const int page = entry[first + 2 * c + h].x;
+                    return my_marks[page * MW] & my_bit ? vis - page * kBS : 0;
+                };
+                auto score = [&](uint32_t bits, int j, int lo, int hi) {
+                    return (j & 15) < (j < 16 ? lo : hi) ? __uint_as_float(bits) * p.scale_log2 : -INFINITY;
+                };
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int lo = live(c, 0), hi = live(c, 1);
+                    tmem_load(tmem_s + lanes + 32 * c, r[0]);
+                    wait_ld(r[0]);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) most = fmaxf(most, score(r[0][j], j, lo, hi));
+                }
+                reference();
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int lo = live(c, 0), hi = live(c, 1);
+                    tmem_load(tmem_s + lanes + 32 * c, r[0]);
+                    wait_ld(r[0]);
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        weights(score(r[0][j], j, lo, hi) + (kShift - ref), score(r[0][j + 1], j + 1, lo, hi) + (kShift - ref), w[j / 2],
+                                w[16 + j / 2]);
+                    tmem_store(tmem_s + lanes + 32 * c, w);
+                }
             }
             if (cut) {   // tokens behind the last one, and pages that are none, may hold anything: 0 times it would not be 0
                 came = __all_sync(0xffffffffu, mbar_wait(&v_full, i & 1));
@@ -384,7 +453,7 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         if (came && steps > 0) came = __all_sync(0xffffffffu, mbar_wait(&o_done, (steps - 1) & 1));
         if (came) {
             fence_after_sync();
-            const float inv = (l > 0.f ? 1.f / l : (l == l ? 0.f : l)) * (1.f / kPUnit);   // no visible token: zeros
+            const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);   // no visible token: zeros
             const size_t at = (size_t(tile.r0 + token) * p.num_heads + size_t(kvh) * G + row % G) * D;
             bool finite = true;
 #pragma unroll
@@ -392,7 +461,7 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 uint32_t r[32];
                 if (steps > 0) {
                     tmem_load(tmem_o + lanes + 32 * c, r);
-                    wait_ld();
+                    wait_ld(r);
                 }
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
@@ -419,7 +488,7 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
     // ---- rows that are not finite, again one by one: an infinity or NaN in V that the row does not see, times its weight of 0,
     // may have reached it
-    for (int row = warp; row < rows * G; row += kSoftWarps + 1) {
+    for (int row = warp; row < rows * G; row += kPromptWarps) {
         if (!(redo[row >> 5] >> (row & 31) & 1u)) continue;
         const int token = row / G, vis = mine.visible(token);
         const int64_t head = (int64_t(tile.r0) + token) * p.num_heads + int64_t(kvh) * G + row % G;
