@@ -2,13 +2,14 @@
 // bf16 caches (attention_selected.cuh): 128 query rows to a CTA on tcgen05.
 //
 // 128 / g neighbouring query tokens with a kv head's g query heads are the M side of the MMAs; the
-// CTA reads the union of their lists once, 8 pages (128 tokens) at a step, and masks by row:
+// CTA reads the union of their lists once, 4 pages (64 tokens) at a step, and masks by row:
 //   S = Q K^T   both operands in shared memory (K-major, 128-byte swizzle), S in TMEM;
 //   softmax     a thread owns a row: no shuffles, its maximum and sum stay with it;
 //   O += P V    P from TMEM, where it takes S's place 32 columns at a time, as two 16-bit halves
 //               (hi, lo) and so two MMAs a k step; V as the cache has it (N-major); O in TMEM.
-// One thread issues the copies, one the MMAs, four warps do the softmax.  256 columns of TMEM and
-// 96 KB of tiles to a CTA: two CTAs to an SM, and one's softmax runs under the other's MMAs.
+// One thread issues the copies, one the MMAs, four warps do the softmax.  K, V and S have two
+// buffers each: the next step's S is there when a softmax ends, and its O += P V runs under the
+// next one.  256 columns of TMEM and 96 KB of tiles to a CTA, two CTAs to an SM.
 //
 // Whatever the lists have in common, the union is no larger than what smaller tiles would read
 // together, and a page costs 128 rows here what 16 rows cost mma.sync.
@@ -20,7 +21,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kRows = 128, kStepPages = 8, kStepTokens = kStepPages * kBS;
+constexpr int kRows = 128, kStepPages = 4, kStepTokens = kStepPages * kBS;
 constexpr int kSoftWarps = 4, kPromptWarps = kSoftWarps + 2, kPromptThreads = kPromptWarps * 32;
 
 // ---------------------------------------------------------------- tcgen05
@@ -119,26 +120,28 @@ __global__ void __launch_bounds__(kPromptThreads, 2)
 attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const SelectedParams p) {
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     constexpr int NC = D / 64;                      // 64-dim chunks of a row
-    constexpr int CHUNK = kRows * 128;              // bytes of a chunk of 128 rows or tokens
-    constexpr int TILE = NC * CHUNK;                // Q, K, V alike
+    constexpr int CHUNK = kRows * 128, TILE = NC * CHUNK;               // bytes of a chunk of Q, and of all
+    constexpr int KV_CHUNK = kStepTokens * 128, KV_TILE = NC * KV_CHUNK;   // of a step's K, or V
     // as PageMath's; here the sums of the weights have fp16's unit too, 2^kShift
     constexpr float kSlack = BF ? 8.f : 1.f, kShift = BF ? 0.f : 14.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint8_t *const sq = smem, *const sk = smem + TILE, *const sv = smem + 2 * TILE;
-    int2* const entry = reinterpret_cast<int2*>(smem + 3 * TILE);             // the union's pages: page, block
+    uint8_t *const sq = smem, *const sk = smem + TILE, *const sv = sk + 2 * KV_TILE;
+    int2* const entry = reinterpret_cast<int2*>(sv + 2 * KV_TILE);            // the union's pages: page, block
     uint32_t* const marks = reinterpret_cast<uint32_t*>(entry + p.entries);   // [pages][mark words]: the tokens that list a page
-    __shared__ uint64_t k_full, v_full, s_done, p_done, o_done;
+    __shared__ uint64_t k_full[2], v_full[2], s_done[2], p_done[2], o_done[2];   // of the two buffers
     __shared__ uint32_t tmem_at;
-    __shared__ int scan[kPromptWarps], kept, failed, counts[kRows];
+    __shared__ int scan[kPromptWarps], kept, failed, counts[kRows], limits[kRows];
     __shared__ uint32_t redo[kRows / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        mbar_init(&k_full, 1);
-        mbar_init(&v_full, 1);
-        mbar_init(&s_done, 1);
-        mbar_init(&p_done, kSoftWarps);
-        mbar_init(&o_done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&k_full[b], 1);
+            mbar_init(&v_full[b], 1);
+            mbar_init(&s_done[b], 1);
+            mbar_init(&p_done[b], kSoftWarps);
+            mbar_init(&o_done[b], 1);
+        }
         fence_barrier_init();
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
@@ -176,30 +179,45 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
 
     // ---- the union of the lists, if every entry is in range and above the one before it; else the slow way
     for (int i = threadIdx.x; i < pages * MW; i += kPromptThreads) marks[i] = 0;
-    if (threadIdx.x < rows) counts[threadIdx.x] = mine.count(threadIdx.x);
+    if (threadIdx.x < rows) {
+        counts[threadIdx.x] = mine.count(threadIdx.x);
+        limits[threadIdx.x] = mine.pages(threadIdx.x);
+    }
     if (warp == 0) tmem_alloc(&tmem_at, 256);
     __syncthreads();
-    // a thread takes entries far apart, eight at a time: their loads are in flight together
+    // a warp takes four rows at a time, 64 entries of each: their loads are in flight together
     bool rising = true;
-    const int entries = rows * p.max_pages;
-    const int32_t* const lists = mine.list(0);
-    const int64_t next_row = int64_t(p.num_kv_heads) * p.max_pages;
-    for (int i0 = threadIdx.x; i0 < entries; i0 += 8 * kPromptThreads) {
-        int e[8], before[8];
+    for (int r0 = warp; r0 < rows; r0 += 4 * kPromptWarps) {
+        int count[4], last[4], most = 0;   // last: the entry before these 64
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + j * kPromptThreads, row = i / p.max_pages, k = i - row * p.max_pages;
-            const bool in = i < entries && k < counts[row];
-            e[j] = in ? lists[row * next_row + k] : INT_MAX;
-            before[j] = in && k > 0 ? lists[row * next_row + k - 1] : -1;
+        for (int j = 0; j < 4; ++j) {
+            const int row = r0 + j * kPromptWarps;
+            count[j] = row < rows ? counts[row] : 0;
+            most = max(most, count[j]);
+            last[j] = -1;
         }
+        for (int k0 = 0; k0 < most; k0 += 64) {
+            int e[4][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + j * kPromptThreads, row = i / p.max_pages, k = i - row * p.max_pages;
-            if (i >= entries || k >= counts[row]) continue;
-            const bool ok = e[j] > before[j] && e[j] < mine.pages(row);
-            rising &= ok;
-            if (ok) atomicOr(marks + e[j] * MW + (row >> 5), 1u << (row & 31));
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + 32 * h + lane;
+                    e[j][h] = k < count[j] ? mine.list(r0 + j * kPromptWarps)[k] : INT_MAX;
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + 32 * h + lane, row = r0 + j * kPromptWarps;
+                    int before = __shfl_up_sync(0xffffffffu, e[j][h], 1);
+                    if (lane == 0) before = last[j];
+                    last[j] = __shfl_sync(0xffffffffu, e[j][h], 31);
+                    if (k >= count[j]) continue;
+                    const bool ok = e[j][h] > before && e[j][h] < limits[row];
+                    rising &= ok;
+                    if (ok) atomicOr(marks + e[j][h] * MW + (row >> 5), 1u << (row & 31));
+                }
         }
     }
     if (__syncthreads_or(!rising)) {
@@ -267,13 +285,15 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 for (int i = 0; i < k; ++i)
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        tma_load_2d(dst + c * CHUNK + i * kBS * 128, map, kvh * D * 2 + c * 128, entry[first + i].y * kBS, bar);
+                        tma_load_2d(dst + c * KV_CHUNK + i * kBS * 128, map, kvh * D * 2 + c * 128, entry[first + i].y * kBS, bar);
             };
             for (int i = 0; i < steps; ++i) {
-                if (i > 0 && !wait_soon(&s_done, (i - 1) & 1)) break;
-                copy(&k_map, sk, &k_full, i);
-                if (i > 0 && !wait_soon(&o_done, (i - 1) & 1)) break;
-                copy(&v_map, sv, &v_full, i);
+                const int b = i & 1;
+                const uint32_t before = ((i >> 1) & 1) ^ 1u;   // the parity of the buffer's last use
+                if (i > 1 && !wait_soon(&s_done[b], before)) break;
+                copy(&k_map, sk + b * KV_TILE, &k_full[b], i);
+                if (i > 1 && !wait_soon(&o_done[b], before)) break;
+                copy(&v_map, sv + b * KV_TILE, &v_full[b], i);
             }
         }
     } else if (warp == kSoftWarps) {
@@ -281,42 +301,52 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         if (lane == 0) {
             // the operands' descriptors: an offset is added to their address field
             const uint64_t q0 = operand(smem_addr(sq), 16, 1024), k0 = operand(smem_addr(sk), 16, 1024);
-            const uint64_t v0 = operand(smem_addr(sv), CHUNK, 1024);
-            bool came = true;
-            for (int i = 0; i < steps; ++i) {
-                const uint32_t parity = i & 1;
-                if (!(came = wait_soon(&k_full, parity))) break;
+            const uint64_t v0 = operand(smem_addr(sv), KV_CHUNK, 1024);
+            auto scores = [&](int i) {   // S of step i
+                const int b = i & 1;
+                const uint32_t parity = (i >> 1) & 1;
+                if (!wait_soon(&k_full[b], parity)) return false;
+                if (i > 1 && !wait_soon(&o_done[b], parity ^ 1u)) return false;   // P of step i - 2 was there
                 fence_after_sync();
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = ((ks >> 2) * CHUNK + (ks & 3) * 32) >> 4;
-                    mma_ss(tmem_s, q0 + off, k0 + off, instruction<BF>(kStepTokens, false), ks > 0);
-                }
-                mma_commit(&s_done);
-                if (!(came = wait_soon(&v_full, parity) && wait_soon(&p_done, parity))) break;
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss(tmem_s + b * kStepTokens, q0 + (((ks >> 2) * CHUNK + (ks & 3) * 32) >> 4),
+                           k0 + ((b * KV_TILE + (ks >> 2) * KV_CHUNK + (ks & 3) * 32) >> 4), instruction<BF>(kStepTokens, false), ks > 0);
+                mma_commit(&s_done[b]);
+                return true;
+            };
+            bool came = steps > 0 ? scores(0) : true;
+            for (int i = 0; i < steps && came; ++i) {
+                const int b = i & 1;
+                const uint32_t parity = (i >> 1) & 1;
+                if (i + 1 < steps && !(came = scores(i + 1))) break;
+                if (!(came = wait_soon(&v_full[b], parity) && wait_soon(&p_done[b], parity))) break;
                 fence_after_sync();
-                mma_ts(tmem_o, tmem_s, v0, instruction<BF>(D, true), i > 0);
-                mma_ts(tmem_o, tmem_s + 16, v0, instruction<BF>(D, true), true);
+                const uint32_t pa = tmem_s + b * kStepTokens;
+                const uint64_t vb = v0 + ((b * KV_TILE) >> 4);
+                mma_ts(tmem_o, pa, vb, instruction<BF>(D, true), i > 0);
+                mma_ts(tmem_o, pa + 16, vb, instruction<BF>(D, true), true);
 #pragma unroll
                 for (int ks = 1; ks < kStepTokens / 16; ++ks) {
-                    const uint32_t pa = tmem_s + 32 * (ks >> 1) + 8 * (ks & 1);   // hi; lo is 16 columns on
-                    mma_ts(tmem_o, pa, v0 + ks * 128, instruction<BF>(D, true), true);
-                    mma_ts(tmem_o, pa + 16, v0 + ks * 128, instruction<BF>(D, true), true);
+                    const uint32_t at = pa + 32 * (ks >> 1) + 8 * (ks & 1);   // hi; lo is 16 columns on
+                    mma_ts(tmem_o, at, vb + ks * 128, instruction<BF>(D, true), true);
+                    mma_ts(tmem_o, at + 16, vb + ks * 128, instruction<BF>(D, true), true);
                 }
-                mma_commit(&o_done);
-                if (!(came = wait_soon(&o_done, parity))) break;   // the next S takes P's place
+                mma_commit(&o_done[b]);
             }
             if (!came) {
                 // something did not come: nothing is under way when the CTA ends (what was not started runs into the limit)
                 flag_error(p.err, PKV_DEVERR_TIMEOUT);
                 failed = 1;
-                mbar_wait(&k_full, 0);
-                mbar_wait(&k_full, 1);
-                mbar_wait(&v_full, 0);
-                mbar_wait(&v_full, 1);
-                mma_commit(&s_done);
-                mbar_wait(&s_done, 0);
-                mbar_wait(&s_done, 1);
+                for (int b = 0; b < 2; ++b) {
+                    mbar_wait(&k_full[b], 0);
+                    mbar_wait(&k_full[b], 1);
+                    mbar_wait(&v_full[b], 0);
+                    mbar_wait(&v_full[b], 1);
+                }
+                mma_commit(&s_done[0]);
+                mbar_wait(&s_done[0], 0);
+                mbar_wait(&s_done[0], 1);
             }
         }
     } else {
@@ -332,7 +362,7 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
         for (int i = 0; i < steps; ++i) {
             const int first = i * kStepPages, k = min(kStepPages, n - first);
             // What is added to the scores of the step's pages: 0, or -inf where the row does not list the page.  Where some row
-            // sees a page in part, or there are fewer than 8, tokens are left out one by one instead.
+            // sees a page in part, or there are fewer than 4, tokens are left out one by one instead.
             float bias[kStepPages];
             bool cut = k < kStepPages, edge = cut;
 #pragma unroll
@@ -342,10 +372,13 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 cut |= page * kBS + kBS > vis_most;
                 edge |= page * kBS + kBS > vis_all;
             }
-            came = __all_sync(0xffffffffu, wait_soon(&s_done, i & 1));
+            const int buf = i & 1;
+            const uint32_t parity = (i >> 1) & 1, tmem_p = tmem_s + buf * kStepTokens + lanes;
+            came = __all_sync(0xffffffffu, wait_soon(&s_done[buf], parity));
             if (!came) break;
             fence_after_sync();
             // A chunk is 32 tokens, two pages; the next one's scores are on their way while one is worked on.
+            constexpr int CH = kStepTokens / 32;
             uint32_t r[2][32];
             float most = -INFINITY, ref = 0.f, f = 1.f;
             auto reference = [&] {
@@ -355,7 +388,9 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 f = grow && m > -INFINITY ? exp2_ftz(m - ref) : 1.f;
                 m = now;
                 l *= f;
-                if (__any_sync(0xffffffffu, f != 1.f)) {   // the sums so far; their MMAs have ended before S's began
+                if (__any_sync(0xffffffffu, f != 1.f)) {   // the sums so far, when the last step's have been added
+                    came = __all_sync(0xffffffffu, wait_soon(&o_done[buf ^ 1], ((i - 1) >> 1) & 1));
+                    fence_after_sync();
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         tmem_load(tmem_o + lanes + 32 * c, r[0]);
@@ -376,31 +411,31 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 lo = pack2<BF>(x - back.x, y - back.y);
             };
             if (!edge) {
-                tmem_load(tmem_s + lanes, r[0]);
+                tmem_load(tmem_p, r[0]);
                 wait_ld(r[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < 3) tmem_load(tmem_s + lanes + 32 * (c + 1), r[(c + 1) & 1]);
+                for (int c = 0; c < CH; ++c) {
+                    if (c + 1 < CH) tmem_load(tmem_p + 32 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         most = fmaxf(most, fmaf(__uint_as_float(r[c & 1][j]), p.scale_log2, bias[2 * c + (j >> 4)]));
-                    if (c < 3) wait_ld(r[(c + 1) & 1]);
+                    if (c + 1 < CH) wait_ld(r[(c + 1) & 1]);
                 }
                 reference();
-                tmem_load(tmem_s + lanes, r[0]);
+                tmem_load(tmem_p, r[0]);
 #pragma unroll
                 for (int b = 0; b < kStepPages; ++b) bias[b] += kShift - ref;
                 wait_ld(r[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < 3) tmem_load(tmem_s + lanes + 32 * (c + 1), r[(c + 1) & 1]);
+                for (int c = 0; c < CH; ++c) {
+                    if (c + 1 < CH) tmem_load(tmem_p + 32 * (c + 1), r[(c + 1) & 1]);
                     uint32_t w[32];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
                         weights(fmaf(__uint_as_float(r[c & 1][j]), p.scale_log2, bias[2 * c + (j >> 4)]),
                                 fmaf(__uint_as_float(r[c & 1][j + 1]), p.scale_log2, bias[2 * c + (j >> 4)]), w[j / 2], w[16 + j / 2]);
-                    if (c < 3) wait_ld(r[(c + 1) & 1]);
-                    tmem_store(tmem_s + lanes + 32 * c, w);
+                    if (c + 1 < CH) wait_ld(r[(c + 1) & 1]);
+                    tmem_store(tmem_p + 32 * c, w);
                 }
             } else {
                 // what the row sees of a chunk's pages
@@ -413,44 +448,44 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                     return (j & 15) < (j < 16 ? lo : hi) ? __uint_as_float(bits) * p.scale_log2 : -INFINITY;
                 };
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < CH; ++c) {
                     const int lo = live(c, 0), hi = live(c, 1);
-                    tmem_load(tmem_s + lanes + 32 * c, r[0]);
+                    tmem_load(tmem_p + 32 * c, r[0]);
                     wait_ld(r[0]);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) most = fmaxf(most, score(r[0][j], j, lo, hi));
                 }
                 reference();
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < CH; ++c) {
                     const int lo = live(c, 0), hi = live(c, 1);
-                    tmem_load(tmem_s + lanes + 32 * c, r[0]);
+                    tmem_load(tmem_p + 32 * c, r[0]);
                     wait_ld(r[0]);
                     uint32_t w[32];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
                         weights(score(r[0][j], j, lo, hi) + (kShift - ref), score(r[0][j + 1], j + 1, lo, hi) + (kShift - ref), w[j / 2],
                                 w[16 + j / 2]);
-                    tmem_store(tmem_s + lanes + 32 * c, w);
+                    tmem_store(tmem_p + 32 * c, w);
                 }
             }
             if (cut) {   // tokens behind the last one, and pages that are none, may hold anything: 0 times it would not be 0
-                came = __all_sync(0xffffffffu, mbar_wait(&v_full, i & 1));
-                if (!came) break;
+                came &= __all_sync(0xffffffffu, mbar_wait(&v_full[buf], parity)) != 0;
                 for (int j = threadIdx.x; j < kStepTokens * NC * 8; j += kSoftWarps * 32) {
                     const int tok = j / (NC * 8), c = j % (NC * 8), b = tok / kBS;
                     const bool keep = b < k && entry[first + b].x * kBS + tok % kBS < vis_most;
-                    if (!keep) *reinterpret_cast<uint4*>(sv + (c >> 3) * CHUNK + tok * 128 + 16 * (c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                    if (!keep) *reinterpret_cast<uint4*>(sv + buf * KV_TILE + (c >> 3) * KV_CHUNK + tok * 128 + 16 * (c & 7)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
+            if (!came) break;
             wait_st();
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_done);
+            if (lane == 0) mbar_arrive(&p_done[buf]);
         }
         // ---- the outputs
-        if (came && steps > 0) came = __all_sync(0xffffffffu, mbar_wait(&o_done, (steps - 1) & 1));
+        if (came && steps > 0) came = __all_sync(0xffffffffu, mbar_wait(&o_done[(steps - 1) & 1], ((steps - 1) >> 1) & 1));
         if (came) {
             fence_after_sync();
             const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);   // no visible token: zeros
@@ -546,7 +581,7 @@ size_t prompt_smem(const SelectedParams& p) {
     int64_t most = int64_t(prompt_tokens(p)) * p.max_pages;
     if (most > p.max_blocks) most = p.max_blocks;
     const int64_t words = (prompt_tokens(p) + 31) / 32;
-    return 1024 + 3 * size_t(kRows) * p.head_dim * 2 + size_t(most) * 8 + size_t(p.max_blocks) * words * 4;
+    return 1024 + size_t(kRows + 4 * kStepTokens) * p.head_dim * 2 + size_t(most) * 8 + size_t(p.max_blocks) * words * 4;
 }
 
 }  // namespace
