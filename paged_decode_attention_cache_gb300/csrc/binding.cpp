@@ -242,6 +242,8 @@ struct Lib {
     decltype(&pkv_paged_attention_scored) paged_attention_scored;
     decltype(&pkv_paged_attention_balanced) paged_attention_balanced;
     decltype(&pkv_gather_kv_cache_dequant) gather_kv_cache_dequant;
+    decltype(&pkv_reshape_and_cache) reshape_and_cache;
+    decltype(&pkv_quantize_kv) quantize_kv;
     decltype(&pkv_key_bounds) key_bounds;
     decltype(&pkv_select_pages) select_pages;
     decltype(&pkv_paged_attention_selected) paged_attention_selected;
@@ -293,6 +295,8 @@ PyObject* py_load(PyObject*, PyObject* arg) {
     PKV_LOOKUP(paged_attention_scored)
     PKV_LOOKUP(paged_attention_balanced)
     PKV_LOOKUP(gather_kv_cache_dequant)
+    PKV_LOOKUP(reshape_and_cache)
+    PKV_LOOKUP(quantize_kv)
     PKV_LOOKUP(key_bounds)
     PKV_LOOKUP(select_pages)
     PKV_LOOKUP(paged_attention_selected)
@@ -472,7 +476,44 @@ PyObject* py_gather_kv_cache_dequant(PyObject*, PyObject* const* a, Py_ssize_t n
     });
 }
 
-// A cache's key bounds: their type and shape; `at` after the other sizes have been checked.
+// The cache writes by slot: (cache, k_new, v_new, slot_mapping, err_flags, stream)
+template <class F>
+PyObject* write_by_slot(PyObject* const* a, Py_ssize_t n, F f) {
+    return guarded(n, 6, [&] {
+        const Call call;
+        const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"), &slots = tensor(a[3], "slot_mapping");
+        if (slots.scalar_type() != at::kLong) raise(PyExc_ValueError, "slot_mapping must be int64");
+        CacheArg c(a[0]);
+        const int64_t needed = slots.numel() * c.c.num_kv_heads * c.c.head_dim;
+        if (k.numel() < needed || v.numel() < needed)
+            raise(PyExc_ValueError, "k_new / v_new must be [num_tokens, num_kv_heads, head_dim]");
+        c.place(call);
+        const void *kp = call.ptr(k), *vp = call.ptr(v);
+        const int64_t* sp = static_cast<const int64_t*>(call.ptr(slots));
+        const int32_t tokens = fits(slots.numel(), "num_tokens");
+        uint32_t* err = call.err(a[4]);
+        const pkv_stream_t stream = call.stream(a[5]);
+        return status_of([&] { return f(c.c, k, kp, vp, sp, tokens, err, stream); });
+    });
+}
+
+PyObject* py_reshape_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return write_by_slot(a, n, [](const pkv_cache& c, const at::Tensor&, const void* k, const void* v, const int64_t* slots, int32_t tokens,
+                                  uint32_t* err, pkv_stream_t stream) {
+        return lib.reshape_and_cache(&c, k, v, slots, tokens, err, stream);
+    });
+}
+
+PyObject* py_quantize_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return write_by_slot(a, n, [](const pkv_cache& c, const at::Tensor& kt, const void* k, const void* v, const int64_t* slots,
+                                  int32_t tokens, uint32_t* err, pkv_stream_t stream) {
+        pkv_dtype dt = PKV_F32;   // which the call refuses
+        half_type(kt, &dt);
+        return lib.quantize_kv(&c, k, v, dt, slots, tokens, err, stream);
+    });
+}
+
+// A cache's key bounds, of their type and shape.
 const at::Tensor& bounds_tensor(PyObject* o, const CacheArg& c) {
     const at::Tensor& b = tensor(o, "bounds");
     const at::ScalarType t = b.scalar_type();
@@ -588,6 +629,8 @@ PyMethodDef methods[] = {{"load", py_load, METH_O, nullptr},
                          PKV_METHOD(paged_attention_scored),
                          PKV_METHOD(paged_attention_balanced),
                          PKV_METHOD(gather_kv_cache_dequant),
+                         PKV_METHOD(reshape_and_cache),
+                         PKV_METHOD(quantize_kv),
                          PKV_METHOD(key_bounds),
                          PKV_METHOD(select_pages),
                          PKV_METHOD(paged_attention_selected),

@@ -5,7 +5,7 @@ contiguity of the torch tensors it is given, passes their device pointers and
 the current CUDA stream to the C entry point of the same name, and raises
 ``PkvError`` with the library's message on a non-OK status.  There is no CPU
 path: if the library is not built, every call raises.  The calls that a decode
-step makes (rotary, append, balanced and scored attention, dequantising read-back,
+step makes (rotary, cache writes, append, balanced and scored attention, dequantising read-back,
 key bounds, page selection and the attention over it) go through a CPython module (csrc/binding.cpp), which also checks the tensors'
 sizes and that they live on the current device; the others go through ctypes.
 """
@@ -275,20 +275,18 @@ def _err_ptr(err: Optional[torch.Tensor]):
 
 def pkv_reshape_and_cache(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                           err_flags: Optional[torch.Tensor] = None, stream=None) -> None:
-    if slot_mapping.dtype != torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    c = cache.c_struct()
-    _check(lib().pkv_reshape_and_cache(ctypes.byref(c), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping),
-                                       int(slot_mapping.numel()), _err_ptr(err_flags), _stream(stream)))
+    st = (_binding or _calls()).reshape_and_cache(cache, k_new, v_new, slot_mapping, err_flags, stream)
+    if st:
+        _check(st)
 
 
 def pkv_quantize_kv(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                     err_flags: Optional[torch.Tensor] = None, stream=None) -> None:
-    if slot_mapping.dtype != torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    c = cache.c_struct()
-    _check(lib().pkv_quantize_kv(ctypes.byref(c), _ptr(k_new), _ptr(v_new), _DT[k_new.dtype], _ptr(slot_mapping),
-                                 int(slot_mapping.numel()), _err_ptr(err_flags), _stream(stream)))
+    if k_new.dtype not in _DT:
+        raise KeyError(k_new.dtype)
+    st = (_binding or _calls()).quantize_kv(cache, k_new, v_new, slot_mapping, err_flags, stream)
+    if st:
+        _check(st)
 
 
 def pkv_quantize_kv_blocks(cache: Cache, k_new: torch.Tensor, v_new: torch.Tensor, seqs: Seqs,
