@@ -122,7 +122,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // A 2-D view of a paged cache tensor: rows = num_blocks*16 token slots, each
 // row `row_bytes` long; box = one kv head's `box_bytes` of 16 consecutive rows.
 pkv_status tile_map(CUtensorMap* map, void* base, int64_t rows, int64_t row_bytes, int box_bytes,
-                    CUtensorMapSwizzle swz) {
+                    CUtensorMapSwizzle swz, CUtensorMapL2promotion promotion) {
     auto fn = encode_fn();
     if (!fn) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     cuuint64_t dims[2] = {cuuint64_t(row_bytes), cuuint64_t(rows)};
@@ -130,7 +130,7 @@ pkv_status tile_map(CUtensorMap* map, void* base, int64_t rows, int64_t row_byte
     cuuint32_t box[2] = {cuuint32_t(box_bytes), 16u};
     cuuint32_t estr[2] = {1u, 1u};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, promotion,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
     return PKV_OK;
@@ -140,7 +140,8 @@ pkv_status tile_map(CUtensorMap* map, void* base, int64_t rows, int64_t row_byte
 // token slot, chunk index across the row}.  One box {128, 16, D/64} is a kv
 // head's 16 rows, landing chunk-major as D/64 sub-tiles of 16 x 128 bytes (the
 // layout the 128B swizzle and ldmatrix want), in a single copy operation.
-pkv_status chunk_map(CUtensorMap* map, void* base, int64_t rows, int64_t row_bytes, int head_dim) {
+pkv_status chunk_map(CUtensorMap* map, void* base, int64_t rows, int64_t row_bytes, int head_dim,
+                     CUtensorMapL2promotion promotion) {
     auto fn = encode_fn();
     if (!fn) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     cuuint64_t dims[3] = {128u, cuuint64_t(rows), cuuint64_t(row_bytes / 128)};
@@ -148,7 +149,7 @@ pkv_status chunk_map(CUtensorMap* map, void* base, int64_t rows, int64_t row_byt
     cuuint32_t box[3] = {128u, 16u, cuuint32_t(head_dim / 64)};
     cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", int(r));
     return PKV_OK;
@@ -159,28 +160,37 @@ CUtensorMapSwizzle swizzle_for(int row_bytes) {
                             : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
 }
 
+// What L2 fetches for a copy of row_bytes a row.  A kernel that reads every kv head of a block takes 256 bytes whatever its
+// rows: the neighbours' bytes are read next.  Where only some heads read a block (alone), no more than the row.
+CUtensorMapL2promotion promotion_for(int row_bytes, bool alone) {
+    if (!alone || row_bytes >= 256) return CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    return row_bytes >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                            : row_bytes >= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+}
+
 // CUDA-core kernel: one box per tile (16 rows x one kv head), no swizzle.
 // Tensor-core kernel: swizzled rows of at most 128 bytes, so that the ldmatrix /
 // 128-bit reads of a tile are conflict-free (fp16/bf16: 64-dim chunks with the
 // 128B swizzle, one 3-D box; 8-bit codes: the whole D-byte row; V4: the whole D/2-byte row).
-pkv_status cache_maps(const pkv_cache* c, CUtensorMap* km, CUtensorMap* vm, bool tc) {
+pkv_status cache_maps(const pkv_cache* c, CUtensorMap* km, CUtensorMap* vm, bool tc, bool alone) {
     const int64_t rows = int64_t(c->num_blocks) * 16;
     const int D = c->head_dim, H = c->num_kv_heads;
     pkv_status st;
     if (c->kind == PKV_CACHE_K8V4 || pkv::is_byte_cache(c->kind)) {
         const int DV = c->kind == PKV_CACHE_K8V4 ? D / 2 : D;   // bytes of a V row
-        st = tile_map(km, c->k, rows, int64_t(H) * D, D, swizzle_for(D));
+        st = tile_map(km, c->k, rows, int64_t(H) * D, D, swizzle_for(D), promotion_for(D, alone));
         if (st != PKV_OK) return st;
-        return tile_map(vm, c->v, rows, int64_t(H) * DV, DV, swizzle_for(DV));
+        return tile_map(vm, c->v, rows, int64_t(H) * DV, DV, swizzle_for(DV), promotion_for(DV, alone));
     }
+    const CUtensorMapL2promotion promotion = promotion_for(D * 2, alone);
     if (tc) {
-        st = chunk_map(km, c->k, rows, int64_t(H) * D * 2, D);
+        st = chunk_map(km, c->k, rows, int64_t(H) * D * 2, D, promotion);
         if (st != PKV_OK) return st;
-        return chunk_map(vm, c->v, rows, int64_t(H) * D * 2, D);
+        return chunk_map(vm, c->v, rows, int64_t(H) * D * 2, D, promotion);
     }
-    st = tile_map(km, c->k, rows, int64_t(H) * D * 2, D * 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+    st = tile_map(km, c->k, rows, int64_t(H) * D * 2, D * 2, CU_TENSOR_MAP_SWIZZLE_NONE, promotion);
     if (st != PKV_OK) return st;
-    return tile_map(vm, c->v, rows, int64_t(H) * D * 2, D * 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+    return tile_map(vm, c->v, rows, int64_t(H) * D * 2, D * 2, CU_TENSOR_MAP_SWIZZLE_NONE, promotion);
 }
 
 #ifdef PKV_TIMELINE
@@ -236,7 +246,7 @@ pkv_status attn_setup(pkv::AttnParams* p, const void* q, pkv_dtype q_dtype, int3
 pkv_status attn_launch(pkv::AttnParams p, const pkv_cache* cache, int gqa, pkv_stream_t stream) {
     const bool tc = pkv::attention_uses_tensor_cores(cache->kind, p.q_len, gqa, pkv::is_cascade_pass(p) || p.scored != 0);
     CUtensorMap km, vm;
-    pkv_status st = cache_maps(cache, &km, &vm, tc);
+    pkv_status st = cache_maps(cache, &km, &vm, tc, false);
     if (st != PKV_OK) return st;
     return cuda_result(pkv::launch_attention(p, cache->kind, gqa, km, vm, reinterpret_cast<cudaStream_t>(stream)),
                        "attention launch");
@@ -927,12 +937,13 @@ pkv_status pkv_paged_attention_selected(void* out, pkv_dtype out_dtype, const vo
     CUtensorMap km, vm;
     if (pkv::prompt_tiles(p, cache->kind)) {
         const int64_t rows = int64_t(cache->num_blocks) * 16, row_bytes = int64_t(cache->num_kv_heads) * cache->head_dim * 2;
-        if ((st = tile_map(&km, cache->k, rows, row_bytes, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != PKV_OK) return st;
-        if ((st = tile_map(&vm, cache->v, rows, row_bytes, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != PKV_OK) return st;
+        const CUtensorMapL2promotion promotion = promotion_for(cache->head_dim * 2, true);
+        if ((st = tile_map(&km, cache->k, rows, row_bytes, 128, CU_TENSOR_MAP_SWIZZLE_128B, promotion)) != PKV_OK) return st;
+        if ((st = tile_map(&vm, cache->v, rows, row_bytes, 128, CU_TENSOR_MAP_SWIZZLE_128B, promotion)) != PKV_OK) return st;
         return cuda_result(pkv::launch_attention_prompt(p, cache->kind, km, vm, reinterpret_cast<cudaStream_t>(stream)),
                            "selected attention launch (prompt)");
     }
-    if ((st = cache_maps(cache, &km, &vm, true)) != PKV_OK) return st;
+    if ((st = cache_maps(cache, &km, &vm, true, true)) != PKV_OK) return st;
     return cuda_result(pkv::launch_attention_selected(p, cache->kind, km, vm, reinterpret_cast<cudaStream_t>(stream)),
                        "selected attention launch");
 }

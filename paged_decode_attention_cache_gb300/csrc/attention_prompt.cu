@@ -13,6 +13,10 @@
 //
 // Whatever the lists have in common, the union is no larger than what smaller tiles would read
 // together, and a page costs 128 rows here what 16 rows cost mma.sync.
+//
+// Bound: the chain S -> softmax -> P -> O of a step, 2.7 thousand clocks of which the MMAs of an SM's two CTAs
+// take 1.5, after a prologue of 20 (the union).  1001 tokens of 3 sequences, 32 query heads over 8 kv heads of
+// 128 dims, 64 of 1024 pages each: 93.5 us (attention_selected_rows.cu: 174); tensor pipes 34 % busy.
 #include <algorithm>
 
 #include "attention_selected.cuh"
@@ -149,7 +153,6 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
     }
     if (threadIdx.x < kRows / 32) redo[threadIdx.x] = 0;
     grid_dep_wait();
-    grid_dep_launch();
     const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
     const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, p.tile_rows, int(blockIdx.x), lane);
     if (tile.s < 0) return;
@@ -514,6 +517,9 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
             failed = 1;
         }
     }
+    // The next kernel may come now: its CTAs, were they here from the start, would take the places beside some of these
+    // CTAs and leave others alone, and this grid's successor would run as unevenly (as in attention_selected.cu; no difference measured here).
+    grid_dep_launch();
     __syncthreads();
     if (warp == 0) {
         fence_after_sync();
@@ -586,11 +592,15 @@ size_t prompt_smem(const SelectedParams& p) {
 
 }  // namespace
 
-// Half of the rows or more of a sequence's average tile, 16-bit caches, and lists that fit.
+// 16-bit caches, lists that fit, sequences of two of attention_rows_kernel's tiles or more, and more than 456 of those tiles:
+// a CTA here takes the time of several, and with fewer the GPU is not filled.  us there / here, 8 kv heads of 128 dims, 4 query
+// heads each, 64 pages of 1024: 1 seq x 128 tokens (256 tiles) 37.9 / 73.6, 4 x 64 (512) 68.8 / 80.2, 4 x 128 (1024)
+// 105.9 / 79.4, 32 x 4 (256) 46.9 / 55.3, 32 x 8 (512) 71.7 / 60.1, 32 x 16 (1024) 107.2 / 65.8, 32 x 128 649 / 313; of 256
+// pages, 16 x 16 (512) 60.5 / 45.6; 32 pages of 256, 128 x 4 (1024, one tile a sequence) 88.3 / 115.
 bool prompt_tiles(const SelectedParams& p, int cache_kind) {
     if (cache_kind != PKV_CACHE_F16 && cache_kind != PKV_CACHE_BF16) return false;
-    const int64_t hint = p.cu_q ? int64_t(p.num_rows) / p.num_seqs : p.q_len;   // rows of a sequence
-    return hint * 2 >= prompt_tokens(p) && prompt_smem(p) <= kPromptSmem;
+    const int64_t rows = p.num_rows, tokens = shared_tokens(p);
+    return rows >= 2 * tokens * p.num_seqs && rows * p.num_kv_heads > 456 * tokens && prompt_smem(p) <= kPromptSmem;
 }
 
 cudaError_t launch_attention_prompt(SelectedParams p, int cache_kind, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {

@@ -4,7 +4,10 @@
 // As TtMath and TeMath: S^T = K Q^T has a page's tokens on the MMA's M side and the kv head's
 // query heads on its 8 columns, O^T = V^T P^T the dims on M.
 //
-// Bound: HBM, from a few pages a warp on (MEASURED).
+// Bound: HBM where 16-bit pages fill the GPU (32 tokens over 128 pages of 8 bf16 heads of 128 dims:
+// 269 MB in 44.4 us, 6.06 TB/s); 8-bit pages by the latency of their widening and MMAs (64 tokens over 64
+// pages of e4m3: 134 MB in 42 us); one token over 64 pages, 5.5 us, by the chain count -> list ->
+// table -> page and the merge's two barriers.
 #include "attention_selected.cuh"
 
 namespace pkv {
@@ -43,7 +46,6 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
         prefetch_tensormap(&v_map);
     }
     grid_dep_wait();
-    grid_dep_launch();
     const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
     const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, 1, int(blockIdx.x / C), lane);
     if (tile.s < 0) {   // no row: the same in every CTA of the cluster
@@ -211,6 +213,9 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
         st = st + 2 == STAGES ? 0 : st + 2;
     }
 
+    // The next kernel may come now: its CTAs, were they here from the start, would take the places beside some of these
+    // CTAs and leave others alone, and this grid's successor would run as unevenly (32 x 64 pages of 8 e4m3 heads: 32.6 us early, 23.2 late).
+    grid_dep_launch();
     // ---- the warp's partial, and the merges
     const float back = (Math::kByte ? vref : 1.f) * (1.f / Math::kPUnit);
     __syncwarp();
@@ -266,8 +271,6 @@ cudaError_t launch_kind(const SelectedParams& p, int64_t units, int cluster, siz
 
 cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CUtensorMap& km, const CUtensorMap& vm,
                                       cudaStream_t stream) {
-    const int64_t hint = p.cu_q ? (int64_t(p.num_rows) + p.num_seqs - 1) / p.num_seqs : p.q_len;   // rows of a sequence
-    const int G = p.num_heads / p.num_kv_heads;
     int C = 1;
     int64_t units = 0, most = 0;   // tiles, and the pages that one may have
     size_t lists = 0;
@@ -289,8 +292,14 @@ cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CU
         while (!size() && C < kSelCluster) C *= 2;
         return size();
     };
-    int rows = 16 / G < kSelTokens ? 16 / G : kSelTokens;
-    if (rows > hint) rows = int(hint);
+    // Neighbouring tokens together, if all lists have more than 96 pages for each SM, which single tokens' clusters, being more,
+    // read sooner; and where a page's K row has 256 bytes, four tokens or more: two or three read that much from L2 sooner than
+    // they find the union of their lists.  us alone / together, 8 kv heads, 64 pages: 8 seqs x 3 bf16 tokens of 4 heads of 128
+    // dims 14.0 / 15.9, 16 x 4 31.4 / 26.8, 64 x 3 70.7 / 82.7, 64 x 8 152 / 106; e4m3 8 x 3 14.0 / 15.6, 16 x 2 23.5 / 19.8,
+    // 64 x 2 74.9 / 60.6; bf16 of 64 dims 64 x 2 62.1 / 44.3.  16 x 3 e4m3 tokens, 4 kv heads, 101 pages: 28.9 / 18.2.
+    int rows = shared_tokens(p);
+    const bool half = cache_kind == PKV_CACHE_F16 || cache_kind == PKV_CACHE_BF16;
+    if (int64_t(p.num_rows) * p.num_kv_heads * p.max_pages <= 96 * 152 || (rows < 4 && half && p.head_dim == 128)) rows = 1;
     if (!(rows > 1 && tiles(rows)) && !tiles(1)) return cudaErrorInvalidValue;
     if (units * C > 0x7fffffff) return cudaErrorInvalidValue;
     if (p.tile_rows > 1) return launch_attention_rows(p, cache_kind, units, C, lists, km, vm, stream);

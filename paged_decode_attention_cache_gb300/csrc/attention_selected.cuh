@@ -561,6 +561,13 @@ constexpr size_t ring_bytes() {
 }
 
 // CTAs to an SM: by registers, and by the rings (64 KB at head_dim 128).
+// How many query tokens of a sequence a CTA of attention_rows_kernel takes: what fills the MMA's 16 rows.
+inline int shared_tokens(const SelectedParams& p) {
+    const int64_t each = (int64_t(p.num_rows) + p.num_seqs - 1) / p.num_seqs;   // of a sequence, on average
+    const int G = p.num_heads / p.num_kv_heads, rows = 16 / G < kSelTokens ? 16 / G : kSelTokens;
+    return rows < each ? rows : int(each);
+}
+
 constexpr int sel_ctas(int D, bool rows) { return D == 64 && !rows ? 4 : 3; }
 
 }  // namespace

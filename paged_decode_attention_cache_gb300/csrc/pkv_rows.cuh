@@ -6,40 +6,6 @@
 
 namespace pkv {
 
-// A query token: its sequence (-1: none, a row behind the last sequence's), its visible tokens (0: none), and
-// whether the sequence's context is longer than its block table (vis is then cut to the table).
-struct Row {
-    int s, vis;
-    bool over;
-};
-
-// Query token r, by a whole warp: sequence s's tokens are rows cu[s] .. cu[s + 1] - 1 (or, without cu, q_len each),
-// and the last of them sees the sequence's whole context.  All lanes probe the remaining range of cu at once.
-__device__ __forceinline__ Row find_row(const int32_t* cu, const int32_t* context_lens, int num_seqs, int q_len,
-                                        int max_blocks, int r, int lane) {
-    int s, behind;   // behind: the sequence's query tokens from this one on
-    if (!cu) {
-        s = r / q_len;
-        behind = q_len - (r - s * q_len);
-        if (s >= num_seqs) return {-1, 0, false};
-    } else {
-        if (num_seqs < 1 || r >= cu[num_seqs] || r < cu[0]) return {-1, 0, false};
-        int lo = 0, hi = num_seqs;   // cu[lo] <= r; the answer is in [lo, hi)
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-            const uint32_t m = __ballot_sync(0xffffffffu, at < hi && cu[at < hi ? at : lo] <= r) | 1u;
-            lo += (31 - __clz(m)) * step;   // the last probe that begins at or before r
-            hi = min(hi, lo + step);
-        }
-        s = lo;
-        behind = cu[s + 1] - r;
-        if (behind < 1) return {-1, 0, false};   // lengths that do not rise
-    }
-    const int64_t ctx = context_lens[s];
-    const int64_t cap = int64_t(max_blocks) * kBlockSize;
-    return {s, int(min(max(ctx - behind + 1, int64_t(0)), cap)), ctx > cap};
-}
-
 // A tile of up to R query tokens of one sequence: its sequence (-1: none), its first row and how many.
 struct RowTile {
     int s, r0, rows;
@@ -67,7 +33,8 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* cu, int num_seqs, in
     return {lo, int(r0), min(R, c1 - int(r0))};
 }
 
-// What row r of sequence s sees, c1 being the row behind the sequence's last one.
+// The tokens that a query token sees, `behind` being how many of the sequence's there are from it on (itself one): the last
+// one sees the whole context, as far as the block table goes.
 __device__ __forceinline__ int visible_tokens(int64_t ctx, int max_blocks, int behind) {
     return int(min(max(ctx - behind + 1, int64_t(0)), int64_t(max_blocks) * kBlockSize));
 }

@@ -962,7 +962,6 @@ cudaError_t launch_select_nt(const SelectParams& p, int64_t units, int cluster, 
 
 template <typename T, int D>
 cudaError_t launch_select_d(SelectParams p, cudaStream_t st) {
-    const int64_t hint = p.cu_q ? (int64_t(p.num_rows) + p.num_seqs - 1) / p.num_seqs : p.q_len;   // rows of a sequence
     int C = 1;
     auto bytes = [&](int nt) {   // the queries' operand and the scores
         p.stride = ((p.max_blocks + C - 1) / C + 15) & ~15;
@@ -972,12 +971,17 @@ cudaError_t launch_select_d(SelectParams p, cudaStream_t st) {
         return p.cu_q ? int64_t(p.num_rows) / p.tile_rows + p.num_seqs
                       : int64_t(p.num_seqs) * ((int64_t(p.q_len) + p.tile_rows - 1) / p.tile_rows);
     };
-    // chunks of prompts: 16 query tokens to a CTA
-    p.tile_rows = 16;
-    if (hint > 4 && bytes(4) <= kSelectSmem)
-        return units() > 0x7fffffff ? cudaErrorInvalidValue : launch_select_nt<T, D, 4, 8, false>(p, units(), 1, bytes(4), st);
-    // single tokens and drafts: 4 to a cluster
-    p.tile_rows = int(p.cu_q || hint > 4 ? 4 : hint);
+    // 16 query tokens to a CTA where 4 to one would be more than three rounds of the GPU (two CTAs to an SM), else 4.  us with
+    // 4 / 16, 64 of up to 1024 pages, 8 kv heads of 128 dims: 1 seq x 32 tokens 22.0 / 48.5, 4 x 32 28.9 / 49.8, 32 x 8
+    // 42.9 / 60.4, 32 x 16 67.5 / 72.9, 4 x 128 71.1 / 59.9, 4 x 512 213 / 178; 4 heads of 64 dims: 4 x 128 30.4 / 37.7,
+    // 4 x 256 51.4 / 44.7.
+    const int64_t all = p.num_rows, each = (all + p.num_seqs - 1) / p.num_seqs;
+    if (each > 4 && all * p.num_kv_heads > 4 * 912) {
+        p.tile_rows = 16;
+        if (bytes(4) <= kSelectSmem)
+            return units() > 0x7fffffff ? cudaErrorInvalidValue : launch_select_nt<T, D, 4, 8, false>(p, units(), 1, bytes(4), st);
+    }
+    p.tile_rows = int(p.cu_q || each > 4 ? 4 : each);
     // As many clusters as run at once (two CTAs of 8 warps to an SM), of 128 pages or more to a CTA, which pay from 512
     // pages on.  8 kv heads of 128 dims, us with C = 1 / 2 / 4 / 8: 1 x 512 pages 13.1 / 13.6 / 12.3 / 12.2, a step of
     // 8 x 256 38.5 / 41.0 / 42.0 / 50.3, 32 x 2048 48.8 / 53.7 / 71.0 / 114, 4 x 8192 (int8) 130 / 78 / 50 / 39.
