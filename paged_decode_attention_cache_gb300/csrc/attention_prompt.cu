@@ -592,15 +592,15 @@ size_t prompt_smem(const SelectedParams& p) {
 
 }  // namespace
 
-// 16-bit caches, lists that fit, sequences of two of attention_rows_kernel's tiles or more, and more than 456 of those tiles:
-// a CTA here takes the time of several, and with fewer the GPU is not filled.  us there / here, 8 kv heads of 128 dims, 4 query
-// heads each, 64 pages of 1024: 1 seq x 128 tokens (256 tiles) 37.9 / 73.6, 4 x 64 (512) 68.8 / 80.2, 4 x 128 (1024)
-// 105.9 / 79.4, 32 x 4 (256) 46.9 / 55.3, 32 x 8 (512) 71.7 / 60.1, 32 x 16 (1024) 107.2 / 65.8, 32 x 128 649 / 313; of 256
-// pages, 16 x 16 (512) 60.5 / 45.6; 32 pages of 256, 128 x 4 (1024, one tile a sequence) 88.3 / 115.
+// 16-bit caches, lists that fit, sequences of two of attention_rows_kernel's tiles or more, and more than 608 of those tiles,
+// two rounds of the GPU: a CTA here takes the time of several, and with fewer the GPU is not filled.  us there / here, 8 kv
+// heads of 128 dims, 4 query heads each, 64 pages of 1024: 1 seq x 128 tokens (256 tiles) 30.9 / 73.6, 4 x 64 (512) 58.7 / 80.2,
+// 32 x 8 (512) 59.2 / 59.9, 4 x 128 (1024) 112 / 78.9, 32 x 16 (1024) 111 / 65.5, 32 x 128 744 / 313; of 256 pages, 16 x 16
+// (512) 51.2 / 45.3, 6 x 64 (768) 73.9 / 52.4; 32 pages of 256, 128 x 4 (1024, one tile a sequence) 83.7 / 114.
 bool prompt_tiles(const SelectedParams& p, int cache_kind) {
     if (cache_kind != PKV_CACHE_F16 && cache_kind != PKV_CACHE_BF16) return false;
     const int64_t rows = p.num_rows, tokens = shared_tokens(p);
-    return rows >= 2 * tokens * p.num_seqs && rows * p.num_kv_heads > 456 * tokens && prompt_smem(p) <= kPromptSmem;
+    return rows >= 2 * tokens * p.num_seqs && rows * p.num_kv_heads > 608 * tokens && prompt_smem(p) <= kPromptSmem;
 }
 
 cudaError_t launch_attention_prompt(SelectedParams p, int cache_kind, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {

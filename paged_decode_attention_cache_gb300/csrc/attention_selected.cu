@@ -15,7 +15,7 @@ namespace pkv {
 namespace {
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(kSelThreads, sel_ctas(D, false))
+__global__ void __launch_bounds__(kSelThreads, sel_ctas(KIND, D, false))
 attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const SelectedParams p) {
     constexpr int COLS = 8;
     using Math = PageMath<KIND, D>;
@@ -256,8 +256,9 @@ cudaError_t launch_one(const SelectedParams& p, int64_t units, int cluster, size
         return int(cudaFuncSetAttribute(attention_selected_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectedSmem));
     }));
     if (e != cudaSuccess) return e;
+    const size_t smem = ring_bytes<PageMath<KIND, D>>() + lists + (cluster > 1 ? exchange_bytes<8, D>() : 0);
     return launch_cluster_kernel(attention_selected_kernel<KIND, D>, dim3(unsigned(units * cluster), p.num_kv_heads), dim3(kSelThreads),
-                                 unsigned(cluster), ring_bytes<PageMath<KIND, D>>() + lists + (cluster > 1 ? exchange_bytes<8, D>() : 0), st, km, vm, p);
+                                 unsigned(cluster), spread(units * cluster * p.num_kv_heads, smem), st, km, vm, p);
 }
 
 template <int KIND>
@@ -286,17 +287,18 @@ cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CU
         most = int64_t(rows) * p.max_pages;
         if (rows > 1 && most > p.max_blocks) most = p.max_blocks;
         // as many clusters as run at once
-        const int64_t room = 152 * (rows > 1 ? 2 : sel_ctas(p.head_dim, false));
+        const int64_t room = 152 * (rows > 1 ? 2 : sel_ctas(cache_kind, p.head_dim, false));
         C = 1;
         while (C < kSelCluster && units * p.num_kv_heads * C * 2 <= room && most >= 2 * C * 2 * kSelWarps) C *= 2;
         while (!size() && C < kSelCluster) C *= 2;
         return size();
     };
     // Neighbouring tokens together, if all lists have more than 96 pages for each SM, which single tokens' clusters, being more,
-    // read sooner; and where a page's K row has 256 bytes, four tokens or more: two or three read that much from L2 sooner than
-    // they find the union of their lists.  us alone / together, 8 kv heads, 64 pages: 8 seqs x 3 bf16 tokens of 4 heads of 128
-    // dims 14.0 / 15.9, 16 x 4 31.4 / 26.8, 64 x 3 70.7 / 82.7, 64 x 8 152 / 106; e4m3 8 x 3 14.0 / 15.6, 16 x 2 23.5 / 19.8,
-    // 64 x 2 74.9 / 60.6; bf16 of 64 dims 64 x 2 62.1 / 44.3.  16 x 3 e4m3 tokens, 4 kv heads, 101 pages: 28.9 / 18.2.
+    // read sooner; and where a page's K row has 256 bytes, four tokens or more: two or three read that much from L2 about as
+    // soon as they find the union of their lists.  us alone / together, 8 kv heads, 64 pages: bf16 of 4 query heads of 128 dims,
+    // 8 seqs x 4 tokens 14.6 / 15.1, 16 x 4 31.7 / 24.4, 64 x 4 84.9 / 69.1, 64 x 8 151 / 106, but 16 x 3 19.2 / 23.4, 32 x 3
+    // 40.3 / 35.0, 64 x 2 60.2 / 60.9; e4m3 8 x 2 12.1 / 14.0, 16 x 3 34.8 / 22.5, 64 x 2 66.8 / 60.7; bf16 of 64 dims 64 x 2
+    // 61.8 / 45.7.  16 x 3 e4m3 tokens, 4 kv heads, 101 pages: 28.9 / 18.2.
     int rows = shared_tokens(p);
     const bool half = cache_kind == PKV_CACHE_F16 || cache_kind == PKV_CACHE_BF16;
     if (int64_t(p.num_rows) * p.num_kv_heads * p.max_pages <= 96 * 152 || (rows < 4 && half && p.head_dim == 128)) rows = 1;

@@ -560,7 +560,6 @@ constexpr size_t ring_bytes() {
     return 1024 + size_t(kSelWarps) * Math::STAGES * (Math::STAGE + Math::SIDE);
 }
 
-// CTAs to an SM: by registers, and by the rings (64 KB at head_dim 128).
 // How many query tokens of a sequence a CTA of attention_rows_kernel takes: what fills the MMA's 16 rows.
 inline int shared_tokens(const SelectedParams& p) {
     const int64_t each = (int64_t(p.num_rows) + p.num_seqs - 1) / p.num_seqs;   // of a sequence, on average
@@ -568,7 +567,22 @@ inline int shared_tokens(const SelectedParams& p) {
     return rows < each ? rows : int(each);
 }
 
-constexpr int sel_ctas(int D, bool rows) { return D == 64 && !rows ? 4 : 3; }
+// CTAs of an SM that the registers are shared out for; the rings, 64 KB at 128 16-bit dims, allow three there.  With three the
+// kernel for several tokens spills 276 bytes (64 x 4 bf16 tokens over 64 pages of 8 heads: 86.9 us, with two 69.0).
+constexpr int sel_ctas(int KIND, int D, bool rows) {
+    const bool half = KIND == PKV_CACHE_F16 || KIND == PKV_CACHE_BF16;
+    return rows && half && D == 128 ? 2 : D == 64 && !rows ? 4 : 3;
+}
+
+// Shared memory with which no SM takes a third CTA (a fourth) of a grid that two (three) to each hold: the GPU hands CTAs out
+// unevenly while the kernel before ends.  32 tokens over 64 pages of 8 e4m3 heads, 256 CTAs: 22.9 us without it, 18.5 with.
+// Fewer CTAs are left alone: the next kernel's start beside them (1 token, 64 CTAs: 5.6 us, 6.0 with one CTA to an SM).
+inline size_t spread(int64_t ctas, size_t smem) {
+    const int64_t each = (ctas + 151) / 152;
+    if (each != 2 && each != 3) return smem;
+    const size_t least = 228 * 1024 / (each + 1);
+    return smem < least ? least : smem;
+}
 
 }  // namespace
 

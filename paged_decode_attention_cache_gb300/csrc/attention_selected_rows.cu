@@ -16,7 +16,7 @@ namespace pkv {
 namespace {
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(kSelThreads, sel_ctas(D, true))
+__global__ void __launch_bounds__(kSelThreads, sel_ctas(KIND, D, true))
 attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const SelectedParams p) {
     constexpr int COLS = 16;   // query rows
     using Math = PageMath<KIND, D>;
@@ -383,8 +383,9 @@ cudaError_t launch_rows(const SelectedParams& p, int64_t units, int cluster, siz
         return int(cudaFuncSetAttribute(attention_rows_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectedSmem));
     }));
     if (e != cudaSuccess) return e;
+    const size_t smem = ring_bytes<PageMath<KIND, D>>() + lists + (cluster > 1 ? exchange_bytes<16, D>() : 0);
     return launch_cluster_kernel(attention_rows_kernel<KIND, D>, dim3(unsigned(units * cluster), p.num_kv_heads), dim3(kSelThreads),
-                                 unsigned(cluster), ring_bytes<PageMath<KIND, D>>() + lists + (cluster > 1 ? exchange_bytes<16, D>() : 0), st, km, vm, p);
+                                 unsigned(cluster), spread(units * cluster * p.num_kv_heads, smem), st, km, vm, p);
 }
 
 template <int KIND>

@@ -36,7 +36,7 @@ def together(width):    # from more on, neighbouring tokens of the attention tog
 
 
 def prompt_pairs(H, hkv):
-    return 456 * min(8, 16 * hkv // H)
+    return 608 * min(8, 16 * hkv // H)
 
 
 def many(w, n, q_len=1):
