@@ -2,7 +2,8 @@
 // cache block's stored tokens, dim by dim and kv head by kv head), and the selection
 // over them for bf16 (select_pages.cuh; the other types: select_half.cu, select_i8.cu, select_e4m3.cu).
 //
-// Bound of the bounds: HBM for prompts, dependent loads (length -> table -> keys) for a step.
+// Bound of the bounds: dependent loads (length -> table -> keys) for a step (64 sequences, 2.4 us with the launch); for
+// prompts the same and then HBM (7 of up to 4000 tokens of e4m3, 18.5 MB in 7.4 us, of which HBM's rate would take 2.7).
 #include "select_pages.cuh"
 
 namespace pkv {

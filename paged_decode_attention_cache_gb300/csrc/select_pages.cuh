@@ -339,6 +339,10 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
 //   Selection, by the warps of all CTAs, a row for each or several warps to a row: a histogram between the
 //   smallest and the largest score, the bin of the border, and again inside it while it holds many; the pages
 //   in it, and those that the error may have moved across its edges, are ranked by each other.
+// Bound: HBM while single tokens' scores are worked out, 6 TB/s (32 x 2048 bf16 pages of 8 heads of 128 dims, 172 MB in 46.5 us:
+// 6 before the first loads, 5 of selection); few or long sequences the clusters' barriers, about 1 us each with what is read
+// across (1 x 512 pages 12.2 us; 4 x 8192 int8 pages, 2 tokens, 37.4 us, 52 MB); chunks of prompts the MMAs and their operands'
+// latency, half of the time, and the bins and lists of 16 rows (1169 tokens over up to 1024 pages, 132 us).
 template <typename T, int D, int NT, int NW, bool CL>
 __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectParams p) {
     using Math = ScoreMath<T, D>;
@@ -350,6 +354,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     uint2* const W = reinterpret_cast<uint2*>(dyn);   // [2 NKS][NT][32 lanes]: columns 2 i, 2 i + 1 are row i's terms
     uint2* const WM = W + 2 * NKS * NT * 32;          // [NKS][MT][32 lanes]: the larger magnitude of both parts
     float* const scores = reinterpret_cast<float*>(WM + NKS * MT * 32);   // [tile_rows][stride]
+    const int words = (p.stride + 31) / 32;
+    uint32_t* const bits = reinterpret_cast<uint32_t*>(scores + p.tile_rows * p.stride);   // [tile_rows][words]: pages that are in
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int C = CL ? int(cl.num_blocks()) : 1, rank = CL ? int(cl.block_rank()) : 0;
@@ -607,7 +613,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float a = Math::E == 1 ? mag[mt][2 * r + e] * fabsf(scale[r]) : mag[mt][2 * r + e];
-                        am[mt][e] = a <= am[mt][e] ? am[mt][e] : a;   // a NaN stays
+                        am[mt][e] = fmaxf(am[mt][e], a);   // not a number: neither is the page's score
                     }
             }
         }
@@ -630,7 +636,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * mt + 2 * t + e;
-                uint32_t c = __float_as_uint(fabsf(am[mt][e]));
+                uint32_t c = __float_as_uint(am[mt][e]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) c = max(c, __shfl_xor_sync(0xffffffffu, c, o));
                 if (g == 0 && row < rows) atomicMax(&sh.amax[row], c);
@@ -756,8 +762,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         __syncthreads();
     }
 
-    // ---- the pages above the border, counted, and those near it, listed
-    if (!none) {
+    // ---- the pages above the border and those always taken, marked, the former counted, and the pages near the border, listed
+    {
         for (int i = first_row + team; i < rows; i += teams) {
             const RowState& s = sh.row[i];
             if (s.slow) continue;
@@ -765,14 +771,18 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             decided(s, l0, l1);
             const float* x = scores + i * p.stride;
             const float above = s.above, below = s.below;
-            for (int k0 = l0; k0 < l1; k0 += 128) {
+            const int end = min(a1, s.n - p0);
+            for (int k0 = a0; k0 < end; k0 += 128) {
                 float v[4];
-                read4(x, k0 + lane, l1, v);
+                read4(x, k0 + lane, end, v);
+                uint32_t who[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int k = k0 + 32 * j + lane;
-                    c += k < l1 && v[j] > above;
-                    if (k < l1 && !(v[j] > above) && v[j] >= below) {
+                    const bool open = k >= l0 && k < l1 && !none, in = open && v[j] > above;
+                    c += in;
+                    who[j] = __ballot_sync(0xffffffffu, in || (k < end && (k < l0 || k >= l1)));
+                    if (open && !in && v[j] >= below) {
                         const int at = atomicAdd(&sh.list_n[i], 1);
                         if (at < LT) {
                             sh.list_page[i][at] = p0 + k;
@@ -780,11 +790,17 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
                         }
                     }
                 }
+                if (lane < 4 && k0 + 32 * lane < end)
+                    bits[i * words + k0 / 32 + lane] = lane < 2 ? (lane ? who[1] : who[0]) : lane == 2 ? who[2] : who[3];
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             if (lane == 0) sh.above[i][member] = c;
         }
+    }
+    if (none) {
+        __syncthreads();
+    } else {
         team_sync(cl, C);
         // ---- their ranks
         for (int i = first_row + warp; i < rows; i += kWarps) {
@@ -892,8 +908,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
                 const uint32_t who2 = __ballot_sync(0xffffffffu, in);
                 if (in) sh.sel[i][taken + __popc(who2 & ((1u << lane) - 1u))] = pages[e];
                 taken += __popc(who2);
-                // this CTA's pages are marked: in +inf, out -inf
-                if (e < m && pages[e] >= p0 && pages[e] < p0 + np) scores[i * p.stride + pages[e] - p0] = in ? INFINITY : -INFINITY;
+                const int k = in ? pages[e] - p0 : -1;
+                if (k >= 0 && k < np) atomicOr(&bits[i * words + k / 32], 1u << (k & 31));
             }
             if (lane == 0) s.taken = taken;
         }
@@ -915,24 +931,37 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         }
         at += min(from, p.keep_first) + max(0, from - (s.n - p.keep_last));
         int32_t* list = out_list(i);
-        const float* x = scores + i * p.stride;
-        const float above = s.above;
-        const int c0 = p.keep_first, c1 = s.n - p.keep_last;
         const int end = min(a1, s.n - p0);
-        for (int k0 = a0; k0 < end; k0 += 128) {
-            float v[4];
-            read4(x, k0 + lane, end, v);
-            uint32_t who[4];
+        // us, 64 x 256 pages of single tokens (32 to a warp), 4 chunks of 256 tokens over 1024 e4m3 pages: a word to a lane
+        // 20.3 / 99.8, a bit to a lane 19.6 / 103.3
+        if (end - a0 > 256) {
+            for (int k0 = a0; k0 < end; k0 += 1024) {   // a word to a lane
+                const int k = k0 + 32 * lane;
+                uint32_t m = k < end ? bits[i * words + k / 32] : 0u;
+                int to = __popc(m);
+                const int mine = to;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + 32 * j + lane, page = p0 + k;
-                who[j] = __ballot_sync(0xffffffffu, k < end && (page < c0 || page >= c1 || (!none && v[j] > above)));
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, to, o);
+                    if (lane >= o) to += y;
+                }
+                const int all = __shfl_sync(0xffffffffu, to, 31);
+                to += at - mine;
+                for (; m; m &= m - 1, ++to)
+                    if (to < p.max_pages) list[to] = p0 + k + __ffs(m) - 1;
+                at += all;
             }
+        } else {
+            for (int k0 = a0; k0 < end; k0 += 128) {   // a bit to a lane
+                uint32_t m[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int to = at + __popc(who[j] & ((1u << lane) - 1u));
-                if ((who[j] >> lane & 1u) && to < p.max_pages) list[to] = p0 + k0 + 32 * j + lane;
-                at += __popc(who[j]);
+                for (int j = 0; j < 4; ++j) m[j] = k0 + 32 * j < end ? bits[i * words + k0 / 32 + j] : 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int to = at + __popc(m[j] & ((1u << lane) - 1u));
+                    if ((m[j] >> lane & 1u) && to < p.max_pages) list[to] = p0 + k0 + 32 * j + lane;
+                    at += __popc(m[j]);
+                }
             }
         }
     }
@@ -965,7 +994,7 @@ cudaError_t launch_select_d(SelectParams p, cudaStream_t st) {
     int C = 1;
     auto bytes = [&](int nt) {   // the queries' operand and the scores
         p.stride = ((p.max_blocks + C - 1) / C + 15) & ~15;
-        return size_t(D / 16 * 32 * 8) * (2 * nt + (nt + 1) / 2) + size_t(p.tile_rows) * p.stride * 4;
+        return size_t(D / 16 * 32 * 8) * (2 * nt + (nt + 1) / 2) + size_t(p.tile_rows) * (p.stride + (p.stride + 31) / 32) * 4;
     };
     auto units = [&] {
         return p.cu_q ? int64_t(p.num_rows) / p.tile_rows + p.num_seqs
