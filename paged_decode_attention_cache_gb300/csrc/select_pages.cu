@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(KeyBoundsPar
 cudaError_t launch_key_bounds(const KeyBoundsParams& p, int cache_kind, cudaStream_t stream) {
     const int chunks = p.num_kv_heads * p.head_dim * (cache_kind == PKV_CACHE_F16 || cache_kind == PKV_CACHE_BF16 ? 2 : 1) / 16;
     int64_t pages = p.max_blocks;
-    if (!p.cu_new && (p.q_len + 14) / kBlockSize + 1 < pages) pages = (p.q_len + 14) / kBlockSize + 1;
+    const int64_t touched = (int64_t(p.q_len) + 14) / kBlockSize + 1;   // by q_len tokens, at most
+    if (!p.cu_new && touched < pages) pages = touched;
     int64_t ctas = (pages * chunks + kBoundsThreads - 1) / kBoundsThreads;
     // lengths that only the device knows: enough CTAs to fill the GPU
     const int64_t most = (2048 + p.num_seqs - 1) / p.num_seqs;

@@ -342,7 +342,7 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
 // Bound: HBM while single tokens' scores are worked out, 6 TB/s (32 x 2048 bf16 pages of 8 heads of 128 dims, 172 MB in 46.5 us:
 // 6 before the first loads, 5 of selection); few or long sequences the clusters' barriers, about 1 us each with what is read
 // across (1 x 512 pages 12.2 us; 4 x 8192 int8 pages, 2 tokens, 37.4 us, 52 MB); chunks of prompts the MMAs and their operands'
-// latency, half of the time, and the bins and lists of 16 rows (1169 tokens over up to 1024 pages, 132 us).
+// latency, half of the time, and the bins and lists of 16 rows (1401 tokens over up to 1024 pages, 132 us).
 template <typename T, int D, int NT, int NW, bool CL>
 __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectParams p) {
     using Math = ScoreMath<T, D>;
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int C = CL ? int(cl.num_blocks()) : 1, rank = CL ? int(cl.block_rank()) : 0;
+    // No grid_dep_launch(): the lists may be the next call's page lists, and sparse_setup_kernel reads those ahead of its wait.
     grid_dep_wait();
-    grid_dep_launch();
     const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
     const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, p.tile_rows, int(blockIdx.x / C), lane);
     if (tile.s < 0) return;   // the same in every CTA of the cluster

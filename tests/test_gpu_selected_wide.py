@@ -304,3 +304,60 @@ def test_single_tokens_of_many_sequences(kind, n):
     check_lists(lists, counts, want, 9)
     got = wide_attention(w, q, [1] * 3, want, n, 9, torch.float32, ragged=False)
     check_out(got, *ref.attention(w, q, 0.15, [1] * 3, want), kind, torch.float32)
+
+
+# ---------------------------------------------------------------- tables much wider than the sequences
+
+
+@pytest.mark.parametrize("cols", [12000, 30000, 140000])
+@pytest.mark.parametrize("H,hkv,d", [(8, 2, 128), (2, 2, 64)])
+def test_wide_tables(cols, H, hkv, d):
+    # what a CTA has room for then has fewer query tokens to a tile, or more CTAs to a cluster
+    w = ref.World("bf16", [400, 35], hkv, d, seed=28, extra_cols=cols)
+    q_lens = [60, 13]
+    q = queries(w, 73, H)
+    b = full_bounds(w)
+    want = ref.select(w, q, b, q_lens, 6, 1, 1)
+    out, mag, big = ref.attention(w, q, 0.15, q_lens, want)
+    for pairs in (1, SELECT_16, prompt_pairs(H, hkv)):
+        n = copies(pairs, 73, hkv)
+        check_lists(*wide_select(w, q, b.cuda(), q_lens, n, 6, 1, 1), want, 6)
+        check_out(wide_attention(w, q, q_lens, want, n, 6, torch.float32), out, mag, big, "bf16", torch.float32)
+
+
+def test_bounds_of_more_new_tokens_than_any_sequence_has():
+    w = ref.World("bf16", [400, 35], 2, 64, seed=29)
+    b = ops.key_bounds(w.on_gpu())
+    ops.pkv_key_bounds(b, w.on_gpu(), w.seqs(2 ** 31 - 1))
+    assert torch.equal(b.cpu(), ref.bounds(w, torch.zeros_like(b.cpu()), [400, 35]))
+
+
+# ---------------------------------------------------------------- a selection for the sparse attention
+
+
+@pytest.mark.parametrize("ctx", [[4000, 700, 33, 2000], [60000]])
+def test_lists_for_the_sparse_attention(ctx):
+    # with one kv head a selection's lists are the sparse attention's: the next call on the stream may read them
+    w = ref.World("bf16", ctx, 1, 64, seed=30)
+    B, pages, n = len(ctx), 16, 12
+    cache, seqs, b = w.on_gpu(), w.seqs(), full_bounds(w).cuda()
+    qs = [queries(w, B, 4, seed=i).cuda() for i in range(n)]
+    lists, counts = torch.empty(B, 1, pages, dtype=torch.int32, device="cuda"), torch.empty(B, 1, dtype=torch.int32, device="cuda")
+    ws = ops.sparse_workspace(B, 1, 64, pages)
+
+    def one(i, wait):
+        out = torch.empty_like(qs[i])
+        ops.pkv_select_pages(lists, counts, qs[i], b, cache, seqs)
+        if wait:
+            torch.cuda.synchronize()
+        return ops.pkv_paged_attention_sparse(out, qs[i], 0.125, cache, seqs, lists.view(B, pages), counts.view(B), ws)
+
+    want = [one(i, True).clone() for i in range(n)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [one(i, False) for i in range(n)]
+    for _ in range(3):
+        got = [one(i, False) for i in range(n)]
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(captured, want))
