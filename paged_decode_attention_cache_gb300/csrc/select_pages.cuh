@@ -198,20 +198,67 @@ __device__ __forceinline__ double exact_score(const SelectParams& p, const doubl
     if (ScoreMath<T, D>::E == 1) x *= double(p.k_scale[head]);
     return x == x ? x : -INFINITY;
 }
+// The same of two pages, in blocks b0 and b1 (out of range: none), whose loads and sums do not wait for one another; the first's
+// in lanes 0-15, the second's in the others.
+template <typename T, int D>
+__device__ __forceinline__ double exact_scores(const SelectParams& p, const double (&w)[2 * D / 32], int kvh, int b0, int b1, int lane) {
+    const bool ok0 = b0 >= 0 && b0 < p.num_blocks, ok1 = b1 >= 0 && b1 < p.num_blocks, second = lane >= 16;
+    const int64_t h0 = int64_t(ok0 ? b0 : 0) * p.num_kv_heads + kvh, h1 = int64_t(ok1 ? b1 : 0) * p.num_kv_heads + kvh;
+    double x = 0.0, y = 0.0;
+#pragma unroll
+    for (int k = 0; k < 2 * D / 32; ++k) {
+        x = fma(w[k], ScoreMath<T, D>::one(p.bounds, h0 * 2 * D + lane + 32 * k), x);
+        y = fma(w[k], ScoreMath<T, D>::one(p.bounds, h1 * 2 * D + lane + 32 * k), y);
+    }
+    const double other = __shfl_xor_sync(0xffffffffu, second ? x : y, 16);
+    x = (second ? y : x) + other;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (ScoreMath<T, D>::E == 1) x *= double(p.k_scale[second ? h1 : h0]);
+    return (second ? ok1 : ok0) && x == x ? x : -INFINITY;
+}
+// fp32's a + b is s + e exactly.
+__device__ __forceinline__ float two_sum(float a, float b, float& e) {
+    const float s = a + b, z = s - a;
+    e = (a - (s - z)) + (b - z);
+    return s;
+}
+// The folded queries in fp64.  A sum of up to 8 numbers of 16 bits nearly always is two fp32 numbers exactly, which takes a tenth
+// of the time that fp64 does; else (a remainder of the remainders, or nothing finite) it is worked out in fp64.
 template <int D>
 __device__ __forceinline__ void exact_weights(const SelectParams& p, int r, int kvh, int lane, double (&w)[2 * D / 32]) {
     const int G = p.num_heads / p.num_kv_heads;
     const int64_t q0 = (int64_t(r) * p.num_heads + int64_t(kvh) * G) * D + lane;
+    float hi[2 * D / 32], lo[2 * D / 32];
+    bool more = false, small = false;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-        double neg = 0.0, pos = 0.0;
-        for (int g = 0; g < G; ++g) {
-            const float q = load_q(p.q, p.q_dtype, q0 + int64_t(g) * D + 32 * k);
-            neg += q < 0.f ? q : 0.f * q;   // not a number stays so
-            pos += q > 0.f ? q : 0.f * q;
+    for (int k = 0; k < 2 * D / 32; ++k) hi[k] = lo[k] = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 2 * D / 32; ++k) {
+            const float q = load_q(p.q, p.q_dtype, q0 + int64_t(g) * D + 32 * (k % (D / 32)));
+            float e, rest;
+            hi[k] = two_sum(hi[k], (k < D / 32 ? q < 0.f : q > 0.f) ? q : 0.f * q, e);   // not a number stays so
+            lo[k] = two_sum(lo[k], e, rest);
+            more |= rest != 0.f;
         }
-        w[k] = neg;
-        w[D / 32 + k] = pos;
+#pragma unroll
+    for (int k = 0; k < 2 * D / 32; ++k) {
+        w[k] = double(hi[k]);
+        small |= lo[k] != 0.f;
+    }
+    if (__any_sync(0xffffffffu, small))
+#pragma unroll
+        for (int k = 0; k < 2 * D / 32; ++k) w[k] += double(lo[k]);
+    if (!__any_sync(0xffffffffu, more)) return;
+#pragma unroll
+    for (int k = 0; k < 2 * D / 32; ++k) {
+        w[k] = 0.0;
+        for (int g = 0; g < G; ++g) {
+            const float q = load_q(p.q, p.q_dtype, q0 + int64_t(g) * D + 32 * (k % (D / 32)));
+            w[k] += (k < D / 32 ? q < 0.f : q > 0.f) ? q : 0.f * q;
+        }
     }
 }
 
@@ -883,12 +930,27 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             double* exact = reinterpret_cast<double*>(&sh.hist[i][0]);   // its bins have been read, by all CTAs
             static_assert(NB * 4 >= LT * 8, "fp64 scores in the row's histogram");
             if (!whole) {
+                int block[EL];   // of this lane's entries, all at once
+#pragma unroll
+                for (int j = 0; j < EL; ++j) {
+                    const int e = lane + 32 * j;
+                    block[j] = e < m ? p.block_tables[int64_t(tile.s) * p.max_blocks + pages[e]] : -1;
+                }
                 double w64[2 * D / 32];
                 exact_weights<D>(p, s.r, kvh, lane, w64);
-                for (int e = 0; e < m; ++e) {
-                    if (xs[e] > up || xs[e] < down) continue;   // the same in every lane
-                    const double d = exact_score<T, D>(p, w64, tile.s, kvh, pages[e], lane);
-                    if (lane == 0) exact[e] = d;
+#pragma unroll
+                for (int j = 0; j < EL; ++j) {
+                    const int e = lane + 32 * j;
+                    uint32_t left = __ballot_sync(0xffffffffu, e < m && !(xs[e] > up) && !(xs[e] < down));
+                    while (left) {   // two at a time
+                        const int e0 = __ffs(left) - 1;
+                        left &= left - 1;
+                        const int e1 = left ? __ffs(left) - 1 : e0;
+                        left &= left - 1;
+                        const double d = exact_scores<T, D>(p, w64, kvh, __shfl_sync(0xffffffffu, block[j], e0),
+                                                            __shfl_sync(0xffffffffu, block[j], e1), lane);
+                        if ((lane & 15) == 0) exact[32 * j + (lane ? e1 : e0)] = d;
+                    }
                 }
                 __syncwarp();
             }
