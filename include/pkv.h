@@ -546,7 +546,8 @@ pkv_status pkv_key_bounds(void *bounds, const pkv_cache *cache, const int32_t *c
  * keep_first and the last keep_last, and of the others those with the largest scores,
  * max_pages in all.  The scores decide as if worked out exactly (fp64); the lower page
  * goes first where two are equal.  A score that is not a number counts as -infinity,
- * and so does that of a block id out of range (flags PKV_DEVERR_OOB_BLOCK).
+ * and so does that of a block id out of range (flags PKV_DEVERR_OOB_BLOCK); queries that
+ * are not finite leave every score of their token and kv head not a number.
  *   page_lists   out int32 [num_rows, num_kv_heads, max_pages]: logical pages in
  *                increasing order, -1 behind the last.
  *   page_counts  out int32 [num_rows, num_kv_heads].

@@ -116,6 +116,47 @@ def test_bounds_that_are_not_finite():
         check_lists(lists, counts, ref.select(w, q, b, [18], pages, 1, 1), pages)
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_queries_of_far_apart_sizes(wide):
+    # pages that only fp64 can rank, under folded queries whose exact sum needs more than two fp32 numbers
+    w = ref.World("bf16", [1600], 1, 64, seed=31)
+    b = full_bounds(w)
+    base = grid((64,), 2.0 ** -3, 4.0, 32)
+    base[3] = 0.0
+    step = torch.randperm(100, generator=torch.Generator().manual_seed(33)).float()
+    for p in range(100):
+        x = base.clone()
+        x[5] = step[p]
+        b[int(w.tables[0, p])] = torch.stack([x, x])[None].bfloat16()
+    q = torch.ones(18, 8, 64)
+    q[:, :, 3] = torch.tensor([2.0 ** 100, 1.0, -2.0 ** 100, 2.0 ** -60, 3.0, -2.0 ** -70, -1.0, 0.0])
+    q[:, :, 5] = 2.0 ** -20
+    q = q.bfloat16()
+    for pages in (3, 30, 64):
+        if wide:
+            lists, counts = wide_select(w, q, b.cuda(), [18], copies(SELECT_16, 18, 1), pages, 1, 0)
+            check_lists(lists, counts, ref.select(w, q, b, [18], pages, 1, 0), pages)
+        else:
+            lists, counts = wide_select(w, q[:1], b.cuda(), [1], 1, pages, 1, 0, ragged=False)
+            check_lists(lists, counts, ref.select(w, q[:1], b, [1], pages, 1, 0), pages)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_queries_that_are_not_finite(kind, value):
+    # their scores are not numbers, so the lower pages go first; the other tokens and kv heads are as ever
+    w = ref.World(kind, [1000], 2, 64, seed=34)
+    b = full_bounds(w)
+    q = queries(w, 18, 8)
+    good = ref.select(w, q, b, [18], 9, 1, 2)
+    q[5, 6, 11] = value   # kv head 1
+    n = -(-(1000 - 17 + 5) // 16)
+    good[5][1] = list(range(7)) + [n - 2, n - 1]
+    for copies_ in (1, copies(SELECT_16, 18, 2)):
+        lists, counts = wide_select(w, q, b.cuda(), [18], copies_, 9, 1, 2)
+        check_lists(lists, counts, good, 9)
+
+
 def test_selection_flags_bad_tables():
     w = ref.World("f16", [600, 600], 1, 64, seed=8)
     q_lens, n = [20, 9], copies(SELECT_16, 29, 1)
