@@ -386,10 +386,11 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
 //   Selection, by the warps of all CTAs, a row for each or several warps to a row: a histogram between the
 //   smallest and the largest score, the bin of the border, and again inside it while it holds many; the pages
 //   in it, and those that the error may have moved across its edges, are ranked by each other.
-// Bound: HBM while single tokens' scores are worked out, 6 TB/s (32 x 2048 bf16 pages of 8 heads of 128 dims, 172 MB in 46.5 us:
-// 6 before the first loads, 5 of selection); few or long sequences the clusters' barriers, about 1 us each with what is read
-// across (1 x 512 pages 12.2 us; 4 x 8192 int8 pages, 2 tokens, 37.4 us, 52 MB); chunks of prompts the MMAs and their operands'
-// latency, half of the time, and the bins and lists of 16 rows (1401 tokens over up to 1024 pages, 132 us).
+// Bound: HBM while single tokens' scores are worked out, 6 TB/s (32 x 2048 bf16 pages of 8 heads of 128 dims, 172 MB in 44.1 us:
+// 6 before the first loads, 3 of selection); few or long sequences the clusters' barriers, about 1 us each with what is read
+// across (1 x 512 pages 11.4 us; 4 x 8192 int8 pages, 2 tokens, 34.4 us, 52 MB), and fp64 where pages next to the border need
+// it, 3 us; chunks of prompts the MMAs and their operands' latency, half of the time, and the bins and lists of 16 rows (1401
+// tokens over up to 1024 pages, 125 us).
 template <typename T, int D, int NT, int NW, bool CL>
 __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectParams p) {
     using Math = ScoreMath<T, D>;
@@ -994,8 +995,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         at += min(from, p.keep_first) + max(0, from - (s.n - p.keep_last));
         int32_t* list = out_list(i);
         const int end = min(a1, s.n - p0);
-        // us, 64 x 256 pages of single tokens (32 to a warp), 4 chunks of 256 tokens over 1024 e4m3 pages: a word to a lane
-        // 20.3 / 99.8, a bit to a lane 19.6 / 103.3
+        // us, 64 x 256 pages of single tokens (64 to a warp), 4 chunks of 256 tokens over 1024 e4m3 pages: a word to a lane
+        // 20.3 / 99.8, a bit to a lane 19.6 / 103.3 (with both, and what came later, 16.5 / 98.2)
         if (end - a0 > 256) {
             for (int k0 = a0; k0 < end; k0 += 1024) {   // a word to a lane
                 const int k = k0 + 32 * lane;
@@ -1063,9 +1064,9 @@ cudaError_t launch_select_d(SelectParams p, cudaStream_t st) {
                       : int64_t(p.num_seqs) * ((int64_t(p.q_len) + p.tile_rows - 1) / p.tile_rows);
     };
     // 16 query tokens to a CTA where 4 to one would be more than three rounds of the GPU (two CTAs to an SM), else 4.  us with
-    // 4 / 16, 64 of up to 1024 pages, 8 kv heads of 128 dims: 1 seq x 32 tokens 22.0 / 48.5, 4 x 32 28.9 / 49.8, 32 x 8
-    // 42.9 / 60.4, 32 x 16 67.5 / 72.9, 4 x 128 71.1 / 59.9, 4 x 512 213 / 178; 4 heads of 64 dims: 4 x 128 30.4 / 37.7,
-    // 4 x 256 51.4 / 44.7.
+    // 4 / 16, 64 of up to 1024 pages, 8 kv heads of 128 dims: 1 seq x 32 tokens 20.2 / 41.6, 4 x 32 26.7 / 41.5, 32 x 8
+    // 39.5 / 57.5, 32 x 16 64.0 / 68.3, 4 x 128 66.4 / 52.3, 4 x 512 206 / 166; 4 heads of 64 dims: 4 x 128 26.6 / 32.4,
+    // 4 x 256 47.8 / 38.3.
     const int64_t all = p.num_rows, each = (all + p.num_seqs - 1) / p.num_seqs;
     if (each > 4 && all * p.num_kv_heads > 4 * 912) {
         p.tile_rows = 16;
@@ -1074,12 +1075,13 @@ cudaError_t launch_select_d(SelectParams p, cudaStream_t st) {
     }
     p.tile_rows = int(p.cu_q || each > 4 ? 4 : each);
     // As many clusters as run at once (two CTAs of 8 warps to an SM), of 128 pages or more to a CTA, which pay from 512
-    // pages on.  8 kv heads of 128 dims, us with C = 1 / 2 / 4 / 8: 1 x 512 pages 13.1 / 13.6 / 12.3 / 12.2, a step of
-    // 8 x 256 38.5 / 41.0 / 42.0 / 50.3, 32 x 2048 48.8 / 53.7 / 71.0 / 114, 4 x 8192 (int8) 130 / 78 / 50 / 39.
+    // pages on.  8 kv heads of 128 dims, us with C = 1 / 2 / 4 / 8: 1 x 512 pages 11.8 / 12.5 / 11.6 / 11.4, a step of
+    // 8 x 256 26.2 / 28.9 / 29.4 / 38.7, 32 x 2048 44.1 / 50.7 / 67.9 / 109, 4 x 8192 (int8) 120 / 64.5 / 41.9 / 34.4.
     const int64_t pairs = units() * p.num_kv_heads;
     if (p.max_blocks >= 512)
         while (C < kMaxCluster && pairs * C * 2 <= 304 && p.max_blocks / (2 * C) >= 128) C *= 2;
-    // CTAs of 4 warps where there are more (a step of 64 x 125 pages, 8 heads: 35.4 us, with 8 warps 40.0)
+    // CTAs of 4 warps where there are more.  us with 4 / 8: 64 x 256 pages, 8 heads 16.5 / 22.0, 128 x 1024 68.8 / 74.2, a step
+    // of 64 x 125 32.3 / 37.5; but 32 x 256 14.8 / 14.3, 32 x 2048 54.9 / 44.2.
     const bool narrow = pairs > 304;
     // what a CTA's shared memory does not hold is spread over more CTAs, then taken in smaller tiles
     while (bytes(1) > kSelectSmem) {
