@@ -523,7 +523,7 @@ template <class Math>
 __device__ __forceinline__ float v_units(float (&vs)[2], float& vref) {
     float grow = 1.f;
     const float mag = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
-    if (mag > vref) {   // the same in every lane
+    if (mag > vref) {   // the same in every lane with the same query
         const uint32_t up = min((__float_as_uint(mag) + 0x007fffffu) & 0xff800000u, 253u << 23);
         grow = vref * __uint_as_float((254u << 23) - up);
         vref = __uint_as_float(up);

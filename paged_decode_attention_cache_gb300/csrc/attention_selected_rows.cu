@@ -164,13 +164,13 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     // or NaN in V.  The first pass takes them so; a warp whose sums are not all finite takes its pages again, with care:
     // those rows then keep their sums.
     float o[NMT][2][4];  // rows g, g + 8 x dims dim(mt, 2t), dim(mt, 2t + 1), and kNext further
-    float m_run[2], l_part[2], vref;
+    float m_run[2], l_part[2], vref[2];
     for (bool care = false;; care = true) {
-        vref = 1.17549435e-38f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             m_run[r] = -INFINITY;
             l_part[r] = 0.f;
+            vref[r] = 1.17549435e-38f;
         }
 #pragma unroll
         for (int mt = 0; mt < NMT; ++mt)
@@ -256,14 +256,18 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
                 ring.give_up();
                 break;
             }
-            float unit[2] = {Math::kPUnit, Math::kPUnit};   // what the weights are multiplied by in the operand
+            // What a row's weights are multiplied by in the operand.  8-bit caches: the V scales that a row's unit grows with are
+            // those of the pages it lists, so that another row's page, however large, takes no bits of its weights.
+            float unit[2][2] = {{Math::kPUnit, Math::kPUnit}, {Math::kPUnit, Math::kPUnit}};   // row, page
             if constexpr (Math::kByte) {
-                unit[0] = Math::v_scale(side[0]);
-                unit[1] = two ? Math::v_scale(side[1]) : 0.f;
-                const float grow = v_units<Math>(unit, vref);
-                f[0] *= grow;
-                f[1] *= grow;
-                rescale |= grow != 1.f;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) unit[r][b] = who[b] & bit[r] ? Math::v_scale(side[b]) : 0.f;
+                    const float grow = v_units<Math>(unit[r], vref[r]);
+                    f[r] *= grow;
+                    rescale |= grow != 1.f;
+                }
             }
             if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -282,7 +286,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        split2<Math>(s[b][h][2 * r] * unit[b], s[b][h][2 * r + 1] * unit[b], hi[2 * h + r], lo[2 * h + r]);
+                        split2<Math>(s[b][h][2 * r] * unit[r][b], s[b][h][2 * r + 1] * unit[r][b], hi[2 * h + r], lo[2 * h + r]);
                 if (!edge[b] && (!care || who[b] == every)) {
                     Math::template tiles<false, 2>(stage[b], side[b], 0u, 0u, lane, [&](int m0, auto& a) {
                         constexpr int N = sizeof(a) / 16;
@@ -344,10 +348,10 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
     // heads: 18.4 us early, 18.2 late).
     grid_dep_launch();
     // ---- the warp's partial, and the merges
-    const float back = (Math::kByte ? vref : 1.f) * (1.f / Math::kPUnit);
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        const float back = (Math::kByte ? vref[r] : 1.f) * (1.f / Math::kPUnit);
         float l = l_part[r];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
