@@ -523,7 +523,7 @@ int32_t pkv_sparse_worthwhile(const int32_t *page_counts, const int32_t *context
  *           of the cache's type; PKV_CACHE_I8 / E4M3: the smallest and largest CODES
  *           (the block's K scale multiplies them; it must not be negative, and
  *           pkv_quantize_kv_blocks writes none that is); PKV_CACHE_K8V4: fp16, code *
- *           scale rounded down and up.
+ *           scale rounded down and up (so past 65504 an infinity).
  * The n_s new tokens of sequence s are its last ones, [context_lens[s] - n_s,
  * context_lens[s]), already in the cache; the bounds of every block that holds one are
  * worked out from all that the block stores (min(16, context_lens[s] - first token)
@@ -542,10 +542,10 @@ pkv_status pkv_key_bounds(void *bounds, const pkv_cache *cache, const int32_t *c
  * query heads of a kv head is
  *   sum over the g heads and the dims d of max(q[d] lo_b[d], q[d] hi_b[d]),
  * which no key of the page exceeds with those queries, summed over them (for a positive
- * scale).  The list of (r, kv head): every page if n <= max_pages; else the first
- * keep_first and the last keep_last, and of the others those with the largest scores,
- * max_pages in all.  The scores decide as if worked out exactly (fp64); the lower page
- * goes first where two are equal.  A score that is not a number counts as -infinity,
+ * scale); a bound may be infinite, and a query of 0 then adds 0.  The list of (r, kv
+ * head): every page if n <= max_pages; else the first keep_first and the last keep_last,
+ * and of the others those with the largest scores, max_pages in all.  The scores decide as
+ * if worked out exactly (fp64); the lower page goes first where two are equal.  A score that is not a number counts as -infinity,
  * and so does that of a block id out of range (flags PKV_DEVERR_OOB_BLOCK); queries that
  * are not finite leave every score of their token and kv head not a number.
  *   page_lists   out int32 [num_rows, num_kv_heads, max_pages]: logical pages in

@@ -183,6 +183,9 @@ __device__ __forceinline__ void team_sync(cg::cluster_group& cl, int C) {
     else __syncthreads();
 }
 
+// A bound's number as a folded query's factor: where that is 0, the maximum took the other bound, and an infinite one adds 0.
+__device__ __forceinline__ double factor(double w, double bound) { return w == 0.0 && isinf(bound) ? 0.0 : bound; }
+
 // A page's score in fp64, by a warp whose lanes hold the folded queries of dims lane, lane + 32, .. of lo, then of hi.
 template <typename T, int D>
 __device__ __forceinline__ double exact_score(const SelectParams& p, const double (&w)[2 * D / 32], int s, int kvh, int page,
@@ -192,14 +195,14 @@ __device__ __forceinline__ double exact_score(const SelectParams& p, const doubl
     const int64_t head = int64_t(pb) * p.num_kv_heads + kvh, at = head * 2 * D;
     double x = 0.0;
 #pragma unroll
-    for (int k = 0; k < 2 * D / 32; ++k) x = fma(w[k], ScoreMath<T, D>::one(p.bounds, at + lane + 32 * k), x);
+    for (int k = 0; k < 2 * D / 32; ++k) x = fma(w[k], factor(w[k], ScoreMath<T, D>::one(p.bounds, at + lane + 32 * k)), x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (ScoreMath<T, D>::E == 1) x *= double(p.k_scale[head]);
     return x == x ? x : -INFINITY;
 }
 // The same of two pages, in blocks b0 and b1 (out of range: none), whose loads and sums do not wait for one another; the first's
-// in lanes 0-15, the second's in the others.
+// in lanes 0-15, the second's in the others.  For rows whose magnitudes are finite, so for finite bounds.
 template <typename T, int D>
 __device__ __forceinline__ double exact_scores(const SelectParams& p, const double (&w)[2 * D / 32], int kvh, int b0, int b1, int lane) {
     const bool ok0 = b0 >= 0 && b0 < p.num_blocks, ok1 = b1 >= 0 && b1 < p.num_blocks, second = lane >= 16;
@@ -324,11 +327,14 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
     // a page is marked: in +inf, out -inf, NaN if it ties with the border and the lower page goes first
     constexpr float kTie = NAN;
     int tie_places = places;
-    if (e2 == 0.f) {   // every score is exactly 0
+    double w64[2 * D / 32];
+    exact_weights<D>(p, row.r, kvh, lane, w64);
+    bool none = false;   // a query that is not finite: every score is not a number
+#pragma unroll
+    for (int k = 0; k < 2 * D / 32; ++k) none |= w64[k] != w64[k];
+    if (e2 == 0.f || __any_sync(0xffffffffu, none)) {   // every score is exactly 0, or none is a number
         for (int i = l0 + threadIdx.x; i < l1; i += kThreads) score[i] = near(score[i]) ? kTie : score[i] > up ? INFINITY : -INFINITY;
     } else {
-        double w64[2 * D / 32];
-        exact_weights<D>(p, row.r, kvh, lane, w64);
         uint64_t top = 0;
         need = places;
         for (int shift = 63; shift >= 0; shift -= BITS) {   // 1 bit, then 7 at a time
@@ -579,14 +585,15 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 #pragma unroll
         for (int c = 0; c < AHEAD; ++c) load(now, c);
     {
-        float lo_[NT], hi_[NT], am[MT][2];   // of rows 4 nt + t, and 8 mt + 2 t, + 1
+        float lo_[NT], hi_[NT];   // of rows 4 nt + t
+        uint32_t am[MT][2];       // the largest magnitudes of rows 8 mt + 2 t, + 1, as bits: one that is not a number is above infinity
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             lo_[nt] = INFINITY;
             hi_[nt] = -INFINITY;
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) am[mt][0] = am[mt][1] = 0.f;
+        for (int mt = 0; mt < MT; ++mt) am[mt][0] = am[mt][1] = 0;
         for (int i0 = warp * 16; i0 < np; i0 += kWarps * 16) {
             const Source then = source(next, i0 + kWarps * 16);
             next = entry(i0 + 2 * kWarps * 16);
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float a = Math::E == 1 ? mag[mt][2 * r + e] * fabsf(scale[r]) : mag[mt][2 * r + e];
-                        am[mt][e] = fmaxf(am[mt][e], a);   // not a number: neither is the page's score
+                        am[mt][e] = max(am[mt][e], __float_as_uint(a));
                     }
             }
         }
@@ -684,7 +691,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * mt + 2 * t + e;
-                uint32_t c = __float_as_uint(am[mt][e]);
+                uint32_t c = am[mt][e];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) c = max(c, __shfl_xor_sync(0xffffffffu, c, o));
                 if (g == 0 && row < rows) atomicMax(&sh.amax[row], c);
@@ -706,7 +713,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         const float inv = float(NB) / (hi - lo);
         // |score - exact| <= 2^-16.7 of the sum of magnitudes: 2^-18 from the chains (17 truncations of 2^-24 an MMA), 2^-18
         // from the two bf16 terms, 2^-21 from the chains' sum, 2^-21 from folding, a rounding of the scale; the magnitudes
-        // are 2^-7 off at most.  And what underflows
+        // are 2^-7 off at most.  And what underflows.  Magnitudes that are not finite (an infinite bound beside a query of the
+        // other sign is a 0 times infinity in the MMAs) leave the row to the slow way
         const float e2 = A > 0.f && A < INFINITY ? 2.f * fmaf(A, 9.6e-6f, 3.0e-36f) : A == 0.f ? 0.f : INFINITY;
         __syncwarp();
         if (lane == 0) {

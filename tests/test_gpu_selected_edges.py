@@ -8,8 +8,8 @@ import torch
 
 from paged_decode_attention_cache_gb300 import ops
 from tests import selected_reference as ref
-from tests.test_gpu_selected import queries, random_lists
-from tests.test_gpu_selected_wide import copies, together, wide_attention
+from tests.test_gpu_selected import check_lists, cu, full_bounds, queries, random_lists
+from tests.test_gpu_selected_wide import SELECT_16, copies, together, wide_attention, wide_select
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,45 @@ def test_a_v_scale_reaches_the_rows_that_list_its_page(kind, d, value):
     assert torch.equal(torch.isfinite(got), fine)
     tol = mag * (2.0 ** -15 + big[..., None] * 2.0 ** -18) + want.abs() * 2.0 ** -24
     assert ((got - want).abs()[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_infinite_bounds_beside_queries_of_the_other_sign(kind, wide):
+    # max(q lo, q hi) is finite where q is negative and hi infinite, or q positive and lo -infinite
+    w = ref.World(kind, [1000], 2, 64, seed=43)
+    b = full_bounds(w)
+    q = queries(w, 18, 8)
+    q[:, :4, 3], q[:, :4, 5] = -q[:, :4, 3].abs() - 0.25, q[:, :4, 5].abs() + 0.25   # kv head 0: every query head alike
+    for page in (7, 20, 33, 50):
+        b[int(w.tables[0, page]), :, 1, 3] = math.inf
+    for page in (9, 20, 41):
+        b[int(w.tables[0, page]), :, 0, 5] = -math.inf
+    assert torch.isfinite(ref.page_scores(q[0], b, w.tables[0, :62].tolist(), None, 2)[0]).all()
+    assert (q != 0).all()
+    for pages in (3, 10, 40, 60):
+        want = ref.select(w, q, b, [18], pages, 1, 1)
+        if wide:
+            check_lists(*wide_select(w, q, b.cuda(), [18], copies(SELECT_16, 18, 2), pages, 1, 1), want, pages)
+        else:
+            check_lists(*wide_select(w, q, b.cuda(), [18], 1, pages, 1, 1), want, pages)
+
+
+@pytest.mark.parametrize("ctx", [600, 12000])
+def test_k8v4_keys_past_fp16(ctx):
+    # codes times scales of up to 127 * 700 are finite keys, and their bounds, rounded outwards to fp16, infinite
+    w = ref.World("k8v4", [ctx], 1, 64, seed=44, q_dtype=torch.bfloat16)
+    for page in (3, 8, 21, 30):
+        w.cache.k_scale[int(w.tables[0, page]), 0, page % 16] = 700.0
+    w.k64 = w.cache.k.double() * w.cache.k_scale.permute(0, 2, 1)[..., None].double()
+    b = torch.zeros(w.cache.num_blocks, 1, 2, 64, dtype=torch.float16)
+    got = b.cuda()
+    ops.pkv_key_bounds(got, w.on_gpu(), w.seqs(), cu([ctx]))
+    b = ref.bounds(w, b, [ctx])
+    assert torch.isinf(b).any() and torch.equal(got.cpu(), b)
+    q = queries(w, 2, 4)
+    q[0, :, :] = q[0, :1, :]   # all heads alike: a bound is taken or not
+    assert (q != 0).all()
+    for pages in (4, 12):
+        lists, counts = wide_select(w, q, got, [2], 1, pages, 1, 1)
+        check_lists(lists, counts, ref.select(w, q, b, [2], pages, 1, 1), pages)
