@@ -110,6 +110,7 @@ struct RowState {
     float slack;            // how far the levels' roundings may have moved a bin's edge
     int r, n, vis;          // the row, its pages, its tokens
     int slow;               // left to the slow way
+    int zero;               // no magnitude that fp32 holds: queries or bounds of zeros, or products that underflow
     int taken;              // near pages that are in (sel)
 };
 
@@ -134,7 +135,7 @@ struct SelectShared {
     float all_score[CL ? R : 1][LT];
     int sel[R][LT];                 // near pages that are in
     int scan[kWarps];
-    int bin, rest, ties, taken, count_a;
+    int bin, rest, ties, taken, count_a, some;
 };
 
 __device__ __forceinline__ int bin_of(float x, float lo, float inv, int bins) {
@@ -267,8 +268,8 @@ __device__ __forceinline__ void exact_weights(const SelectParams& p, int r, int 
 
 // A row's selection in the general way, all CTAs together: T, the want-th largest fp32 score, by a radix selection on
 // its bits; the pages between T - e2 and T + e2 by the same on the bits of their fp64 scores, worked out again for each
-// digit; ties by page.  For rows with hundreds of pages that near (the same text again and again, or nothing but
-// zeros) and for scores that are not finite.
+// digit; ties by page.  For rows with hundreds of pages that near (the same text again and again, nothing but zeros,
+// products that underflow) and for magnitudes that are not finite.
 template <typename T, int D, bool CL, typename Sh>
 __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_group& cl, Sh& sh, const RowState& row, int seq,
                                          int kvh, float* score, int p0, int np, int32_t* list) {
@@ -316,7 +317,7 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
     }
     const float T0 = from_key32(prefix), up = T0 + e2, down = T0 - e2;
     auto near = [&](float x) { return !(x > up) && !(x < down); };
-    if (threadIdx.x == 0) sh.count_a = 0;
+    if (threadIdx.x == 0) sh.count_a = sh.some = 0;
     __syncthreads();
     int a = 0;
     for (int i = l0 + threadIdx.x; i < l1; i += kThreads) a += score[i] > up;
@@ -329,10 +330,24 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
     int tie_places = places;
     double w64[2 * D / 32];
     exact_weights<D>(p, row.r, kvh, lane, w64);
-    bool none = false;   // a query that is not finite: every score is not a number
+    bool none = false, any = false;   // a query that is not finite: every score is not a number
 #pragma unroll
-    for (int k = 0; k < 2 * D / 32; ++k) none |= w64[k] != w64[k];
-    if (e2 == 0.f || __any_sync(0xffffffffu, none)) {   // every score is exactly 0, or none is a number
+    for (int k = 0; k < 2 * D / 32; ++k) {
+        none |= w64[k] != w64[k];
+        any |= w64[k] != 0.0;
+    }
+    // queries of zeros: every score is 0, but where a bound is not finite, and e2 then neither
+    bool same = __any_sync(0xffffffffu, none) || (e2 < INFINITY && !__any_sync(0xffffffffu, any));
+    if (!same && row.zero) {   // bounds of zeros alike, or what only fp64 holds
+        bool some = false;
+        for (int i = l0 + warp; i < l1; i += kWarps)
+            if (near(score[i])) some |= exact_score<T, D>(p, w64, seq, kvh, p0 + i, lane) != 0.0;
+        if (some) sh.some = 1;
+        team_sync(cl, C);
+        for (int k = 0; k < C; ++k) some |= *cl.map_shared_rank(&sh.some, k) != 0;
+        same = !some;   // in every CTA
+    }
+    if (same) {   // every score near the border is the same
         for (int i = l0 + threadIdx.x; i < l1; i += kThreads) score[i] = near(score[i]) ? kTie : score[i] > up ? INFINITY : -INFINITY;
     } else {
         uint64_t top = 0;
@@ -713,9 +728,9 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         const float inv = float(NB) / (hi - lo);
         // |score - exact| <= 2^-16.7 of the sum of magnitudes: 2^-18 from the chains (17 truncations of 2^-24 an MMA), 2^-18
         // from the two bf16 terms, 2^-21 from the chains' sum, 2^-21 from folding, a rounding of the scale; the magnitudes
-        // are 2^-7 off at most.  And what underflows.  Magnitudes that are not finite (an infinite bound beside a query of the
+        // are 2^-7 off at most.  And what underflows, 2^-126 for each of the 2 D products of both terms.  Magnitudes that are not finite (an infinite bound beside a query of the
         // other sign is a 0 times infinity in the MMAs) leave the row to the slow way
-        const float e2 = A > 0.f && A < INFINITY ? 2.f * fmaf(A, 9.6e-6f, 3.0e-36f) : A == 0.f ? 0.f : INFINITY;
+        const float e2 = A < INFINITY ? 2.f * fmaf(A, 9.6e-6f, 6.1e-36f) : INFINITY;
         __syncwarp();
         if (lane == 0) {
             s.lo[0] = lo;
@@ -723,6 +738,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             s.slack = 0.f;
             s.lowest = 1;
             s.e2 = e2;
+            s.zero = A == 0.f;
             s.slow = s.need > 0 && !(e2 < INFINITY);
         }
     }
@@ -902,7 +918,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
             }
             __syncwarp();
             const int places = p.max_pages - p.keep_first - p.keep_last - above;
-            if (m > LT || s.e2 == 0.f) {   // too many, or every score is 0
+            if (m > LT) {   // too many
                 if (lane == 0) s.slow = 1;
                 continue;
             }

@@ -87,3 +87,37 @@ def test_k8v4_keys_past_fp16(ctx):
     for pages in (4, 12):
         lists, counts = wide_select(w, q, got, [2], 1, pages, 1, 1)
         check_lists(lists, counts, ref.select(w, q, b, [2], pages, 1, 1), pages)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("ctx,wide", [(1000, False), (1000, True), (20000, False)])
+def test_scores_that_underflow_fp32(kind, ctx, wide):
+    # products of 2^-155 and less, which fp64 tells apart
+    w = ref.World(kind, [ctx], 1, 64, seed=45, q_dtype=torch.bfloat16)
+    b = full_bounds(w)
+    if kind == "bf16":
+        b = (b.float() * 2.0 ** -75).bfloat16()
+    else:
+        w.cache.k_scale *= 2.0 ** -80
+    rows = 18 if wide else 2
+    q = (queries(w, rows, 8, dtype=torch.float32) * 2.0 ** -85).bfloat16()
+    q[0, 1:] = 0.0   # one query head left
+    n = copies(SELECT_16, rows, 1) if wide else 1
+    for pages in (5, 30, 60):
+        lists, counts = wide_select(w, q, b.cuda(), [rows], n, pages, 1, 1)
+        check_lists(lists, counts, ref.select(w, q, b, [rows], pages, 1, 1), pages)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("ctx", [1000, 20000])
+def test_bounds_of_zeros(kind, ctx):
+    # every score is 0 whatever the queries; a block id out of range goes behind them
+    w = ref.World(kind, [ctx], 2, 64, seed=46)
+    b = torch.zeros_like(full_bounds(w))
+    q = queries(w, 3, 8)
+    t = w.tables.clone()
+    t[0, 3], t[0, 5] = -1, 2 ** 30
+    seqs = ops.Seqs(t.cuda(), torch.tensor([ctx], dtype=torch.int32).cuda())
+    for pages in (5, 60):
+        lists, counts = wide_select(w, q, b.cuda(), [3], 1, pages, 1, 1, seqs=seqs)
+        check_lists(lists, counts, ref.select(w, q, b, [3], pages, 1, 1, tables=t), pages)
