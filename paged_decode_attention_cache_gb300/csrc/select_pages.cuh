@@ -9,7 +9,7 @@
 //
 // The selection is that of the exact scores.  They are worked out by 16-bit MMAs with
 // fp32 sums, with a bound e on their error; T, the k-th largest of them, is found; a page
-// above T + 2 e is in, one below T - 2 e is out, and only if more pages lie between than
+// above T + 2 e is in, one below T - 2 e is out (score_error.h), and only if more pages lie between than
 // there are places left are those pages' scores worked out again in fp64 (the products
 // are exact there), which runs at a sixtieth of the fp32 rate on this GPU.
 #pragma once
@@ -21,6 +21,7 @@
 
 #include "attention_byte.cuh"
 #include "pkv_rows.cuh"
+#include "score_error.h"
 
 namespace cg = cooperative_groups;
 
@@ -726,11 +727,9 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         RowState& s = sh.row[i];
         const float lo = from_key32(a), hi = from_key32(b), A = __uint_as_float(c) * (Math::kBf ? 1.f : sh.back[i]);
         const float inv = float(NB) / (hi - lo);
-        // |score - exact| <= 2^-16.7 of the sum of magnitudes: 2^-18 from the chains (17 truncations of 2^-24 an MMA), 2^-18
-        // from the two bf16 terms, 2^-21 from the chains' sum, 2^-21 from folding, a rounding of the scale; the magnitudes
-        // are 2^-7 off at most.  And what underflows, 2^-126 for each of the 2 D products of both terms.  Magnitudes that are not finite (an infinite bound beside a query of the
-        // other sign is a 0 times infinity in the MMAs) leave the row to the slow way
-        const float e2 = A < INFINITY ? 2.f * fmaf(A, 9.6e-6f, 6.1e-36f) : INFINITY;
+        // twice the bound on a score's error.  Magnitudes that are not finite (an infinite bound beside a query of the other sign
+        // is a 0 times infinity in the MMAs) leave the row to the slow way
+        const float e2 = A < INFINITY ? 2.f * fmaf(A, ScoreError<Math::kBf>::kRelative, ScoreError<Math::kBf>::kUnderflow) : INFINITY;
         __syncwarp();
         if (lane == 0) {
             s.lo[0] = lo;

@@ -121,3 +121,35 @@ def test_bounds_of_zeros(kind, ctx):
     for pages in (5, 60):
         lists, counts = wide_select(w, q, b.cuda(), [3], 1, pages, 1, 1, seqs=seqs)
         check_lists(lists, counts, ref.select(w, q, b, [3], pages, 1, 1, tables=t), pages)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("ctx,wide", [(1600, False), (1600, True), (16000, False)])
+def test_errors_that_line_up(kind, ctx, wide):
+    # folded queries that two 16-bit terms miss by as much as they can, upwards in even dims and downwards in odd ones, and
+    # pages of either: their exact scores differ by 2^-20 and less of themselves
+    w = ref.World(kind, [ctx], 1, 128, seed=47)
+    u = 8 if kind == "bf16" else 11   # bits of a number
+    parts = [1.0, 2.0 ** -u - 2.0 ** (-2 * u), 2.0 ** (-2 * u - 1) * (1 - 2.0 ** (1 - u)), 0.0]
+    q = torch.zeros(18 if wide else 2, 8, 128, dtype=torch.float64)
+    for h, x in enumerate(parts):
+        q[:, h] = x
+    q[:, 3, 1::2] = 2.0 ** (-2 * u)   # past the half: rounded up
+    if kind == "f16":
+        q[:, 2:] *= 0.0               # below fp16's smallest number beside 1
+    q[:, :, 0], q[:, 4, 0] = 0.0, 2.0 ** -12
+    assert torch.equal(q, q.to(w.q_dtype).double())
+    n, g = -(-ctx // 16), torch.Generator().manual_seed(48)
+    b = full_bounds(w)
+    hi = torch.zeros(n, 128)
+    odd = torch.randint(0, 2, (n,), generator=g).bool()
+    hi[~odd, 2::2] = 1.0
+    hi[odd, 1::2] = 1.0
+    hi[odd, 1] = 0.0                  # 63 dims each
+    hi[:, 0] = torch.randint(0, 64, (n,), generator=g).float() / 8
+    b[w.tables[0, :n].long(), 0] = torch.stack([torch.zeros_like(hi), hi], dim=1).to(b.dtype)
+    q = q.to(w.q_dtype)
+    copies_ = copies(SELECT_16, q.shape[0], 1) if wide else 1
+    for pages in (9, 50):
+        lists, counts = wide_select(w, q, b.cuda(), [q.shape[0]], copies_, pages, 1, 1)
+        check_lists(lists, counts, ref.select(w, q, b, [q.shape[0]], pages, 1, 1), pages)
