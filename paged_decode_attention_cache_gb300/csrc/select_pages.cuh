@@ -729,7 +729,10 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
         const float inv = float(NB) / (hi - lo);
         // twice the bound on a score's error.  Magnitudes that are not finite (an infinite bound beside a query of the other sign
         // is a 0 times infinity in the MMAs) leave the row to the slow way
-        const float e2 = A < INFINITY ? 2.f * fmaf(A, ScoreError<Math::kBf>::kRelative, ScoreError<Math::kBf>::kUnderflow) : INFINITY;
+        // 8-bit caches: as do folded queries of 2^109 and more or below 2^-98, whose scores leave fp32 before the scale brings
+        // them back, or lose bits that the scale makes large.
+        const bool far = Math::E == 1 && sh.wmax[i] > 0 && (sh.wmax[i] >= 236u << 23 || sh.wmax[i] < 29u << 23);
+        const float e2 = A < INFINITY && !far ? 2.f * fmaf(A, ScoreError<Math::kBf>::kRelative, ScoreError<Math::kBf>::kUnderflow) : INFINITY;
         __syncwarp();
         if (lane == 0) {
             s.lo[0] = lo;

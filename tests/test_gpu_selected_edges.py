@@ -153,3 +153,27 @@ def test_errors_that_line_up(kind, ctx, wide):
     for pages in (9, 50):
         lists, counts = wide_select(w, q, b.cuda(), [q.shape[0]], copies_, pages, 1, 1)
         check_lists(lists, counts, ref.select(w, q, b, [q.shape[0]], pages, 1, 1), pages)
+
+
+@pytest.mark.parametrize("kind,up", [("i8", True), ("e4m3", True), ("e4m3", False)])   # sums of int8 codes do not get that small
+@pytest.mark.parametrize("wide", [False, True])
+def test_queries_that_the_scales_bring_back(kind, up, wide):
+    # queries times codes leave fp32 in some pages, upwards or downwards; times the scales all are ordinary numbers
+    w = ref.World(kind, [1600], 1, 64, seed=49, q_dtype=torch.bfloat16)
+    g = torch.Generator().manual_seed(50)
+    large = torch.rand(w.cache.num_blocks, generator=g) < 0.5   # pages of large codes
+    code = torch.where(large[:, None, None, None], torch.randint(90, 128, (w.cache.num_blocks, 1, 2, 64), generator=g),
+                       torch.randint(0, 5, (w.cache.num_blocks, 1, 2, 64), generator=g))
+    if kind == "i8":
+        code[:, :, 0] *= -1
+        b, back, more = code.to(torch.int8), -124, 5
+    else:   # the codes 0 .. 4 stand for 2^-9 each, 80 .. 117 for 8 to 208
+        code = torch.where(large[:, None, None, None], code - 10, code)
+        code[:, :, 0] += 128
+        b, back, more = code.to(torch.uint8).view(torch.float8_e4m3fn), -124 if up else 105, 14
+    w.cache.k_scale[:, 0] = torch.where(large, 2.0 ** back, 2.0 ** (back + more))
+    rows = 18 if wide else 2
+    q = (queries(w, rows, 8, dtype=torch.float32) * 2.0 ** (115 if up else -131)).bfloat16()
+    for pages in (5, 30, 70):
+        lists, counts = wide_select(w, q, b.cuda(), [rows], copies(SELECT_16, rows, 1) if wide else 1, pages, 1, 1)
+        check_lists(lists, counts, ref.select(w, q, b, [rows], pages, 1, 1), pages)
