@@ -551,12 +551,13 @@ attention_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_
                 for (int d = 0; d < E; ++d) s = fmaf(q[d], Half16<T>::to_float(static_cast<const uint16_t*>(p.k)[at + d]), s);
 #pragma unroll
                 for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                const float now = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - now), w = exp2f(s - now);
+                // the maximum so far; 0 while there is no score above -infinity, whose weight is 0.  A sum that is infinite or not
+                // a number stays so, however small its factor
+                const float now = fmaxf(m, s), to = now == -INFINITY ? 0.f : now, f = m == -INFINITY ? 1.f : exp2f(m - to), w = exp2f(s - to);
                 m = now;
                 l = l * f + w;
 #pragma unroll
-                for (int d = 0; d < E; ++d)
-                    o[d] = (l == w ? 0.f : o[d] * f) + w * Half16<T>::to_float(static_cast<const uint16_t*>(p.v)[at + d]);
+                for (int d = 0; d < E; ++d) o[d] = o[d] * f + w * Half16<T>::to_float(static_cast<const uint16_t*>(p.v)[at + d]);
             }
         }
         for (int d = 0; d < E; ++d)

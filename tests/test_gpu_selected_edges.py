@@ -9,7 +9,7 @@ import torch
 from paged_decode_attention_cache_gb300 import ops
 from tests import selected_reference as ref
 from tests.test_gpu_selected import check_lists, cu, full_bounds, queries, random_lists
-from tests.test_gpu_selected_wide import SELECT_16, copies, together, wide_attention, wide_select
+from tests.test_gpu_selected_wide import SELECT_16, copies, prompt_pairs, together, wide_attention, wide_select
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,53 @@ def test_queries_that_the_scales_bring_back(kind, up, wide):
     for pages in (5, 30, 70):
         lists, counts = wide_select(w, q, b.cuda(), [rows], copies(SELECT_16, rows, 1) if wide else 1, pages, 1, 1)
         check_lists(lists, counts, ref.select(w, q, b, [rows], pages, 1, 1), pages)
+
+
+def chunk_of_a_prompt(kind, seed):
+    """65 query tokens of one sequence, every one of which lists page 0 and some others; dim 0 of the queries is 4, of the keys 0."""
+    w = ref.World(kind, [400], 2, 64, seed=seed)
+    q = queries(w, 65, 8)
+    q[:, :, 0] = 4.0
+    w.cache.k[..., 0] = 0.0
+    w.k64 = w.cache.k.double()
+    lists = [[sorted(set(h) | {0}) for h in heads] for heads in random_lists(w.ctx, [65], 2, 7, seed)]
+    return w, q, lists
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_chunks_of_prompts_keep_an_infinity_of_little_weight(kind, value):
+    # the first token of each list weighs 2^-34 of the others
+    w, q, lists = chunk_of_a_prompt(kind, 51)
+    first = int(w.tables[0, 0])
+    w.cache.k[first, 0, :, 0] = -40.0
+    w.cache.v[first, 0, 0, 7] = value
+    w.k64, w.v64 = w.cache.k.double(), w.cache.v.double()
+    want, mag, big = ref.attention(w, q, 0.15, [65], lists)
+    got = wide_attention(w, q, [65], lists, copies(prompt_pairs(8, 2), 65, 2), 8, torch.float32).double().cpu()
+    fine = torch.isfinite(want)
+    assert torch.equal(~fine, torch.zeros_like(fine).index_fill_(2, torch.tensor([7]), True) & (torch.arange(8) < 4)[None, :, None])
+    assert torch.equal(torch.isfinite(got), fine)
+    tol = mag * (2.0 ** -15 + big[..., None] * 2.0 ** -18) + want.abs() * 2.0 ** -24
+    assert ((got - want).abs()[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_chunks_of_prompts_whose_first_scores_are_minus_infinity(kind, value):
+    # three tokens that weigh nothing, and an infinity or NaN in the V of a page that another token lists
+    w, q, lists = chunk_of_a_prompt(kind, 52)
+    lists = [[sorted((set(h) - {9}) | ({9} if r == 30 else set())) for h in heads] for r, heads in enumerate(lists)]
+    _, _, big = ref.attention(w, q, 0.15, [65], lists)
+    first = int(w.tables[0, 0])
+    w.k64[first, :3, :, 0] = -1e6   # as good as
+    w.v64[int(w.tables[0, 9])] = value
+    want, mag, _ = ref.attention(w, q, 0.15, [65], lists)
+    w.cache.k[first, :3, :, 0] = -math.inf
+    w.cache.v[int(w.tables[0, 9])] = value
+    got = wide_attention(w, q, [65], lists, copies(prompt_pairs(8, 2), 65, 2), 9, torch.float32).double().cpu()
+    fine = torch.isfinite(want)
+    assert torch.equal(~fine, (torch.arange(65) == 30)[:, None, None].expand_as(fine))
+    assert torch.equal(torch.isfinite(got), fine)
+    tol = mag * (2.0 ** -15 + big[..., None] * 2.0 ** -18) + want.abs() * 2.0 ** -24
+    assert ((got - want).abs()[fine] <= tol[fine]).all()
