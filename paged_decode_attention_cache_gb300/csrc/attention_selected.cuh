@@ -318,10 +318,11 @@ constexpr size_t exchange_bytes() {
 }
 
 // A column's weight for one of n partials, by n neighbouring threads (n a power of two): the weighted sum L, the maximum M.
+// 0 for a partial without a page alone: an infinity or NaN in another's sums stays, however small its weight.
 __device__ __forceinline__ float weigh(int n, float m, float l, float& L, float& M) {
     M = l == 0.f ? -INFINITY : m;   // no page (a page has a token whose weight is 1)
     for (int o = 1; o < n; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float w = l == 0.f ? 0.f : exp2f(m - M);
+    const float w = l == 0.f ? 0.f : fmaxf(exp2f(m - M), 1.4e-45f);
     L = l == 0.f ? 0.f : w * l;
     for (int o = 1; o < n; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     return w;

@@ -227,3 +227,37 @@ def test_chunks_of_prompts_whose_first_scores_are_minus_infinity(kind, value):
     assert torch.equal(torch.isfinite(got), fine)
     tol = mag * (2.0 ** -15 + big[..., None] * 2.0 ** -18) + want.abs() * 2.0 ** -24
     assert ((got - want).abs()[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "k8v4"])
+@pytest.mark.parametrize("q_lens,width", [([1, 1], 9), ([1, 1], 64), ([4, 4], 9)])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_partial_sums_keep_an_infinity_of_little_weight(kind, q_lens, width, value):
+    # page 1's tokens weigh some 2^-200 of the others and less: nothing, in the fp32 weights of one warp's or CTA's sums beside another's
+    w = ref.World(kind, [1100, 200], 2, 64, seed=53, q_dtype=torch.float16)
+    q = queries(w, sum(q_lens), 8)
+    q[:, :, 0] = 8.0
+    if kind == "k8v4":
+        w.cache.k[..., 0], w.cache.k_scale[...] = 0, 1 / 32   # codes of -127: scores 8 * -4 * 5.5
+    else:
+        w.cache.k[..., 0] = 0.0
+    lists = [[sorted(set(h) | {1, 2, 3}) for h in heads] for heads in random_lists(w.ctx, q_lens, 2, width - 3, 54)]
+    for s in range(2):
+        b = int(w.tables[s, 1])
+        w.cache.k[b, :, :, 0] = -127 if kind == "k8v4" else -4.0
+        if kind == "k8v4":
+            w.cache.v_zero[b, :, 5, 0] = value
+        else:
+            w.cache.v[b, 5, :, :32] = value
+    if kind == "k8v4":
+        w.k64 = w.cache.k.double() / 32
+        for s in range(2):
+            w.v64[int(w.tables[s, 1]), 5, :, :32] = value
+    else:
+        w.k64, w.v64 = w.cache.k.double(), w.cache.v.double()
+    want, _, _ = ref.attention(w, q, 5.5, q_lens, lists)
+    fine = torch.isfinite(want)
+    assert torch.equal(~fine, (torch.arange(64) < 32)[None, None].expand_as(fine))
+    n = copies(together(width), sum(q_lens), 2) if q_lens[0] > 1 else 1
+    got = wide_attention(w, q, q_lens, lists, n, width, torch.float32, ragged=False, scale=5.5).cpu()
+    assert torch.equal(torch.isfinite(got), fine)
