@@ -476,14 +476,16 @@ PyObject* py_gather_kv_cache_dequant(PyObject*, PyObject* const* a, Py_ssize_t n
     });
 }
 
-// The cache writes by slot: (cache, k_new, v_new, slot_mapping, err_flags, stream)
-template <class F>
-PyObject* write_by_slot(PyObject* const* a, Py_ssize_t n, F f) {
+// The cache writes by slot: (cache, k_new, v_new, slot_mapping, err_flags, stream).  type(cache, k_new, v_new) refuses tensors that
+// the call would read as what they are not.
+template <class Type, class F>
+PyObject* write_by_slot(PyObject* const* a, Py_ssize_t n, Type type, F f) {
     return guarded(n, 6, [&] {
         const Call call;
         const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"), &slots = tensor(a[3], "slot_mapping");
         if (slots.scalar_type() != at::kLong) raise(PyExc_ValueError, "slot_mapping must be int64");
         CacheArg c(a[0]);
+        type(c, k, v);
         const int64_t needed = slots.numel() * c.c.num_kv_heads * c.c.head_dim;
         if (k.numel() < needed || v.numel() < needed)
             raise(PyExc_ValueError, "k_new / v_new must be [num_tokens, num_kv_heads, head_dim]");
@@ -498,15 +500,27 @@ PyObject* write_by_slot(PyObject* const* a, Py_ssize_t n, F f) {
 }
 
 PyObject* py_reshape_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return write_by_slot(a, n, [](const pkv_cache& c, const at::Tensor&, const void* k, const void* v, const int64_t* slots, int32_t tokens,
-                                  uint32_t* err, pkv_stream_t stream) {
+    // the cache's type, or the type that the cache's own tensors give its 16 bits; the library refuses the other kinds
+    auto type = [](const CacheArg& c, const at::Tensor& k, const at::Tensor& v) {
+        if (c.c.kind != PKV_CACHE_F16 && c.c.kind != PKV_CACHE_BF16) return;
+        const at::ScalarType own = c.c.kind == PKV_CACHE_BF16 ? at::kBFloat16 : at::kHalf;
+        auto fits_cache = [&](const at::Tensor& t) {
+            return t.scalar_type() == own || (t.scalar_type() == c.k.t->scalar_type() && t.element_size() == 2);
+        };
+        if (!fits_cache(k) || !fits_cache(v)) raise(PyExc_ValueError, "k_new / v_new must be %s, as the cache is", c10::toString(own));
+    };
+    return write_by_slot(a, n, type, [](const pkv_cache& c, const at::Tensor&, const void* k, const void* v, const int64_t* slots,
+                                        int32_t tokens, uint32_t* err, pkv_stream_t stream) {
         return lib.reshape_and_cache(&c, k, v, slots, tokens, err, stream);
     });
 }
 
 PyObject* py_quantize_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return write_by_slot(a, n, [](const pkv_cache& c, const at::Tensor& kt, const void* k, const void* v, const int64_t* slots,
-                                  int32_t tokens, uint32_t* err, pkv_stream_t stream) {
+    auto type = [](const CacheArg&, const at::Tensor& k, const at::Tensor& v) {
+        if (v.scalar_type() != k.scalar_type()) raise(PyExc_ValueError, "k_new / v_new must be of one type");
+    };
+    return write_by_slot(a, n, type, [](const pkv_cache& c, const at::Tensor& kt, const void* k, const void* v, const int64_t* slots,
+                                        int32_t tokens, uint32_t* err, pkv_stream_t stream) {
         pkv_dtype dt = PKV_F32;   // which the call refuses
         half_type(kt, &dt);
         return lib.quantize_kv(&c, k, v, dt, slots, tokens, err, stream);
