@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     cg::cluster_group cl = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int C = CL ? int(cl.num_blocks()) : 1, rank = CL ? int(cl.block_rank()) : 0;
-    // No grid_dep_launch(): the lists may be the next call's page lists, and sparse_setup_kernel reads those ahead of its wait.
+    // No grid_dep_launch(): with it the next kernels' starts, ahead of this one's end, changed no time.
     grid_dep_wait();
     const int kvh = blockIdx.y, G = p.num_heads / p.num_kv_heads;
     const RowTile tile = find_tile(p.cu_q, p.num_seqs, p.num_rows, p.q_len, p.tile_rows, int(blockIdx.x / C), lane);

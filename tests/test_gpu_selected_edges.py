@@ -261,3 +261,27 @@ def test_partial_sums_keep_an_infinity_of_little_weight(kind, q_lens, width, val
     n = copies(together(width), sum(q_lens), 2) if q_lens[0] > 1 else 1
     got = wide_attention(w, q, q_lens, lists, n, width, torch.float32, ragged=False, scale=5.5).cpu()
     assert torch.equal(torch.isfinite(got), fine)
+
+
+def test_long_lists_for_the_sparse_attention():
+    # lists of more than one round of the sparse attention's set-up, which reads the first ones ahead, and counts that change
+    w = ref.World("bf16", [60000, 30000, 9000], 1, 64, seed=55)
+    B, pages, n = 3, 1500, 6
+    cache, b = w.on_gpu(), full_bounds(w).cuda()
+    qs = [queries(w, B, 4, seed=i).cuda() for i in range(n)]
+    seqs = [w.seqs(ctx=[60000, 30000 - 3000 * i, 9000]) for i in range(n)]
+    lists, counts = torch.empty(B, 1, pages, dtype=torch.int32, device="cuda"), torch.empty(B, 1, dtype=torch.int32, device="cuda")
+    ws = ops.sparse_workspace(B, 1, 64, pages)
+
+    def one(i, wait):
+        out = torch.empty_like(qs[i])
+        ops.pkv_select_pages(lists, counts, qs[i], b, cache, seqs[i])
+        if wait:
+            torch.cuda.synchronize()
+        return ops.pkv_paged_attention_sparse(out, qs[i], 0.125, cache, seqs[i], lists.view(B, pages), counts.view(B), ws)
+
+    want = [one(i, True).clone() for i in range(n)]
+    assert int(counts[1]) < pages
+    for _ in range(3):
+        got = [one(i, False) for i in range(n)]
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
