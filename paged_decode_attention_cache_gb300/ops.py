@@ -547,7 +547,7 @@ def pkv_sparse_worthwhile(page_counts: torch.Tensor, context_lens: torch.Tensor,
 def key_bounds(cache: Cache) -> torch.Tensor:
     """Caller-side storage for pkv_key_bounds: [num_blocks, num_kv_heads, 2, head_dim], lo then hi, of the cache's key
     type (k8v4: float16)."""
-    dtype = torch.float16 if cache.kind == "k8v4" else cache.k.dtype
+    dtype = {"f16": torch.float16, "bf16": torch.bfloat16, "k8v4": torch.float16}.get(cache.kind, cache.k.dtype)
     shape = (cache.num_blocks, cache.num_kv_heads, 2, cache.head_dim)
     if dtype == torch.float8_e4m3fn:
         return torch.zeros(shape, dtype=torch.uint8, device=cache.k.device).view(dtype)

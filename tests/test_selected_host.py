@@ -131,3 +131,12 @@ def test_wrong_tensors(ops, name, bad, text):
     if name != "bounds":
         with pytest.raises(ValueError, match=text):
             ops.pkv_paged_attention_selected(t["out"], t["q"], 0.1, t["cache"], t["seqs"], t["lists"], t["counts"])
+
+
+@pytest.mark.parametrize("kind,want", [("f16", torch.float16), ("bf16", torch.bfloat16)])
+def test_bounds_of_a_cache_that_holds_16_bits_under_another_name(ops, kind, want):
+    c = ops.Cache(kind, *(torch.zeros(4, 16, HKV, D, dtype=torch.int16) for _ in "kv"))
+    b = ops.key_bounds(c)
+    assert b.dtype == want
+    with pytest.raises(ValueError, match="CUDA device"):
+        ops.pkv_key_bounds(b, c, ops.Seqs(torch.zeros(B, 1, dtype=torch.int32), torch.ones(B, dtype=torch.int32)))
