@@ -91,8 +91,14 @@ struct ScoreMath {
             }
         }
     }
-    static __device__ __forceinline__ double one(const void* base, int64_t i) {
-        if constexpr (kHalf) return double(Half16<T>::to_float(static_cast<const uint16_t*>(base)[i]));
+    // a bound's number; SKIP: 0 in the place of an infinity that `skip` says has a weight of 0 (the maximum took the other bound)
+    template <bool SKIP = false>
+    static __device__ __forceinline__ double one(const void* base, int64_t i, bool skip = false) {
+        if constexpr (kHalf) {
+            uint16_t u = static_cast<const uint16_t*>(base)[i];
+            if (SKIP && skip && (u & 0x7fffu) == (kBf ? 0x7f80u : 0x7c00u)) u = 0;
+            return double(Half16<T>::to_float(u));
+        }
         else if constexpr (std::is_same<T, I8>::value) return double(static_cast<const int8_t*>(base)[i]);
         else return double(__half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(base)[i], __NV_E4M3))));
     }
@@ -136,7 +142,7 @@ struct SelectShared {
     float all_score[CL ? R : 1][LT];
     int sel[R][LT];                 // near pages that are in
     int scan[kWarps];
-    int bin, rest, ties, taken, count_a, some;
+    int bin, rest, in_bin, ties, taken, count_a, some;
 };
 
 __device__ __forceinline__ int bin_of(float x, float lo, float inv, int bins) {
@@ -185,41 +191,26 @@ __device__ __forceinline__ void team_sync(cg::cluster_group& cl, int C) {
     else __syncthreads();
 }
 
-// A bound's number as a folded query's factor: where that is 0, the maximum took the other bound, and an infinite one adds 0.
-__device__ __forceinline__ double factor(double w, double bound) { return w == 0.0 && isinf(bound) ? 0.0 : bound; }
-
-// A page's score in fp64, by a warp whose lanes hold the folded queries of dims lane, lane + 32, .. of lo, then of hi.
-template <typename T, int D>
-__device__ __forceinline__ double exact_score(const SelectParams& p, const double (&w)[2 * D / 32], int s, int kvh, int page,
-                                              int lane) {
-    const int pb = p.block_tables[int64_t(s) * p.max_blocks + page];
-    if (pb < 0 || pb >= p.num_blocks) return -INFINITY;
-    const int64_t head = int64_t(pb) * p.num_kv_heads + kvh, at = head * 2 * D;
-    double x = 0.0;
-#pragma unroll
-    for (int k = 0; k < 2 * D / 32; ++k) x = fma(w[k], factor(w[k], ScoreMath<T, D>::one(p.bounds, at + lane + 32 * k)), x);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (ScoreMath<T, D>::E == 1) x *= double(p.k_scale[head]);
-    return x == x ? x : -INFINITY;
-}
-// The same of two pages, in blocks b0 and b1 (out of range: none), whose loads and sums do not wait for one another; the first's
-// in lanes 0-15, the second's in the others.  For rows whose magnitudes are finite, so for finite bounds.
-template <typename T, int D>
+// The scores in fp64 of the pages in blocks b0 and b1 (out of range: none), whose loads and sums do not wait for one another, by a
+// warp whose lanes hold the folded queries of dims lane, lane + 32, .. of lo, then of hi: the first's in lanes 0-15, the
+// second's in the others.  INF: bounds may be infinite.
+template <typename T, int D, bool INF>
 __device__ __forceinline__ double exact_scores(const SelectParams& p, const double (&w)[2 * D / 32], int kvh, int b0, int b1, int lane) {
+    using Math = ScoreMath<T, D>;
     const bool ok0 = b0 >= 0 && b0 < p.num_blocks, ok1 = b1 >= 0 && b1 < p.num_blocks, second = lane >= 16;
     const int64_t h0 = int64_t(ok0 ? b0 : 0) * p.num_kv_heads + kvh, h1 = int64_t(ok1 ? b1 : 0) * p.num_kv_heads + kvh;
     double x = 0.0, y = 0.0;
 #pragma unroll
     for (int k = 0; k < 2 * D / 32; ++k) {
-        x = fma(w[k], ScoreMath<T, D>::one(p.bounds, h0 * 2 * D + lane + 32 * k), x);
-        y = fma(w[k], ScoreMath<T, D>::one(p.bounds, h1 * 2 * D + lane + 32 * k), y);
+        const bool none = INF && (__double_as_longlong(w[k]) << 1) == 0;   // a weight of 0
+        x = fma(w[k], Math::template one<INF>(p.bounds, h0 * 2 * D + lane + 32 * k, none), x);
+        y = fma(w[k], Math::template one<INF>(p.bounds, h1 * 2 * D + lane + 32 * k, none), y);
     }
     const double other = __shfl_xor_sync(0xffffffffu, second ? x : y, 16);
     x = (second ? y : x) + other;
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (ScoreMath<T, D>::E == 1) x *= double(p.k_scale[second ? h1 : h0]);
+    if (Math::E == 1) x *= double(p.k_scale[second ? h1 : h0]);
     return (second ? ok1 : ok0) && x == x ? x : -INFINITY;
 }
 // fp32's a + b is s + e exactly.
@@ -268,67 +259,71 @@ __device__ __forceinline__ void exact_weights(const SelectParams& p, int r, int 
 }
 
 // A row's selection in the general way, all CTAs together: T, the want-th largest fp32 score, by a radix selection on
-// its bits; the pages between T - e2 and T + e2 by the same on the bits of their fp64 scores, worked out again for each
-// digit; ties by page.  For rows with hundreds of pages that near (the same text again and again, nothing but zeros,
-// products that underflow) and for magnitudes that are not finite.
+// its bits; the pages between T - e2 and T + e2 by the same on the high words of their fp64 scores, and those whose high word is
+// the border's on the low words, worked out again; ties by page.  For rows with hundreds of pages that near (the same text again
+// and again, nothing but zeros, products that underflow) and for magnitudes that are not finite.  open: a bit for each of this
+// CTA's pages.  zeros: whether all pages' bounds are 0; -1: not looked at yet.
+// Bound: fp64, a row and page at a time.  All pages alike, 8 bf16 kv heads of 128 dims: 1 sequence of 512 92 us, 32 of up to 2048
+// 1.76 ms, 1401 tokens over up to 1024 29 ms; an infinite bound a sequence 50 us, 0.9 and 14.5 ms; queries of zeros 21, 54, 506 us.
 template <typename T, int D, bool CL, typename Sh>
-__device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_group& cl, Sh& sh, const RowState& row, int seq,
-                                         int kvh, float* score, int p0, int np, int32_t* list) {
+__device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_group& cl, Sh& sh, const RowState& row, int seq, int kvh,
+                                         float* score, uint32_t* open, int p0, int np, int& zeros, int32_t* list) {
     const int C = CL ? int(cl.num_blocks()) : 1, rank = CL ? int(cl.block_rank()) : 0, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kThreads = Sh::kThreads, kWarps = Sh::kWarps;
     const int n = row.n, want = p.max_pages - p.keep_first - p.keep_last;
     const float e2 = row.e2;
     const int mine = max(0, min(np, n - p0));   // this CTA's pages of the row
     const int l0 = min(max(p.keep_first - p0, 0), mine), l1 = max(min(n - p.keep_last - p0, mine), l0);
+    uint32_t* const raw = reinterpret_cast<uint32_t*>(score);
     uint32_t* hist = &sh.hist[0][0];   // 128 bins or more; 7 bits a digit
     constexpr int BITS = 7, BINS = 1 << BITS;
-    int bin, rest;
-    auto zero = [&] {
-        team_sync(cl, C);   // the last histogram has been read
-        for (int i = threadIdx.x; i < BINS; i += kThreads) hist[i] = 0;
-        __syncthreads();
-    };
-    auto find = [&](int need) {   // the bin, from the top, that holds the need-th number, and the place in it
-        team_sync(cl, C);
-        const int b = BINS - 1 - int(threadIdx.x);
-        int c = 0;
-        if (b >= 0)
-            for (int k = 0; k < C; ++k) c += int(cl.map_shared_rank(hist, k)[b]);
-        int total;
-        const int before = block_scan(c, sh.scan, total);
-        if (before < need && before + c >= need) {
-            sh.bin = b;
-            sh.rest = need - before;
+    int need = want, in_bin = 0;   // the place among the numbers that equal the one found, and how many do
+    // the need-th largest of the keys of pages that are counted
+    auto radix = [&](auto counted, auto key) {
+        uint32_t prefix = 0;
+        for (int shift = 28; shift >= 0; shift -= BITS) {   // 4 bits, then 7 at a time
+            team_sync(cl, C);   // the last histogram has been read
+            for (int i = threadIdx.x; i < BINS; i += kThreads) hist[i] = 0;
+            __syncthreads();
+            for (int i = l0 + threadIdx.x; i < l1; i += kThreads) {
+                if (!counted(i)) continue;
+                const uint32_t k = key(i);
+                if (shift == 28 || k >> (shift + BITS) == prefix) atomicAdd(&hist[(k >> shift) & (BINS - 1)], 1u);
+            }
+            team_sync(cl, C);
+            // the bin, from the top, that holds the need-th number, and the place in it
+            const int b = BINS - 1 - int(threadIdx.x);
+            int c = 0;
+            if (b >= 0)
+                for (int k = 0; k < C; ++k) c += int(cl.map_shared_rank(hist, k)[b]);
+            int total;
+            const int before = block_scan(c, sh.scan, total);
+            if (before < need && before + c >= need) {
+                sh.bin = b;
+                sh.rest = need - before;
+                sh.in_bin = c;
+            }
+            __syncthreads();
+            prefix = (prefix << BITS) | uint32_t(sh.bin);
+            need = sh.rest;
+            in_bin = sh.in_bin;
         }
-        __syncthreads();
-        bin = sh.bin;
-        rest = sh.rest;
+        return prefix;
     };
-    uint32_t prefix = 0;
-    int need = want;
-    for (int shift = 28; shift >= 0; shift -= BITS) {   // 4 bits, then 7 at a time
-        zero();
-        for (int i = l0 + threadIdx.x; i < l1; i += kThreads) {
-            const uint32_t k = key32(score[i]);
-            if (shift == 28 || k >> (shift + BITS) == prefix) atomicAdd(&hist[(k >> shift) & (BINS - 1)], 1u);
-        }
-        find(need);
-        prefix = (prefix << BITS) | uint32_t(bin);
-        need = rest;
-    }
-    const float T0 = from_key32(prefix), up = T0 + e2, down = T0 - e2;
+    // with a bound that is not finite every page is near, and T is not needed
+    const float T0 = e2 < INFINITY ? from_key32(radix([](int) { return true; }, [&](int i) { return key32(score[i]); })) : 0.f;
+    const float up = T0 + e2, down = T0 - e2;
     auto near = [&](float x) { return !(x > up) && !(x < down); };
-    if (threadIdx.x == 0) sh.count_a = sh.some = 0;
+    if (threadIdx.x == 0) sh.count_a = 0;
     __syncthreads();
     int a = 0;
     for (int i = l0 + threadIdx.x; i < l1; i += kThreads) a += score[i] > up;
     if (a) atomicAdd(&sh.count_a, a);
     team_sync(cl, C);
-    int places = want;   // for the pages between
-    for (int k = 0; k < C; ++k) places -= *cl.map_shared_rank(&sh.count_a, k);
+    need = want;   // places for the pages between
+    for (int k = 0; k < C; ++k) need -= *cl.map_shared_rank(&sh.count_a, k);
     // a page is marked: in +inf, out -inf, NaN if it ties with the border and the lower page goes first
     constexpr float kTie = NAN;
-    int tie_places = places;
     double w64[2 * D / 32];
     exact_weights<D>(p, row.r, kvh, lane, w64);
     bool none = false, any = false;   // a query that is not finite: every score is not a number
@@ -337,45 +332,76 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
         none |= w64[k] != w64[k];
         any |= w64[k] != 0.0;
     }
-    // queries of zeros: every score is 0, but where a bound is not finite, and e2 then neither
-    bool same = __any_sync(0xffffffffu, none) || (e2 < INFINITY && !__any_sync(0xffffffffu, any));
-    if (!same && row.zero) {   // bounds of zeros alike, or what only fp64 holds
+    any = __any_sync(0xffffffffu, any);
+    const int32_t* table = p.block_tables + int64_t(seq) * p.max_blocks + p0;
+    if (any && row.zero && zeros < 0) {
+        constexpr int E = ScoreMath<T, D>::E;
+        if (threadIdx.x == 0) sh.some = 0;
+        __syncthreads();
         bool some = false;
-        for (int i = l0 + warp; i < l1; i += kWarps)
-            if (near(score[i])) some |= exact_score<T, D>(p, w64, seq, kvh, p0 + i, lane) != 0.0;
+        constexpr uint32_t kSigns = E == 2 ? 0x7fff7fffu : std::is_same<T, E4M3>::value ? 0x7f7f7f7fu : 0xffffffffu;   // all but them
+        for (int i0 = 8 * warp; i0 < np; i0 += 8 * kWarps) {   // eight pages' loads in flight
+            int pb[8];
+            uint4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) pb[j] = i0 + j < np ? table[i0 + j] : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = pb[j] >= 0 && pb[j] < p.num_blocks && lane < 2 * D * E / 16
+                           ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.bounds) +
+                                                                  (int64_t(pb[j]) * p.num_kv_heads + kvh) * 2 * D * E) + lane)
+                           : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) some |= ((v[j].x | v[j].y | v[j].z | v[j].w) & kSigns) != 0;
+        }
         if (some) sh.some = 1;
         team_sync(cl, C);
-        for (int k = 0; k < C; ++k) some |= *cl.map_shared_rank(&sh.some, k) != 0;
-        same = !some;   // in every CTA
+        zeros = 1;
+        for (int k = 0; k < C; ++k) zeros &= *cl.map_shared_rank(&sh.some, k) == 0;
     }
-    if (same) {   // every score near the border is the same
+    // queries or bounds of zeros: every score is 0, but where a bound is not finite, and e2 then neither
+    if (__any_sync(0xffffffffu, none) || (e2 < INFINITY && (!any || (row.zero && zeros)))) {   // every score near the border is the same
         for (int i = l0 + threadIdx.x; i < l1; i += kThreads) score[i] = near(score[i]) ? kTie : score[i] > up ? INFINITY : -INFINITY;
     } else {
-        uint64_t top = 0;
-        need = places;
-        for (int shift = 63; shift >= 0; shift -= BITS) {   // 1 bit, then 7 at a time
-            zero();
-            for (int i = l0 + warp; i < l1; i += kWarps) {
-                if (!near(score[i])) continue;
-                const uint64_t k = key64(exact_score<T, D>(p, w64, seq, kvh, p0 + i, lane));
-                if (lane == 0 && (shift == 63 || k >> (shift + BITS) == top)) atomicAdd(&hist[(k >> shift) & (BINS - 1)], 1u);
+        // pages that stay open by f(i), the others marked by g(i); a word's pages to a warp
+        auto close = [&](auto f, auto g) {
+            for (int i0 = (l0 & ~31) + 32 * warp; i0 < l1; i0 += 32 * kWarps) {
+                const int i = i0 + lane;
+                const bool there = i >= l0 && i < l1, stays = there && f(i);
+                if (there && !stays) score[i] = g(i);
+                const uint32_t word = __ballot_sync(0xffffffffu, stays);
+                if (lane == 0) open[i0 / 32] = word;
             }
-            find(need);
-            top = (top << BITS) | uint64_t(bin);
-            need = rest;
-        }
-        for (int i = l0 + warp; i < l1; i += kWarps) {
-            const float x = score[i];
-            float mark = x > up ? INFINITY : -INFINITY;
-            if (near(x)) {
-                const uint64_t k = key64(exact_score<T, D>(p, w64, seq, kvh, p0 + i, lane));
-                mark = k > top ? INFINITY : k < top ? -INFINITY : kTie;
+            __syncthreads();
+        };
+        auto is_open = [&](int i) { return (open[i >> 5] >> (i & 31) & 1u) != 0; };
+        // the words of the open pages' fp64 scores, two pages at a time
+        auto exact = [&](int shift) {
+            for (int i = l0 + 2 * warp; i < l1; i += 2 * kWarps) {
+                const bool first = is_open(i), second = i + 1 < l1 && is_open(i + 1);
+                if (!first && !second) continue;
+                const double d = exact_scores<T, D, true>(p, w64, kvh, first ? table[i] : -1, second ? table[i + 1] : -1, lane);
+                if ((lane & 15) == 0 && (lane ? second : first)) raw[i + (lane >> 4)] = uint32_t(key64(d) >> shift);
             }
-            __syncwarp();
-            if (lane == 0) score[i] = mark;
+            __syncthreads();
+        };
+        auto word = [&](int i) { return raw[i]; };
+        close([&](int i) { return near(score[i]); }, [&](int i) { return score[i] > up ? INFINITY : -INFINITY; });
+        exact(32);
+        const uint32_t high = radix(is_open, word);
+        const bool all = in_bin == need;   // of the pages with the border's high word
+        close([&](int i) { return is_open(i) && raw[i] == high; },
+              [&](int i) { return is_open(i) ? raw[i] > high ? INFINITY : -INFINITY : score[i]; });
+        uint32_t low = 0;
+        if (!all) {
+            exact(0);
+            low = radix(is_open, word);
         }
-        tie_places = need;
+        close([](int) { return false; }, [&](int i) {
+            return !is_open(i) ? score[i] : all || raw[i] > low ? INFINITY : raw[i] < low ? -INFINITY : kTie;
+        });
     }
+    const int tie_places = need;
     __syncthreads();
     // a thread takes neighbouring pages, so that both prefix sums below go by page
     const int per = (mine + kThreads - 1) / kThreads, b0 = min(int(threadIdx.x) * per, mine), b1 = min(b0 + per, mine);
@@ -974,7 +1000,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
                         left &= left - 1;
                         const int e1 = left ? __ffs(left) - 1 : e0;
                         left &= left - 1;
-                        const double d = exact_scores<T, D>(p, w64, kvh, __shfl_sync(0xffffffffu, block[j], e0),
+                        const double d = exact_scores<T, D, false>(p, w64, kvh, __shfl_sync(0xffffffffu, block[j], e0),
                                                             __shfl_sync(0xffffffffu, block[j], e1), lane);
                         if ((lane & 15) == 0) exact[32 * j + (lane ? e1 : e0)] = d;
                     }
@@ -1056,8 +1082,10 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectPa
     }
 
     // ---- rows left to the slow way, all CTAs together
+    int zeros = -1;
     for (int i = first_row; i < rows; ++i)
-        if (sh.row[i].slow) select_slow<T, D, CL>(p, cl, sh, sh.row[i], tile.s, kvh, scores + i * p.stride, p0, np, out_list(i));
+        if (sh.row[i].slow)
+            select_slow<T, D, CL>(p, cl, sh, sh.row[i], tile.s, kvh, scores + i * p.stride, bits + i * words, p0, np, zeros, out_list(i));
     if (C > 1) cl.sync();   // no CTA leaves while another reads its shared memory
 }
 

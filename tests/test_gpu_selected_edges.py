@@ -285,3 +285,25 @@ def test_long_lists_for_the_sparse_attention():
     for _ in range(3):
         got = [one(i, False) for i in range(n)]
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("ctx,wide", [(6400, False), (6400, True), (30000, False)])
+def test_many_pages_that_the_last_bits_of_fp64_tell_apart(kind, ctx, wide):
+    # hundreds of scores that differ by 2^-36 of themselves and less, some of them equal, and a few far from them
+    w = ref.World(kind, [ctx], 1, 64, seed=56, q_dtype=torch.float16 if kind == "f16" else torch.bfloat16)
+    n, g = -(-ctx // 16), torch.Generator().manual_seed(57)
+    x = torch.full((n, 64), 1.0 if kind == "i8" else 1.5)
+    x[:, 5] = torch.randint(0, 120, (n,), generator=g).float()
+    x[7], x[100], x[200] = 3.0, -2.0, 4.0
+    b = full_bounds(w)
+    b[w.tables[0, :n].long(), 0] = torch.stack([x, x], dim=1).to(b.dtype)
+    if kind == "i8":
+        w.cache.k_scale[:] = 0.75
+    q = torch.ones(18 if wide else 2, 2, 64)
+    q[:, 0] = 128.0
+    q[:, :, 5] = 2.0 ** (-24 if kind == "f16" else -28)
+    q = q.to(w.q_dtype)
+    for pages in (3, 30, 64):
+        lists, counts = wide_select(w, q, b.cuda(), [q.shape[0]], copies(SELECT_16, q.shape[0], 1) if wide else 1, pages, 1, 1)
+        check_lists(lists, counts, ref.select(w, q, b, [q.shape[0]], pages, 1, 1), pages)
