@@ -9,14 +9,17 @@
 //               (hi, lo) and so two MMAs a k step; V as the cache has it (N-major); O in TMEM.
 // One thread issues the copies, one the MMAs, four warps do the softmax.  K, V and S have two
 // buffers each: the next step's S is there when a softmax ends, and its O += P V runs under the
-// next one.  256 columns of TMEM and 96 KB of tiles to a CTA, two CTAs to an SM.
+// next one.  256 columns of TMEM to a CTA; at 128 dims 96 KB of tiles, 8 bytes for each page that its
+// lists may hold together, and 4 bytes (groups of 2 and 1: 8 and 16) for each column of the block table.
+// Two CTAs to an SM as far as that goes: with lists of 64 up to 1,260 columns (20 thousand tokens) for
+// groups of 4, 630 for groups of 1; the chunks below take 149 us, not 94, in a table of 1280 columns.
 //
 // Whatever the lists have in common, the union is no larger than what smaller tiles would read
 // together, and a page costs 128 rows here what 16 rows cost mma.sync.
 //
 // Bound: the chain S -> softmax -> P -> O of a step, 2.7 thousand clocks of which the MMAs of an SM's two CTAs
 // take 1.5, after a prologue of 20 (the union).  1001 tokens of 3 sequences, 32 query heads over 8 kv heads of
-// 128 dims, 64 of 1024 pages each: 93.5 us (attention_selected_rows.cu: 174); tensor pipes 34 % busy.
+// 128 dims, 64 of 1024 pages each: 94 us (attention_selected_rows.cu: 174); tensor pipes 34 % busy.
 #include <algorithm>
 
 #include "attention_selected.cuh"

@@ -5,9 +5,9 @@
 // query heads on its 8 columns, O^T = V^T P^T the dims on M.
 //
 // Bound: HBM where 16-bit pages fill the GPU (32 tokens over 128 pages of 8 bf16 heads of 128 dims:
-// 269 MB in 44.4 us, 6.06 TB/s); 8-bit pages by the latency of their widening and MMAs (64 tokens over 64
-// pages of e4m3: 134 MB in 42 us); one token over 64 pages, 5.5 us, by the chain count -> list ->
-// table -> page and the merge's two barriers.
+// 269 MB in 44 us, 6.1 TB/s); 8-bit pages by the latency of their widening and MMAs (64 tokens of 8192 over
+// 64 of their pages, 8 heads: e4m3, 134 MB, 38 us, int8 38, K8/V4 41); one token over 64 pages, 5.6 us, by the
+// chain count -> list -> table -> page and the merge's two barriers.
 #include "attention_selected.cuh"
 
 namespace pkv {
@@ -214,7 +214,8 @@ attention_selected_kernel(const __grid_constant__ CUtensorMap k_map, const __gri
     }
 
     // The next kernel may come now: its CTAs, were they here from the start, would take the places beside some of these
-    // CTAs and leave others alone, and this grid's successor would run as unevenly (32 x 64 pages of 8 e4m3 heads: 32.6 us early, 23.2 late).
+    // CTAs and leave others alone, and this grid's successor would run as unevenly (32 tokens of 8192 over 64 pages of 8 e4m3 heads, without
+    // spread(): 32.9 us early, 22.9 late).
     grid_dep_launch();
     // ---- the warp's partial, and the merges
     const float back = (Math::kByte ? vref : 1.f) * (1.f / Math::kPUnit);

@@ -576,7 +576,8 @@ constexpr int sel_ctas(int KIND, int D, bool rows) {
 }
 
 // Shared memory with which no SM takes a third CTA (a fourth) of a grid that two (three) to each hold: the GPU hands CTAs out
-// unevenly while the kernel before ends.  32 tokens over 64 pages of 8 e4m3 heads, 256 CTAs: 22.9 us without it, 18.5 with.
+// unevenly while the kernel before ends.  256 CTAs, 8 heads, without it / with it: 32 tokens of 8192 over 64 e4m3 pages 22.9 / 18.4 us,
+// of 16384 over 128 41.0 / 31.9 (int8 41.1 / 35.9, bf16 44.3 / 44.0); drafts, 32 x 3 over 64 e4m3 pages 36.2 / 32.4.
 // Fewer CTAs are left alone: the next kernel's start beside them (1 token, 64 CTAs: 5.6 us, 6.0 with one CTA to an SM).
 inline size_t spread(int64_t ctas, size_t smem) {
     const int64_t each = (ctas + 151) / 152;

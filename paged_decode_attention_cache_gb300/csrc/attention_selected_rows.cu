@@ -7,8 +7,8 @@
 // With 16 rows the queries take the MMA's M side, S = Q K^T and O = P V: P's accumulators are then
 // its operand as they lie, and a thread has two rows' statistics where it would have four columns'.
 //
-// Bound: latency, in three parts of about the same length (16 x 3 tokens over 101 pages of 4 e4m3 heads, 27 MB in
-// 18.2 us: the union of the lists 5.6 thousand clocks, the pages 15, the merges 7.7; issue slots 24 % used).
+// Bound: latency, in three parts one after the other (16 x 3 tokens over 101 pages of 4 e4m3 heads, 27 MB in
+// 19.0 us: the union of the lists 5.6 thousand clocks, the pages 15, the merges 7.7; issue slots 25 % used).
 #include "attention_selected.cuh"
 
 namespace pkv {
@@ -345,7 +345,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_co
 
     // The next kernel may come now: its CTAs, were they here from the start, would take the places beside some of these
     // CTAs and leave others alone, and this grid's successor would run as unevenly (as in attention_selected.cu; 16 x 3 tokens over 101 pages of 4 e4m3
-    // heads: 18.4 us early, 18.2 late).
+    // heads: 19.2 us early, 19.1 late).
     grid_dep_launch();
     // ---- the warp's partial, and the merges
     __syncwarp();

@@ -434,11 +434,12 @@ __device__ __noinline__ void select_slow(const SelectParams& p, cg::cluster_grou
 //   Selection, by the warps of all CTAs, a row for each or several warps to a row: a histogram between the
 //   smallest and the largest score, the bin of the border, and again inside it while it holds many; the pages
 //   in it, and those that the error may have moved across its edges, are ranked by each other.
-// Bound: HBM while single tokens' scores are worked out, 6 TB/s (32 x 2048 bf16 pages of 8 heads of 128 dims, 172 MB in 44.1 us:
-// 6 before the first loads, 3 of selection); few or long sequences the clusters' barriers, about 1 us each with what is read
-// across (1 x 512 pages 11.4 us; 4 x 8192 int8 pages, 2 tokens, 34.4 us, 52 MB), and fp64 where pages next to the border need
-// it, 3 us; chunks of prompts the MMAs and their operands' latency, half of the time, and the bins and lists of 16 rows (1401
-// tokens over up to 1024 pages, 125 us).
+// Bound: a wave of CTAs whose loads do not cover HBM's latency: two to an SM, 64 registers of a thread in flight.  32 sequences of
+// 2048 bf16 pages, 8 heads of 128 dims, take 54.3 us for 269 MB, 6 of them before the first loads and 3 of selection: 5.9 TB/s
+// between; of 512 to 2048 pages (172 MB) 44.5 us, the time of the longest ones' CTAs, 4.8 TB/s between, DRAM 43 % busy over
+// the whole.  Few or long sequences: the clusters' barriers, about 1 us each with what is read across (1 x 512 pages 11.6 us; 4 x
+// 8192 int8 pages, 2 tokens, 33.5 us, 52 MB), and fp64 where pages next to the border need it, 3 us.  Chunks of prompts: the
+// MMAs and their operands' latency, half of the time, and the bins and lists of 16 rows (1401 tokens over up to 1024 pages, 126 us).
 template <typename T, int D, int NT, int NW, bool CL>
 __global__ void __launch_bounds__(32 * NW, 16 / NW) select_pages_kernel(SelectParams p) {
     using Math = ScoreMath<T, D>;
@@ -1120,7 +1121,10 @@ cudaError_t launch_select_d(SelectParams p, cudaStream_t st) {
     // 16 query tokens to a CTA where 4 to one would be more than three rounds of the GPU (two CTAs to an SM), else 4.  us with
     // 4 / 16, 64 of up to 1024 pages, 8 kv heads of 128 dims: 1 seq x 32 tokens 20.2 / 41.6, 4 x 32 26.7 / 41.5, 32 x 8
     // 39.5 / 57.5, 32 x 16 64.0 / 68.3, 4 x 128 66.4 / 52.3, 4 x 512 206 / 166; 4 heads of 64 dims: 4 x 128 26.6 / 32.4,
-    // 4 x 256 47.8 / 38.3.
+    // 4 x 256 47.8 / 38.3.  The host knows the rows of all sequences together and the table's width, no lengths: one chunk of 512
+    // with 63 single tokens takes 80 us (apart 38 and 27).  Shared memory goes by the width: at 128 dims two CTAs of 16 to an SM up
+    // to 1072 columns, one up to 2480, then tiles of 4; 1401 tokens over 1024 pages 126 us in a table of 1072 columns, 178 of 1088
+    // and 2048, 220 of 4096, 367 of 8192, 553 of 20480.
     const int64_t all = p.num_rows, each = (all + p.num_seqs - 1) / p.num_seqs;
     if (each > 4 && all * p.num_kv_heads > 4 * 912) {
         p.tile_rows = 16;
