@@ -576,9 +576,11 @@ pkv_status pkv_select_pages(int32_t *page_lists, int32_t *page_counts, int32_t m
  *                skipped and flags PKV_DEVERR_PAGE_LIST; counts are cut to [0, max_pages].
  *   cu_q_lens, num_rows  as for pkv_select_pages.
  * Rows behind cu[num_seqs] keep their outputs; a row without a listed page gets zeros.
- * No workspace.  K and V of tokens that a row does not see reach no output of it,
- * whatever they hold.  max_pages above 131,072 and a sliding window are
- * PKV_ERR_UNSUPPORTED.
+ * No workspace.  K and V of tokens that a row does not see, and pages that it does not
+ * list, reach no output of it, whatever they hold.  8-bit caches: a weight times its
+ * page's V scale is kept to 2^-39 of the largest V scale that the row lists, so pages of
+ * scales 2^-20 of that and less lose bits (as in the other calls over such caches).
+ * max_pages above 131,072 and a sliding window are PKV_ERR_UNSUPPORTED.
  */
 pkv_status pkv_paged_attention_selected(void *out, pkv_dtype out_dtype, const void *q, pkv_dtype q_dtype,
                                         int32_t num_heads, int32_t num_rows, float scale, const pkv_cache *cache,

@@ -299,7 +299,7 @@ cudaError_t launch_attention_selected(SelectedParams p, int cache_kind, const CU
     // soon as they find the union of their lists.  us alone / together, 8 kv heads, 64 pages: bf16 of 4 query heads of 128 dims,
     // 8 seqs x 4 tokens 14.6 / 15.1, 16 x 4 31.7 / 24.4, 64 x 4 84.9 / 69.1, 64 x 8 151 / 106, but 16 x 3 19.2 / 23.4, 32 x 3
     // 40.3 / 35.0, 64 x 2 60.2 / 60.9; e4m3 8 x 2 12.1 / 14.0, 16 x 3 34.8 / 22.5, 64 x 2 66.8 / 60.7; bf16 of 64 dims 64 x 2
-    // 61.8 / 45.7.  16 x 3 e4m3 tokens, 4 kv heads, 101 pages: 28.9 / 18.2.
+    // 61.8 / 45.7.  16 x 3 e4m3 tokens, 4 kv heads, 101 pages: 28.9 / 19.0.
     int rows = shared_tokens(p);
     const bool half = cache_kind == PKV_CACHE_F16 || cache_kind == PKV_CACHE_BF16;
     if (int64_t(p.num_rows) * p.num_kv_heads * p.max_pages <= 96 * 152 || (rows < 4 && half && p.head_dim == 128)) rows = 1;

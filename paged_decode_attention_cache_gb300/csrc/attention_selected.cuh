@@ -518,8 +518,10 @@ __device__ __forceinline__ float column_scale(const SelectedParams& p, const uin
     return p.scale_log2 * __uint_as_float((min(max(q_most[col], 16u), 254u) - 8u) << 23);
 }
 
-// 8-bit caches: the sums hold P V / vref times kPUnit, vref a power of two that grows with the pages' V scales.  Two pages'
-// scales -> what their weights are multiplied by, and what the sums are.
+// 8-bit caches: the sums hold P V / vref times kPUnit, vref a power of two that grows with the V scales of the pages that the
+// query lists.  Two pages' scales -> what their weights are multiplied by, and what the sums are.  The operand's two halves keep a
+// weight to 2^-39 of vref over its page's scale (as byte_attention_kernel's do): what a query gets of a page whose scale is less than
+// 2^-20 of the largest one that it lists loses bits, and of less than 2^-38 is lost.
 template <class Math>
 __device__ __forceinline__ float v_units(float (&vs)[2], float& vref) {
     float grow = 1.f;
